@@ -1,5 +1,7 @@
 /*
- * ag.h -- C ABI of libag, pair-bias multi-query attention for B200 (sm_100a).
+ * ag.h -- C ABI of libag, pair-bias multi-query attention for B200 (sm_100a),
+ * with the linear layers, the query and key norm and rotation and the gradient
+ * clipping that go around it.
  *
  * The operation is the sequence attention of the page "Making Full-Context
  * AlphaGenome Fit on an RTX 3090" (section "Why stock FlashAttention was not
@@ -48,9 +50,17 @@ typedef enum {
     AG_ERR_CUDA = 6,        /* a CUDA runtime or driver call failed           */
     AG_ERR_ALIAS = 7,       /* an output buffer overlaps an input buffer      */
     AG_ERR_DEVICE = 8,      /* the device error word is set (see below)       */
-    AG_ERR_SCRATCH = 9      /* ag_attn_fwd_noalloc: the call needs more scratch
-                               than its static buffer holds                   */
+    AG_ERR_SCRATCH = 9      /* the call needs more scratch than it has: the
+                               static buffer of ag_attn_fwd_noalloc, or the
+                               workspace of the calls that take one           */
 } ag_status;
+
+/* Element types of the arguments that come in more than one. */
+typedef enum {
+    AG_F32 = 0,
+    AG_BF16 = 1,
+    AG_F16 = 2
+} ag_dtype;
 
 /* Static, human-readable name of a status code (never NULL). */
 const char *ag_status_string(int status);
@@ -325,6 +335,220 @@ ag_status ag_attn_bwd(const void *q, const void *k, const void *v, const float *
  * other widths.  Launches nothing.
  */
 ag_status ag_attn_bwd_launch_count(int64_t Dv, int *count);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The layers around the attention: the linear maps that make its queries,
+ * keys and values and read its output, the norm and rotation of queries and
+ * keys, and the clipping of all gradients by their global norm.  (The pages
+ * name no such operators beyond the attention itself; these are what a model
+ * that contains it, or its training, calls next to it.)
+ *
+ * Conventions beyond those at the top: matrices are row-major with a row
+ * stride of their own in elements (ldx >= the row's length; the elements of a
+ * row are dense).  A `workspace` is device memory of the caller's, 256-byte
+ * aligned, of at least the bytes that the call's _workspace function gives
+ * for the same arguments (0 bytes: it may be NULL; too few: AG_ERR_SCRATCH).
+ * Its contents before the call do not matter and after it mean nothing.  Calls
+ * that may overlap in time need a workspace each, which includes two captured
+ * graphs that may run at once; calls in order on one stream may share one.
+ */
+
+/* Activations of the linear layers. */
+typedef enum {
+    AG_ACT_NONE = 0,      /* z                                                  */
+    AG_ACT_RELU = 1,      /* max(z, 0)                                          */
+    AG_ACT_GELU = 2,      /* z (1 + erf(z / sqrt 2)) / 2                        */
+    AG_ACT_GELU_TANH = 3, /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2    */
+    AG_ACT_SILU = 4       /* z / (1 + exp(-z))                                  */
+} ag_act;
+
+/*
+ * ag_linear_fwd -- y = act(x W^T + bias) + residual.
+ *
+ *   x        [M, K] dtype, row stride ldx
+ *   W        [N, K] dtype, row stride ldw
+ *   bias     [N] float32, or NULL
+ *   residual [M, N] y_dtype, row stride ldr, or NULL
+ *   y        [M, N] y_dtype, row stride ldy (written)
+ *   preact   [M, N] dtype, row stride ldz, or NULL (written): z = x W^T + bias
+ *            rounded to dtype, which ag_linear_bwd of the NEXT layer takes
+ *   dtype AG_BF16 or AG_F16; y_dtype dtype or AG_F32; act an ag_act.
+ * Products of dtype values are summed in float32; bias, activation and
+ * residual are applied in float32 and y (and preact) rounded once.  The sums
+ * are promoted out of the tensor core's accumulator every 512 terms, which
+ * truncates rather than rounds (see linear_sm100.cu).
+ * M >= 0 (M == 0 is a no-op), N, K >= 1 (AG_ERR_SHAPE), and a row stride not
+ * below its row (AG_ERR_SHAPE); M <= 2^26, N, K <= 2^20, every stride <= 2^28
+ * (AG_ERR_UNSUPPORTED); an unknown dtype, y_dtype or act is AG_ERR_VALUE.
+ * Pointers aligned to their element; rows whose start is not 16-byte aligned
+ * (odd sizes, strides or offsets) cost a copy of that matrix into the
+ * workspace.  The outputs may not overlap an input or each other
+ * (AG_ERR_ALIAS); y may be the residual itself (same pointer and stride).
+ * Bitwise reproducible.
+ */
+ag_status ag_linear_fwd(const void *x, int64_t ldx, const void *W, int64_t ldw,
+                        const float *bias, const void *residual, int64_t ldr, int64_t M,
+                        int64_t N, int64_t K, int dtype, int act, void *preact, int64_t ldz,
+                        void *y, int64_t ldy, int y_dtype, void *workspace,
+                        int64_t workspace_bytes, void *stream);
+
+/* Bytes of workspace that ag_linear_fwd takes for these arguments on the
+ * current device (bytes is a host pointer; AG_ERR_NULL if NULL). */
+ag_status ag_linear_fwd_workspace(const void *x, int64_t ldx, const void *W, int64_t ldw,
+                                  int64_t M, int64_t N, int64_t K, int64_t *bytes);
+
+/*
+ * ag_linear_bwd -- gradients of y = x W^T + bias for an upstream gradient dy
+ * (that of ag_linear_fwd before its activation; the residual's gradient is dy
+ * itself):
+ *   dx[m,k] = sum_n dy[m,n] W[n,k]  (times act'(preact[m,k]) when given)
+ *   dW[n,k] = sum_m dy[m,n] x[m,k]
+ *   db[n]   = sum_m dy[m,n]
+ * The activation here is the one that made x: with x = act(preact), as the
+ * layer before wrote both, dx is the gradient of preact, which is that
+ * layer's dy.  So a chain of layers needs no pass over an activation alone.
+ *
+ *   dy [M, N] dtype, row stride lddy;  x [M, K], W [N, K] as ag_linear_fwd
+ *   preact [M, K] dtype, row stride ldz, or NULL with act == AG_ACT_NONE
+ *   dx [M, K] dx_dtype, row stride lddx, or NULL: not wanted
+ *   dW [N, K] dW_dtype, row stride lddw, or NULL: not wanted
+ *   db [N] float32, or NULL: not wanted
+ *   dx_dtype, dW_dtype: dtype or AG_F32.
+ * With M == 0, dW and db are written as zeros.  x is read for dW only and W
+ * for dx only (either may be NULL when its product is not wanted).  Sums,
+ * rounding, sizes, statuses and the workspace as ag_linear_fwd; AG_ERR_VALUE
+ * also for an act without a preact.  Bitwise reproducible.
+ */
+ag_status ag_linear_bwd(const void *dy, int64_t lddy, const void *x, int64_t ldx,
+                        const void *W, int64_t ldw, const void *preact, int64_t ldz, int act,
+                        int64_t M, int64_t N, int64_t K, int dtype, void *dx, int64_t lddx,
+                        int dx_dtype, void *dW, int64_t lddw, int dW_dtype, float *db,
+                        void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Bytes of workspace that ag_linear_bwd takes for these arguments (dx, dW and
+ * db only as wanted or NULL). */
+ag_status ag_linear_bwd_workspace(const void *dy, int64_t lddy, const void *x, int64_t ldx,
+                                  const void *W, int64_t ldw, int64_t M, int64_t N, int64_t K,
+                                  const void *dx, const void *dW, const float *db,
+                                  int64_t *bytes);
+
+/* How a head is normalised, and which of its elements a rotation pairs. */
+typedef enum {
+    AG_NORM_NONE = 0,
+    AG_NORM_RMS = 1,      /* x / sqrt(mean(x^2) + eps)                          */
+    AG_NORM_LAYER = 2     /* (x - mean x) / sqrt(var x + eps)                   */
+} ag_norm;
+typedef enum {
+    AG_ROPE_HALVES = 0,      /* pairs (i, i + R/2), i < R/2                     */
+    AG_ROPE_INTERLEAVED = 1  /* pairs (2i, 2i + 1)                              */
+} ag_rope;
+
+/*
+ * ag_qk_norm_rope_fwd -- the norm of every head of the queries and of the
+ * keys, their weights, the rotation by position, and the change to the
+ * attention's layout, in one pass.  For each (b, l, head), with w and b the
+ * queries' or the keys':
+ *   n = norm(x[b, l, h, :]),  v = n * w + b,
+ *   (out_i, out_j) = (v_i cos a - v_j sin a, v_j cos a + v_i sin a),
+ *   a = position[b, l] * inv_freq[p] for the p-th pair (i, j) of the first R
+ *   elements; the elements from R on are v.
+ * Angles are formed and reduced in 64 bits, so positions far apart (alignment
+ * columns, base pairs) keep their phase; everything else is float32, rounded
+ * once.
+ *
+ *   q  [B, L, Hq, D] x_dtype, element strides q_sb, q_sl, q_sh over b, l, h
+ *      (>= 0; D is dense), e.g. a slice of a fused projection's rows
+ *   k  [B, L, Hk, D] likewise
+ *   q_weight, q_bias, k_weight, k_bias [D] float32, each NULL for 1 or 0
+ *   inv_freq [R / 2] float64 (radians per position), or NULL with R == 0
+ *   positions int64, position[b, l] = positions[b * pos_sb + l]; NULL: l
+ *   q_out [B, Hq, L, D], k_out [B, Hk, L, D] out_dtype, dense (written): with
+ *      Hk == 1 the layouts of ag_attn_fwd's q and k
+ *   norm an ag_norm, eps >= 0 and finite, rope an ag_rope (AG_ERR_VALUE);
+ *   x_dtype, out_dtype any ag_dtype.
+ * Hq == 0 (or Hk == 0) leaves the queries (the keys) out.  1 <= D <= 1024, R
+ * even, 0 <= R <= D (AG_ERR_SHAPE / AG_ERR_UNSUPPORTED for D > 1024); B * L *
+ * (Hq + Hk) <= 2^31 - 1, Hq and Hk <= 65536 and no dimension spanning more
+ * than 2^50 elements (AG_ERR_UNSUPPORTED); B == 0 or L == 0 is a no-op.
+ * Pointers aligned to their element.  Outputs may not overlap inputs or each
+ * other (AG_ERR_ALIAS).  A row of zeros with eps == 0 has no norm (NaN).
+ */
+ag_status ag_qk_norm_rope_fwd(const void *q, int64_t q_sb, int64_t q_sl, int64_t q_sh,
+                              const void *k, int64_t k_sb, int64_t k_sl, int64_t k_sh,
+                              int x_dtype, const float *q_weight, const float *q_bias,
+                              const float *k_weight, const float *k_bias, int norm, float eps,
+                              const double *inv_freq, int64_t R, int rope,
+                              const int64_t *positions, int64_t pos_sb, int64_t B, int64_t Hq,
+                              int64_t Hk, int64_t L, int64_t D, void *q_out, void *k_out,
+                              int out_dtype, void *stream);
+
+/*
+ * ag_qk_norm_rope_bwd -- gradients of ag_qk_norm_rope_fwd for upstream
+ * gradients of q_out and k_out (e.g. ag_attn_bwd's dq and dk).  With g the
+ * upstream gradient rotated back, r the norm's factor and d = g * w:
+ *   db = sum g,  dw = sum g * n  (over b, l and the heads),
+ *   dx = r (d - n mean(d n) [- mean d for AG_NORM_LAYER])  (AG_NORM_NONE: d).
+ * The norm's statistics are formed again from q and k.
+ *
+ *   dq_out [B, Hq, L, D], dk_out [B, Hk, L, D] g_dtype, dense
+ *   q ... D as ag_qk_norm_rope_fwd (the biases have no part in the gradients)
+ *   dq [B, L, Hq, D] x_dtype with element strides dq_sb, dq_sl, dq_sh and dk
+ *      likewise (written).  No two elements of dq (of dk) may share an
+ *      address (AG_ERR_SHAPE).  dq and dk may lie side by side in the same
+ *      rows (a fused projection's gradient); otherwise no output may overlap
+ *      an input or another output (AG_ERR_ALIAS).
+ *   dq_weight, dq_bias, dk_weight, dk_bias [D] float32 (written), each NULL:
+ *      not wanted.  With B == 0 or L == 0, or for a side without heads, they
+ *      are written as zeros.
+ * workspace: ag_qk_norm_rope_bwd_workspace.  Bitwise reproducible.
+ */
+ag_status ag_qk_norm_rope_bwd(const void *dq_out, const void *dk_out, int g_dtype,
+                              const void *q, int64_t q_sb, int64_t q_sl, int64_t q_sh,
+                              const void *k, int64_t k_sb, int64_t k_sl, int64_t k_sh,
+                              int x_dtype, const float *q_weight, const float *k_weight,
+                              int norm, float eps, const double *inv_freq, int64_t R, int rope,
+                              const int64_t *positions, int64_t pos_sb, int64_t B, int64_t Hq,
+                              int64_t Hk, int64_t L, int64_t D, void *dq, int64_t dq_sb,
+                              int64_t dq_sl, int64_t dq_sh, void *dk, int64_t dk_sb,
+                              int64_t dk_sl, int64_t dk_sh, float *dq_weight, float *dq_bias,
+                              float *dk_weight, float *dk_bias, void *workspace,
+                              int64_t workspace_bytes, void *stream);
+
+/* Bytes of workspace that ag_qk_norm_rope_bwd takes on the current device
+ * (0 when none of the four weight and bias gradients is wanted). */
+ag_status ag_qk_norm_rope_bwd_workspace(int64_t B, int64_t L, int64_t D, int wants_params,
+                                        int64_t *bytes);
+
+/*
+ * ag_grad_clip -- the global 2-norm of n gradient tensors, and their scaling
+ * in place:
+ *   norm = sqrt(sum over all tensors and elements of g^2)   -> *norm_out
+ *   c = min(1, max_norm / (norm + eps)),  g = c g  (rounded to g's type)
+ * grads, counts and dtypes are HOST arrays of n device pointers, element
+ * counts and ag_dtype codes, read before the call returns; each tensor is
+ * dense (any dimension order).  A tensor with count 0 is skipped (its pointer
+ * may be NULL).  With c == 1 the gradients are left as they are; max_norm =
+ * +INFINITY only measures.  A gradient that is not finite makes norm
+ * infinite or NaN: an infinite norm scales by 0 (so that the infinite
+ * elements become NaN), a NaN one makes every element NaN.
+ *   norm_out  float32, 4-byte aligned (written); the sum is kept in 64 bits
+ *   max_norm >= 0, eps >= 0 and not NaN (AG_ERR_VALUE); an unknown dtype
+ *   likewise.  n >= 0, every count in [0, 2^40] (AG_ERR_SHAPE), their sum at
+ *   most 2^42 and n at most 2^20 (AG_ERR_UNSUPPORTED); pointers aligned to
+ *   their element.  No two tensors may overlap (the same tensor twice
+ *   included), nor norm_out or the workspace a tensor (AG_ERR_ALIAS).
+ *   n == 0 writes norm 0.
+ * Bitwise reproducible.  The host arrays are not read again by a replay of a
+ * captured graph, which uses the pointers of the capture.
+ */
+ag_status ag_grad_clip(void *const *grads, const int64_t *counts, const int *dtypes, int64_t n,
+                       float max_norm, float eps, float *norm_out, void *workspace,
+                       int64_t workspace_bytes, void *stream);
+
+/* Bytes of workspace that ag_grad_clip takes for n tensors on the current
+ * device. */
+ag_status ag_grad_clip_workspace(int64_t n, int64_t *bytes);
 
 /*
  * Device error word.  Every wait inside the kernels is bounded (about one

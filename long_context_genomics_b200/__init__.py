@@ -1,4 +1,5 @@
-"""Python binding of libag: pair-bias multi-query attention on B200.
+"""Python binding of libag: pair-bias multi-query attention on B200, and the
+layers around it.
 
 Argument marshalling only.  Every step of the computation runs in the CUDA
 kernels of libag.so (see include/ag.h for the C ABI); there is no CPU or
@@ -8,13 +9,19 @@ missing.  PyTorch supplies device memory and the current stream.
     ag_pair_bias_project(pair[P,P,Cp] f32, W[Cp,H] f32) -> bias[H,P,P] f32
     ag_attn_fwd(q[B,H,L,D] bf16, k[B,L,D] bf16, v[B,L,D] bf16,
                 bias[H,P,P] f32, cap) -> (out[B,H,L,D] f32, lse[B,H,L] f32)
+    ag_linear_fwd(x[M,K], W[N,K], bias, act, residual) -> y[M,N]
+    ag_qk_norm_rope_fwd(q[B,L,H,D], k[B,L,D], ...) -> (q[B,H,L,D], k[B,L,D])
+    ag_grad_clip(grads, max_norm) -> norm
+    (and the gradients of the first three: ag_attn_bwd, ag_linear_bwd,
+    ag_qk_norm_rope_bwd)
 
-The operation is Eq. L_ij of the page "Making Full-Context AlphaGenome Fit
+The attention is Eq. L_ij of the page "Making Full-Context AlphaGenome Fit
 on an RTX 3090" (section "Why stock FlashAttention was not a drop-in
 replacement") with a softmax over all keys.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -82,6 +89,30 @@ def _load() -> ctypes.CDLL:
     lib.ag_attn_bwd.restype = ctypes.c_int
     lib.ag_attn_bwd_launch_count.argtypes = [i64, ctypes.POINTER(ctypes.c_int)]
     lib.ag_attn_bwd_launch_count.restype = ctypes.c_int
+    i32 = ctypes.c_int
+    i64p = ctypes.POINTER(i64)
+    lib.ag_linear_fwd.argtypes = [vp, i64, vp, i64, vp, vp, i64, i64, i64, i64, i32, i32, vp,
+                                  i64, vp, i64, i32, vp, i64, vp]
+    lib.ag_linear_fwd_workspace.argtypes = [vp, i64, vp, i64, i64, i64, i64, i64p]
+    lib.ag_linear_bwd.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, i32, i64, i64, i64, i32,
+                                  vp, i64, i32, vp, i64, i32, vp, vp, i64, vp]
+    lib.ag_linear_bwd_workspace.argtypes = [vp, i64, vp, i64, vp, i64, i64, i64, i64, vp, vp,
+                                            vp, i64p]
+    heads = [vp, i64, i64, i64]
+    lib.ag_qk_norm_rope_fwd.argtypes = (heads + heads + [i32, vp, vp, vp, vp, i32, f32, vp, i64,
+                                                         i32, vp, i64, i64, i64, i64, i64, i64,
+                                                         vp, vp, i32, vp])
+    lib.ag_qk_norm_rope_bwd.argtypes = ([vp, vp, i32] + heads + heads
+                                        + [i32, vp, vp, i32, f32, vp, i64, i32, vp, i64, i64,
+                                           i64, i64, i64, i64] + heads + heads
+                                        + [vp, vp, vp, vp, vp, i64, vp])
+    lib.ag_qk_norm_rope_bwd_workspace.argtypes = [i64, i64, i64, i32, i64p]
+    lib.ag_grad_clip.argtypes = [vp, vp, vp, i64, f32, f32, vp, vp, i64, vp]
+    lib.ag_grad_clip_workspace.argtypes = [i64, i64p]
+    for fn in (lib.ag_linear_fwd, lib.ag_linear_fwd_workspace, lib.ag_linear_bwd,
+               lib.ag_linear_bwd_workspace, lib.ag_qk_norm_rope_fwd, lib.ag_qk_norm_rope_bwd,
+               lib.ag_qk_norm_rope_bwd_workspace, lib.ag_grad_clip, lib.ag_grad_clip_workspace):
+        fn.restype = i32
     lib.ag_device_error.argtypes = [ctypes.c_int, ctypes.POINTER(ctypes.c_int),
                                     ctypes.c_int]
     lib.ag_device_error.restype = ctypes.c_int
@@ -346,6 +377,411 @@ def ag_attn_bwd_launch_count(Dv: int = 128) -> int:
     if st != AG_OK:
         raise AgError("ag_attn_bwd_launch_count", st)
     return int(n.value)
+
+
+# ---------------------------------------------------------------------------
+# The layers around the attention.
+
+DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+NORMS = {"none": 0, "rms": 1, "layer": 2}
+ROPES = {"halves": 0, "interleaved": 1}
+_HALF = (torch.bfloat16, torch.float16)
+_NOTHING = contextlib.nullcontext()
+
+
+def _site(dev: torch.device, stream):
+    """Context in which a call's memory is allocated and its kernels launched:
+    the tensors' device and the caller's stream (default: that device's
+    current stream).  Workspaces belong to that stream, so a later call on it
+    may take their memory over, and no other stream does."""
+    if stream is None:
+        return _NOTHING if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=dev)
+    if stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, the tensors are on {dev}")
+    return torch.cuda.stream(stream)
+
+
+def _current(dev: torch.device) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev.index)
+
+
+def _code(table: dict, value, name: str) -> int:
+    try:
+        return table[value]
+    except (KeyError, TypeError):
+        raise ValueError(f"{name} must be one of {', '.join(map(str, table))}, got {value}") from None
+
+
+def _on_gpu(t, name: str, dtypes) -> None:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be on a CUDA device")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+
+
+def _matrix(t, name: str, dtypes, rows: int, cols: int) -> int:
+    """Checks a row-major matrix (its rows may be apart) and returns its row stride."""
+    _on_gpu(t, name, dtypes)
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError(f"{name} must be [{rows},{cols}], got {list(t.shape)}")
+    ld, inner = t.stride()
+    if inner != 1 and cols > 1:
+        raise ValueError(f"the rows of {name} must be dense")
+    return ld if rows > 1 else max(ld, cols)
+
+
+def _vector(t, name: str, n: int):
+    """Checks an optional dense float32 vector of n and returns its pointer."""
+    if t is None:
+        return None
+    _on_gpu(t, name, (torch.float32,))
+    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous [{n}]")
+    return t.data_ptr()
+
+
+def _workspace(query, dev: torch.device, name: str, *args):
+    """Workspace of the bytes that `query` gives for args: (tensor, pointer, bytes)."""
+    n = ctypes.c_int64(0)
+    st = query(*args, ctypes.byref(n))
+    if st != AG_OK:
+        raise AgError(name, st)
+    if n.value == 0:
+        return None, None, 0
+    t = torch.empty(n.value, dtype=torch.uint8, device=dev)
+    return t, t.data_ptr(), n.value
+
+
+def ag_linear_fwd(x: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = None,
+                  act: str = "none", residual: torch.Tensor | None = None, preact=False,
+                  out: torch.Tensor | None = None, out_dtype: torch.dtype | None = None,
+                  stream=None):
+    """y = act(x W^T + bias) + residual (libag kernels).
+
+    x [M,K] and W [N,K] bf16 or fp16 (rows dense, row strides free); bias [N]
+    fp32; residual and y [M,N] in out_dtype (x's type, the default, or fp32).
+    act: none, relu, gelu, gelu_tanh, silu.  preact=True (or a [M,N] tensor of
+    x's type to write) also returns x W^T + bias, which ag_linear_bwd of the
+    next layer takes: (y, preact).  out may be the residual itself."""
+    _on_gpu(x, "x", _HALF)
+    if x.dim() != 2 or not isinstance(W, torch.Tensor) or W.dim() != 2:
+        raise ValueError("x must be [M,K] and W [N,K]")
+    (M, K), N, T, dev = x.shape, W.shape[0], x.dtype, x.device
+    ldx = _matrix(x, "x", (T,), M, K)
+    ldw = _matrix(W, "W", (T,), N, K)
+    code = _code(ACTIVATIONS, act, "act")
+    if out_dtype is None:
+        out_dtype = T if out is None else out.dtype
+    if out_dtype not in (T, torch.float32):
+        raise TypeError(f"out_dtype must be {T} or torch.float32, got {out_dtype}")
+    used = [x, W]
+    b = _vector(bias, "bias", N)
+    ldr = 0 if residual is None else _matrix(residual, "residual", (out_dtype,), M, N)
+    used += [t for t in (bias, residual) if t is not None]
+    with _site(dev, stream):
+        if out is None:
+            out = torch.empty((M, N), dtype=out_dtype, device=dev)
+        ldy = _matrix(out, "out", (out_dtype,), M, N)
+        used.append(out)
+        z = None
+        if preact is not False and preact is not None:
+            z = torch.empty((M, N), dtype=T, device=dev) if preact is True else preact
+            used.append(z)
+        ldz = 0 if z is None else _matrix(z, "preact", (T,), M, N)
+        _one_device(*used)
+        xp, wp = x.data_ptr(), W.data_ptr()
+        ws, wsp, n = _workspace(lib.ag_linear_fwd_workspace, dev, "ag_linear_fwd_workspace", xp,
+                                ldx, wp, ldw, M, N, K)
+        st = lib.ag_linear_fwd(xp, ldx, wp, ldw, b, None if residual is None else
+                               residual.data_ptr(), ldr, M, N, K, DTYPES[T], code,
+                               None if z is None else z.data_ptr(), ldz, out.data_ptr(), ldy,
+                               DTYPES[out_dtype], wsp, n, _current(dev))
+    if st != AG_OK:
+        raise AgError("ag_linear_fwd", st)
+    return out if z is None else (out, z)
+
+
+def ag_linear_bwd(dy: torch.Tensor, x: torch.Tensor, W: torch.Tensor, act: str = "none",
+                  preact: torch.Tensor | None = None, need_dx: bool = True,
+                  need_dW: bool = True, need_db: bool = True,
+                  dx_dtype: torch.dtype | None = None, dW_dtype: torch.dtype = torch.float32,
+                  dx: torch.Tensor | None = None, dW: torch.Tensor | None = None, stream=None):
+    """Gradients of y = x W^T + bias for the upstream gradient dy [M,N] (libag
+    kernels): (dx [M,K], dW [N,K], db [N] fp32), None where not needed.
+
+    With act and preact (x = act(preact), both from the layer before) dx is
+    the gradient of preact instead of x.  dx_dtype: x's type (default) or
+    fp32; dW_dtype: fp32 (default) or x's type.  dx and dW may be given to
+    write into.  The gradient of ag_linear_fwd's residual is dy itself."""
+    _on_gpu(dy, "dy", _HALF)
+    if dy.dim() != 2 or not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise ValueError("dy must be [M,N] and x [M,K]")
+    (M, N), K, T, dev = dy.shape, x.shape[1], dy.dtype, dy.device
+    lddy = _matrix(dy, "dy", (T,), M, N)
+    ldx = _matrix(x, "x", (T,), M, K)
+    ldw = _matrix(W, "W", (T,), N, K)
+    code = _code(ACTIVATIONS, act, "act")
+    ldz = 0 if preact is None else _matrix(preact, "preact", (T,), M, K)
+    if code and preact is None:
+        raise ValueError(f"act {act} needs the preact of x")
+    used = [t for t in (dy, x, W, preact) if t is not None]
+    with _site(dev, stream):
+        lddx = lddw = 0
+        if need_dx:
+            if dx is None:
+                dx = torch.empty((M, K), dtype=dx_dtype or T, device=dev)
+            lddx = _matrix(dx, "dx", (dx_dtype,) if dx_dtype else (T, torch.float32), M, K)
+            used.append(dx)
+        else:
+            dx = None
+        if need_dW:
+            if dW is None:
+                dW = torch.empty((N, K), dtype=dW_dtype, device=dev)
+            lddw = _matrix(dW, "dW", (T, torch.float32), N, K)
+            used.append(dW)
+        else:
+            dW = None
+        db = torch.empty(N, dtype=torch.float32, device=dev) if need_db else None
+        _one_device(*used)
+        p = [None if t is None else t.data_ptr() for t in (dy, x, W, preact, dx, dW, db)]
+        ws, wsp, n = _workspace(lib.ag_linear_bwd_workspace, dev, "ag_linear_bwd_workspace", p[0],
+                                lddy, p[1], ldx, p[2], ldw, M, N, K, p[4], p[5], p[6])
+        st = lib.ag_linear_bwd(p[0], lddy, p[1], ldx, p[2], ldw, p[3], ldz, code, M, N, K,
+                               DTYPES[T], p[4], lddx, DTYPES[dx.dtype] if need_dx else 0, p[5],
+                               lddw, DTYPES[dW.dtype] if need_dW else 0, p[6], wsp, n,
+                               _current(dev))
+    if st != AG_OK:
+        raise AgError("ag_linear_bwd", st)
+    return dx, dW, db
+
+
+def ag_rope_frequencies(rotary_dim: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
+    """inv_freq[p] = base^(-2p / rotary_dim), p < rotary_dim / 2, in fp64: the
+    usual frequencies for ag_qk_norm_rope_fwd (which takes any)."""
+    p = torch.arange(0, rotary_dim, 2, dtype=torch.float64)
+    return (float(base) ** (-p / rotary_dim)).to(device)
+
+
+def _heads(t, name: str, dtypes, B=None, L=None, H=None, D=None):
+    """Checks a [B,L,H,D] (or [B,L,D]: one head) tensor with dense heads.
+    Returns its sizes and its (b, l, h) strides."""
+    _on_gpu(t, name, dtypes)
+    if t.dim() not in (3, 4):
+        raise ValueError(f"{name} must be [B,L,H,D] or [B,L,D]")
+    shape, stride = tuple(t.shape), t.stride()
+    if t.dim() == 3:
+        shape, stride = shape[:2] + (1,) + shape[2:], stride[:2] + (0,) + stride[2:]
+    for got, want in zip(shape, (B, L, H, D)):
+        if want is not None and got != want:
+            raise ValueError(f"{name} must be {[B, L, H, D]}, got {list(shape)}")
+    if stride[3] != 1 and shape[3] > 1:
+        raise ValueError(f"the heads of {name} must be dense")
+    return shape, stride[:3]
+
+
+class _QkCall:
+    """The arguments that the two directions of ag_qk_norm_rope share."""
+
+    def __init__(self, q, k, q_weight, k_weight, q_bias, k_bias, norm, eps, inv_freq, rope,
+                 positions):
+        first = q if q is not None else k
+        if first is None:
+            raise ValueError("q and k are both None")
+        (self.B, self.L, _, self.D), _ = _heads(first, "q" if q is not None else "k", DTYPES)
+        self.T, self.dev = first.dtype, first.device
+        self.used, self.inputs, self.H, self.flat = [], [], [], []
+        for t, name in ((q, "q"), (k, "k")):
+            if t is None:
+                self.inputs += [None, 0, 0, 0]
+                self.H.append(0)
+                self.flat.append(False)
+                continue
+            shape, strides = _heads(t, name, (self.T,), B=self.B, L=self.L, D=self.D)
+            self.inputs += [t.data_ptr(), *strides]
+            self.H.append(shape[2])
+            self.flat.append(t.dim() == 3)
+            self.used.append(t)
+        self.weights = [_vector(t, n, self.D) for t, n in ((q_weight, "q_weight"),
+                                                           (k_weight, "k_weight"))]
+        self.biases = [_vector(t, n, self.D) for t, n in ((q_bias, "q_bias"), (k_bias, "k_bias"))]
+        self.used += [t for t in (q_weight, k_weight, q_bias, k_bias) if t is not None]
+        self.norm, self.rope = _code(NORMS, norm, "norm"), _code(ROPES, rope, "rope")
+        self.eps, self.R, freq = float(eps), 0, None
+        if inv_freq is not None:
+            _on_gpu(inv_freq, "inv_freq", (torch.float64,))
+            if inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+                raise ValueError("inv_freq must be a contiguous [R/2]")
+            self.R, freq = 2 * inv_freq.shape[0], inv_freq.data_ptr()
+            self.used.append(inv_freq)
+        where, pos_sb = None, 0
+        if positions is not None:
+            _on_gpu(positions, "positions", (torch.int64,))
+            if tuple(positions.shape) not in ((self.L,), (self.B, self.L)):
+                raise ValueError(f"positions must be [{self.L}] or [{self.B},{self.L}]")
+            if self.L > 1 and positions.stride(-1) != 1:
+                raise ValueError("the rows of positions must be dense")
+            where = positions.data_ptr()
+            pos_sb = positions.stride(0) if positions.dim() == 2 and self.B > 1 else 0
+            self.used.append(positions)
+        self.rotation = [freq, self.R, self.rope, where, pos_sb]
+        self.sizes = [self.B, self.H[0], self.H[1], self.L, self.D]
+
+    def layout(self, side: int):
+        """The attention's layout of a side: [B,H,L,D], or [B,L,D] for a [B,L,D] input."""
+        B, L, D, H = self.B, self.L, self.D, self.H[side]
+        return (B, L, D) if self.flat[side] else (B, H, L, D)
+
+    def dense(self, t, name: str, dtypes, side: int) -> int:
+        _on_gpu(t, name, dtypes)
+        if tuple(t.shape) != self.layout(side) or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {list(self.layout(side))}")
+        self.used.append(t)
+        return t.data_ptr()
+
+
+def ag_qk_norm_rope_fwd(q: torch.Tensor | None, k: torch.Tensor | None,
+                        q_weight: torch.Tensor | None = None,
+                        k_weight: torch.Tensor | None = None,
+                        q_bias: torch.Tensor | None = None,
+                        k_bias: torch.Tensor | None = None, norm: str = "rms",
+                        eps: float = 1e-6, inv_freq: torch.Tensor | None = None,
+                        rope: str = "halves", positions: torch.Tensor | None = None,
+                        out_dtype: torch.dtype = torch.bfloat16,
+                        q_out: torch.Tensor | None = None,
+                        k_out: torch.Tensor | None = None, stream=None):
+    """Norm of every query and key head, its weight and bias, the rotation by
+    position and the change to ag_attn_fwd's layout, in one pass (libag kernel).
+
+    q [B,L,H,D] and k [B,L,D] (or [B,L,Hk,D]) of one type, fp32, bf16 or fp16,
+    with dense heads and any other strides, e.g. slices of a fused
+    projection; weights and biases [D] fp32.  norm: rms, layer or none; rope:
+    halves (pairs i, i + R/2) or interleaved (2i, 2i+1) over the first
+    R = 2 len(inv_freq) elements, angle = position * inv_freq (fp64, see
+    ag_rope_frequencies; None: no rotation); positions int64 [L] or [B,L]
+    (default 0 .. L-1).  Returns (q_out [B,H,L,D], k_out [B,L,D] or
+    [B,Hk,L,D]); q or k may be None."""
+    c = _QkCall(q, k, q_weight, k_weight, q_bias, k_bias, norm, eps, inv_freq, rope, positions)
+    if out_dtype not in DTYPES:
+        raise TypeError(f"out_dtype must be one of {', '.join(map(str, DTYPES))}, got {out_dtype}")
+    with _site(c.dev, stream):
+        outs, ptrs = [q_out, k_out], [None, None]
+        for i, (t, name) in enumerate(((q, "q_out"), (k, "k_out"))):
+            if t is None:
+                outs[i] = None
+                continue
+            if outs[i] is None:
+                outs[i] = torch.empty(c.layout(i), dtype=out_dtype, device=c.dev)
+            ptrs[i] = c.dense(outs[i], name, (out_dtype,), i)
+        _one_device(*c.used)
+        st = lib.ag_qk_norm_rope_fwd(*c.inputs, DTYPES[c.T], c.weights[0], c.biases[0],
+                                     c.weights[1], c.biases[1], c.norm, c.eps, *c.rotation,
+                                     *c.sizes, *ptrs, DTYPES[out_dtype], _current(c.dev))
+    if st != AG_OK:
+        raise AgError("ag_qk_norm_rope_fwd", st)
+    return outs[0], outs[1]
+
+
+def ag_qk_norm_rope_bwd(dq_out: torch.Tensor | None, dk_out: torch.Tensor | None,
+                        q: torch.Tensor | None, k: torch.Tensor | None,
+                        q_weight: torch.Tensor | None = None,
+                        k_weight: torch.Tensor | None = None,
+                        q_bias: torch.Tensor | None = None,
+                        k_bias: torch.Tensor | None = None, norm: str = "rms",
+                        eps: float = 1e-6, inv_freq: torch.Tensor | None = None,
+                        rope: str = "halves", positions: torch.Tensor | None = None,
+                        dq: torch.Tensor | None = None, dk: torch.Tensor | None = None,
+                        stream=None):
+    """Gradients of ag_qk_norm_rope_fwd (libag kernels) for dq_out and dk_out
+    in the layout of its outputs and one type, e.g. ag_attn_bwd's dq and dk;
+    the other arguments as the forward's.  Returns (dq, dk, dq_weight,
+    dk_weight, dq_bias, dk_bias): dq and dk in the shape and type of q and k,
+    written into the tensors given (which may be slices of one fused
+    projection's gradient) or new ones; the others [D] fp32, None where the
+    forward had none."""
+    c = _QkCall(q, k, q_weight, k_weight, q_bias, k_bias, norm, eps, inv_freq, rope, positions)
+    g_dtype = next((t.dtype for t in (dq_out, dk_out) if isinstance(t, torch.Tensor)), None)
+    ups = [None if t is None else c.dense(g, name, (g_dtype,), i)
+           for i, (t, g, name) in enumerate(((q, dq_out, "dq_out"), (k, dk_out, "dk_out")))]
+    gt = _code(DTYPES, g_dtype, "the type of dq_out and dk_out")
+    with _site(c.dev, stream):
+        grads, outs = [dq, dk], []
+        for i, (t, name) in enumerate(((q, "dq"), (k, "dk"))):
+            if t is None:
+                grads[i] = None
+                outs += [None, 0, 0, 0]
+                continue
+            if grads[i] is None:
+                grads[i] = torch.empty(tuple(t.shape), dtype=c.T, device=c.dev)
+            if grads[i].dim() != t.dim():
+                raise ValueError(f"{name} must have the shape of {name[1:]}")
+            _, strides = _heads(grads[i], name, (c.T,), B=c.B, L=c.L, H=c.H[i], D=c.D)
+            outs += [grads[i].data_ptr(), *strides]
+            c.used.append(grads[i])
+        params = [None if t is None else torch.empty(c.D, dtype=torch.float32, device=c.dev)
+                  for t in (q_weight, q_bias, k_weight, k_bias)]
+        _one_device(*c.used)
+        p = [None if t is None else t.data_ptr() for t in params]
+        ws, wsp, n = _workspace(lib.ag_qk_norm_rope_bwd_workspace, c.dev,
+                                "ag_qk_norm_rope_bwd_workspace", c.B, c.L, c.D,
+                                int(any(p)))
+        st = lib.ag_qk_norm_rope_bwd(*ups, gt, *c.inputs, DTYPES[c.T], *c.weights, c.norm, c.eps,
+                                     *c.rotation, *c.sizes, *outs, *p, wsp, n, _current(c.dev))
+    if st != AG_OK:
+        raise AgError("ag_qk_norm_rope_bwd", st)
+    return grads[0], grads[1], params[0], params[2], params[1], params[3]
+
+
+def _is_dense(t: torch.Tensor) -> bool:
+    """Whether the elements fill one block of memory, in any dimension order."""
+    if t.is_contiguous():
+        return True
+    want = 1
+    for stride, size in sorted((s, n) for s, n in zip(t.stride(), t.shape) if n > 1):
+        if stride != want:
+            return False
+        want *= size
+    return True
+
+
+def ag_grad_clip(grads, max_norm: float, eps: float = 1e-6,
+                 norm: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The global 2-norm of the gradients and their scaling in place by
+    min(1, max_norm / (norm + eps)) (libag kernels).
+
+    grads: a sequence of dense fp32, bf16 or fp16 tensors on one device, none
+    overlapping another (None entries are skipped).  max_norm = math.inf only
+    measures.  Returns the norm before scaling, an fp32 scalar tensor on the
+    device (`norm` if given); nothing waits for it."""
+    grads = [g for g in grads if g is not None]
+    if not grads:
+        raise ValueError("grads has no tensor")
+    for g in grads:
+        _on_gpu(g, "every gradient", DTYPES)
+        if g.layout != torch.strided or not _is_dense(g):
+            raise ValueError("every gradient must be dense")
+    n = len(grads)
+    dev = grads[0].device if norm is None else _one_device(grads[0], norm)
+    _one_device(*grads)
+    ptrs = (ctypes.c_void_p * n)(*[g.data_ptr() for g in grads])
+    counts = (ctypes.c_int64 * n)(*[g.numel() for g in grads])
+    types = (ctypes.c_int * n)(*[DTYPES[g.dtype] for g in grads])
+    with _site(dev, stream):
+        if norm is None:
+            norm = torch.empty((), dtype=torch.float32, device=dev)
+        _on_gpu(norm, "norm", (torch.float32,))
+        if norm.numel() != 1:
+            raise ValueError("norm must have one element")
+        ws, wsp, size = _workspace(lib.ag_grad_clip_workspace, dev, "ag_grad_clip_workspace", n)
+        st = lib.ag_grad_clip(ptrs, counts, types, n, float(max_norm), float(eps),
+                              norm.data_ptr(), wsp, size, _current(dev))
+    if st != AG_OK:
+        raise AgError("ag_grad_clip", st)
+    return norm
 
 
 def ag_device_error(device: int = 0, clear: bool = True) -> int:

@@ -17,9 +17,10 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libag.so")
-SOURCES = ["ag_api.cu", "attn_fwd_sm100.cu", "attn_noalloc.cu", "attn_bwd.cu",
-           "attn_bwd_sm100.cu", "pair_bias_project.cu"]
-HEADERS = ["sm100.cuh", "ag_internal.h", "attn_bwd_phases.cuh"]
+SOURCES = ["ag_api.cu", "ag_layers_api.cu", "attn_fwd_sm100.cu", "attn_noalloc.cu", "attn_bwd.cu",
+           "attn_bwd_sm100.cu", "pair_bias_project.cu", "linear.cu", "qk_norm_rope.cu",
+           "grad_clip.cu"]
+HEADERS = ["sm100.cuh", "ag_internal.h", "attn_bwd_phases.cuh", "linear_epilogue.cuh"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 

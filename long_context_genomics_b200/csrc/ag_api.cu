@@ -132,7 +132,7 @@ const char *ag_status_string(int s) {
     case AG_ERR_ALIAS: return "AG_ERR_ALIAS: an output overlaps an input";
     case AG_ERR_DEVICE: return "AG_ERR_DEVICE: the device error word is set";
     case AG_ERR_SCRATCH:
-      return "AG_ERR_SCRATCH: the call needs more scratch than the static buffer holds";
+      return "AG_ERR_SCRATCH: the call needs more scratch than it was given or the library holds";
     default: return "unknown ag_status";
   }
 }

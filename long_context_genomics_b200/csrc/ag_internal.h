@@ -103,6 +103,77 @@ cudaError_t launch_pair_bias_project(const float *pair, const float *W,
                                      unsigned *err, EncodeTiledFn encode,
                                      cudaStream_t stream);
 
+// Linear layers (linear.cu, linear_sm100.cu): what is done to a product's
+// float32 sums before they are stored (linear_epilogue.cuh).
+struct LinearEpilogue {
+  const float *bias;      // [columns], or NULL
+  const void *pre_in;     // multiply by act'(pre_in), or NULL: apply act
+  void *pre_out;          // the sums with their bias, rounded to dtype, or NULL
+  const void *residual;   // of the output's type, or NULL
+  void *out;
+  int64_t ld_pre_in, ld_pre_out, ld_res, ld_out;
+  int act, dtype, out_dtype;  // dtype: of the operands, pre_in and pre_out
+  int vec8;               // rows of 8-column groups are 16-byte aligned in every array
+};
+struct LinearFwd {
+  const void *x, *W;
+  int64_t ldx, ldw, M, N, K;
+  LinearEpilogue epi;
+  void *workspace;
+  int num_sms;
+  unsigned *err;
+  EncodeTiledFn encode;
+  cudaStream_t stream;
+};
+cudaError_t linear_fwd_workspace(const LinearFwd &a, int64_t *bytes);
+cudaError_t launch_linear_fwd(const LinearFwd &a);
+struct LinearBwd {
+  const void *dy, *x, *W;
+  int64_t lddy, ldx, ldw, M, N, K;
+  LinearEpilogue dx, dW;  // out NULL: not wanted
+  float *db;              // or NULL
+  void *workspace;
+  int num_sms;
+  unsigned *err;
+  EncodeTiledFn encode;
+  cudaStream_t stream;
+};
+cudaError_t linear_bwd_workspace(const LinearBwd &a, int64_t *bytes);
+cudaError_t launch_linear_bwd(const LinearBwd &a);
+
+// Norm and rotation of queries and keys (qk_norm_rope.cu).
+struct QkSide {
+  const void *x;          // [B, L, H, D] with element strides sb, sl, sh
+  int64_t sb, sl, sh;
+  int H;
+  const float *w, *b;
+  void *out;              // forward: [B, H, L, D]
+  const void *g;          // backward: upstream gradient [B, H, L, D]
+  void *dx;               // backward: element strides db_, dl, dh
+  int64_t dxb, dxl, dxh;
+  float *dw, *db;         // backward: parameter gradients, or NULL
+};
+struct QkArgs {
+  QkSide side[2];         // queries, keys
+  const double *inv_freq;
+  const int64_t *positions;
+  int64_t pos_sb;
+  int64_t positions_total;  // B * L
+  int64_t B, L;
+  int D, R, norm, rope, x_dtype, o_dtype;  // o_dtype: of out or g
+  float eps;
+  float *partial;         // backward: parameter gradients' partial sums
+};
+cudaError_t launch_qk_fwd(const QkArgs &a, int num_sms, cudaStream_t stream);
+cudaError_t launch_qk_bwd(const QkArgs &a, int num_sms, cudaStream_t stream);
+int64_t qk_bwd_workspace(int64_t positions_total, int64_t D, int num_sms);
+
+// Global gradient norm and clipping (grad_clip.cu).
+cudaError_t launch_grad_clip(void *const *grads, const int64_t *counts, const int *dtypes,
+                             int64_t n, float max_norm, float eps, float *norm_out,
+                             double *workspace, int num_sms, cudaStream_t stream);
+int64_t grad_clip_workspace(int64_t n, int num_sms);
+
 cudaError_t launch_wait_timeout_probe(uint64_t timeout_ns, unsigned *err,
                                       cudaStream_t stream);
 

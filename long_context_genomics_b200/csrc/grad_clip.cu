@@ -1,0 +1,214 @@
+// grad_clip.cu -- the global 2-norm of many gradient tensors and their scaling
+// in place (ag_grad_clip).
+//
+//   norm = sqrt(sum g^2),  c = min(1, max_norm / (norm + eps)),  g = c g
+//
+// Bound by memory: one read for the norm, and where c < 1 another read and a
+// write.  The tensors are cut into chunks; a fixed grid of blocks takes them
+// in turn, so a partial sum belongs to a block and the order of every
+// addition is fixed.  Squares and sums are in 64 bits: a float32 square of a
+// large gradient overflows and of a small one vanishes.
+#include <cmath>
+
+#include "ag_internal.h"
+#include "linear_epilogue.cuh"
+
+namespace ag {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kChunk = 16384;         // elements
+constexpr int kMaxTensors = 512;      // per launch: the list travels as a kernel argument
+constexpr int kBlocksPerSm = 4;
+
+struct TensorList {
+  void *ptr[kMaxTensors];
+  int64_t count[kMaxTensors];
+  uint32_t first[kMaxTensors + 1];    // first chunk of each tensor
+  uint8_t dtype[kMaxTensors];
+  int n;
+};
+
+struct Chunk {
+  void *base;
+  int64_t at;
+  int len, dtype;
+};
+__device__ __forceinline__ Chunk chunk_of(const TensorList &list, uint32_t c) {
+  int lo = 0, hi = list.n;            // first[lo] <= c < first[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (list.first[mid] <= c) lo = mid;
+    else hi = mid;
+  }
+  Chunk k;
+  k.base = list.ptr[lo];
+  k.at = static_cast<int64_t>(c - list.first[lo]) * kChunk;
+  const int64_t left = list.count[lo] - k.at;
+  k.len = static_cast<int>(left < kChunk ? left : kChunk);
+  k.dtype = list.dtype[lo];
+  return k;
+}
+
+// Elements of the chunk before the first whose address is 16-byte aligned.
+__device__ __forceinline__ int head_of(const Chunk &k) {
+  const int size = k.dtype == AG_F32 ? 4 : 2;
+  const uintptr_t p = reinterpret_cast<uintptr_t>(k.base) + static_cast<uintptr_t>(k.at) * size;
+  const int h = static_cast<int>((16 - (p & 15)) & 15) / size;
+  return h < k.len ? h : k.len;
+}
+
+__device__ __forceinline__ double block_sum(double s) {
+  __shared__ double part[kThreads / 32];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  __syncthreads();
+  if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = s;
+  __syncthreads();
+  double t = 0.0;
+#pragma unroll
+  for (int i = 0; i < kThreads / 32; ++i) t += part[i];
+  return t;
+}
+
+__global__ void __launch_bounds__(kThreads)
+    square_sum_kernel(const __grid_constant__ TensorList list, double *partial) {
+  double s = 0.0;
+  for (uint32_t c = blockIdx.x; c < list.first[list.n]; c += gridDim.x) {
+    const Chunk k = chunk_of(list, c);
+    const int head = head_of(k), body = (k.len - head) / 8;
+    for (int i = threadIdx.x; i < body; i += kThreads) {
+      float v[8];
+      load_values<8>(k.base, k.at + head + 8 * static_cast<int64_t>(i), k.dtype, v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s = fma(static_cast<double>(v[j]), static_cast<double>(v[j]), s);
+    }
+    const int rest = k.len - 8 * body;  // the head and the tail, one by one
+    if (static_cast<int>(threadIdx.x) < rest) {
+      const int i = static_cast<int>(threadIdx.x) < head ? threadIdx.x : threadIdx.x + 8 * body;
+      float v[1];
+      load_values<1>(k.base, k.at + i, k.dtype, v);
+      s = fma(static_cast<double>(v[0]), static_cast<double>(v[0]), s);
+    }
+  }
+  s = block_sum(s);
+  if (threadIdx.x == 0) partial[blockIdx.x] = s;
+}
+
+// The sum of `slots` partials, the same in every block and thread.
+__device__ __forceinline__ double total_of(const double *partial, int slots) {
+  double s = 0.0;
+  for (int i = threadIdx.x; i < slots; i += kThreads) s += partial[i];
+  return block_sum(s);
+}
+
+__global__ void __launch_bounds__(kThreads)
+    total_kernel(const double *partial, int slots, double *total) {
+  const double t = total_of(partial, slots);
+  if (threadIdx.x == 0) *total = t;
+}
+
+__global__ void __launch_bounds__(kThreads)
+    scale_kernel(const __grid_constant__ TensorList list, const double *partial, int slots,
+                 float max_norm, float eps, float *norm_out) {
+  const double norm = sqrt(total_of(partial, slots));
+  if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = static_cast<float>(norm);
+  if (max_norm == INFINITY) return;
+  const double ratio = static_cast<double>(max_norm) / (norm + static_cast<double>(eps));
+  // Written so that a NaN stays a NaN.
+  const float c = ratio >= 1.0 ? 1.f : static_cast<float>(ratio);
+  if (c == 1.f) return;
+  for (uint32_t q = blockIdx.x; q < list.first[list.n]; q += gridDim.x) {
+    const Chunk k = chunk_of(list, q);
+    const int head = head_of(k), body = (k.len - head) / 8;
+    for (int i = threadIdx.x; i < body; i += kThreads) {
+      float v[8];
+      const int64_t at = k.at + head + 8 * static_cast<int64_t>(i);
+      load_values<8>(k.base, at, k.dtype, v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] *= c;
+      store_values<8>(k.base, at, k.dtype, v);
+    }
+    const int rest = k.len - 8 * body;
+    if (static_cast<int>(threadIdx.x) < rest) {
+      const int i = static_cast<int>(threadIdx.x) < head ? threadIdx.x : threadIdx.x + 8 * body;
+      float v[1];
+      load_values<1>(k.base, k.at + i, k.dtype, v);
+      v[0] *= c;
+      store_values<1>(k.base, k.at + i, k.dtype, v);
+    }
+  }
+}
+
+// Takes tensors [from, n) that are not empty into `list` up to its capacity;
+// returns the next index.  The entry point's limits (2^42 elements, 2^20
+// tensors) keep the chunks of a launch below 2^29.
+int64_t fill(TensorList &list, void *const *grads, const int64_t *counts, const int *dtypes,
+             int64_t from, int64_t n) {
+  list.n = 0;
+  list.first[0] = 0;
+  int64_t chunks = 0;
+  int64_t i = from;
+  for (; i < n && list.n < kMaxTensors; ++i) {
+    if (counts[i] == 0) continue;
+    list.ptr[list.n] = grads[i];
+    list.count[list.n] = counts[i];
+    list.dtype[list.n] = static_cast<uint8_t>(dtypes[i]);
+    chunks += (counts[i] + kChunk - 1) / kChunk;
+    list.first[++list.n] = static_cast<uint32_t>(chunks);
+  }
+  return i;
+}
+
+}  // namespace
+
+// One partial per block and launch, and the total of several launches.
+int64_t grad_clip_workspace(int64_t n, int num_sms) {
+  const int64_t launches = n <= kMaxTensors ? 1 : (n + kMaxTensors - 1) / kMaxTensors;
+  return (launches * num_sms * kBlocksPerSm + 1) * static_cast<int64_t>(sizeof(double));
+}
+
+cudaError_t launch_grad_clip(void *const *grads, const int64_t *counts, const int *dtypes,
+                             int64_t n, float max_norm, float eps, float *norm_out,
+                             double *workspace, int num_sms, cudaStream_t stream) {
+  const int most = num_sms * kBlocksPerSm;
+  TensorList list;
+  int slots = 0, launches = 0;
+  for (int64_t i = 0; i < n;) {
+    i = fill(list, grads, counts, dtypes, i, n);
+    if (list.n == 0) break;
+    const unsigned chunks = list.first[list.n];
+    const int blocks = chunks < static_cast<unsigned>(most) ? static_cast<int>(chunks) : most;
+    square_sum_kernel<<<blocks, kThreads, 0, stream>>>(list, workspace + slots);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    slots += blocks;
+    ++launches;
+  }
+  const double *sums = workspace;
+  if (launches > 1) {
+    double *total = workspace + slots;
+    total_kernel<<<1, kThreads, 0, stream>>>(workspace, slots, total);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    sums = total;
+    slots = 1;
+  }
+  int64_t i = 0;
+  bool first = true;
+  do {
+    i = fill(list, grads, counts, dtypes, i, n);
+    if (list.n == 0 && !first) break;
+    const unsigned chunks = list.first[list.n];
+    int blocks = chunks < static_cast<unsigned>(most) ? static_cast<int>(chunks) : most;
+    if (blocks == 0 || std::isinf(max_norm)) blocks = 1;
+    scale_kernel<<<blocks, kThreads, 0, stream>>>(list, sums, slots, max_norm, eps,
+                                                  first ? norm_out : nullptr);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    first = false;
+  } while (i < n && !std::isinf(max_norm));
+  return cudaSuccess;
+}
+
+}  // namespace ag
