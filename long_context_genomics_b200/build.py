@@ -41,7 +41,7 @@ def build(verbose: bool = False, ptxas_v: bool = False) -> str:
     cmd = [
         NVCC, "-gencode", "arch=compute_100a,code=sm_100a", "-O3",
         "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-shared",
-        "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include"),
+        "--expt-relaxed-constexpr", "--threads", "0", "--split-compile", "0", "-I", os.path.join(ROOT, "include"),
         "-o", LIB,
     ] + [os.path.join(CSRC, s) for s in SOURCES]
     if ptxas_v:

@@ -8,37 +8,83 @@
 #include <cuda_fp16.h>
 
 #include "ag_internal.h"
+#include "sm100.cuh"
 
 namespace ag {
 
+// Phi(-|z|), the tail of the normal distribution, and exp(-z^2 / 2):
+// Abramowitz and Stegun 7.1.26 for erfc(|z| / sqrt 2) / 2, within 7e-8 (so the
+// GELU within 2.2e-7).  Two special-function instructions, shared by the GELU
+// and its derivative; erff and expf cost some 40 instructions an element, which
+// made the epilogue of a feed-forward layer slower than its product.
+struct NormalTail {
+  float tail, exp;
+};
+__device__ __forceinline__ NormalTail normal_tail(float x) {  // x = |z|
+  const float t = rcp_approx(fmaf(0.23164189f, x, 1.f));      // 0.3275911 / sqrt 2
+  NormalTail n;
+  n.exp = ex2_approx(-0.72134752f * x * x);                   // log2(e) / 2
+  float q = fmaf(0.5307027145f, t, -0.7265760135f);           // halves of the published a5 .. a1
+  q = fmaf(q, t, 0.7107068705f);
+  q = fmaf(q, t, -0.142248368f);
+  q = fmaf(q, t, 0.127414796f);
+  n.tail = q * t * n.exp;
+  return n;
+}
+__device__ __forceinline__ float logistic(float u) {
+  return rcp_approx(1.f + ex2_approx(-1.44269504f * u));
+}
+
+// Activations and their derivatives (AG_ACT_*).  In the GELU, |z| beyond 30
+// counts as 30 beside a tail that is zero there, so that an infinity gives its
+// limit.
+template <int ACT>
+__device__ __forceinline__ float act_value(float z) {
+  if constexpr (ACT == AG_ACT_RELU) return z > 0.f ? z : (z != z ? z : 0.f);
+  if constexpr (ACT == AG_ACT_GELU) {
+    const float x = fminf(fabsf(z), 30.f);
+    // z Phi(z) = max(z, 0) - |z| Phi(-|z|); z - z keeps a NaN.
+    return fmaf(-x, normal_tail(x).tail, z > 0.f ? z : (z != z ? z : 0.f));
+  }
+  if constexpr (ACT == AG_ACT_GELU_TANH)  // (1 + tanh u) / 2 is the logistic of 2u
+    return z * logistic(1.5957691f * z * fmaf(0.044715f * z, z, 1.f));
+  if constexpr (ACT == AG_ACT_SILU) return z * logistic(z);
+  return z;
+}
+template <int ACT>
+__device__ __forceinline__ float act_slope(float z) {
+  if constexpr (ACT == AG_ACT_RELU) return z > 0.f ? 1.f : 0.f;
+  if constexpr (ACT == AG_ACT_GELU) {
+    const float x = fminf(fabsf(z), 30.f);
+    const NormalTail n = normal_tail(x);
+    return fmaf(copysignf(x, z) * 0.39894228f, n.exp,
+                z > 0.f ? 1.f - n.tail : (z != z ? z : n.tail));
+  }
+  if constexpr (ACT == AG_ACT_GELU_TANH) {
+    const float p = logistic(1.5957691f * z * fmaf(0.044715f * z, z, 1.f));
+    return fmaf(z * p * (1.f - p), 1.5957691f * fmaf(0.134145f * z, z, 1.f), p);
+  }
+  if constexpr (ACT == AG_ACT_SILU) {
+    const float p = logistic(z);
+    return p * fmaf(z, 1.f - p, 1.f);
+  }
+  return 1.f;
+}
 __device__ __forceinline__ float act_value(float z, int act) {
   switch (act) {
-    case AG_ACT_RELU: return z > 0.f ? z : (z != z ? z : 0.f);
-    case AG_ACT_GELU: return 0.5f * z * (1.f + erff(z * 0.70710678f));
-    case AG_ACT_GELU_TANH: {
-      // (1 + tanh u) / 2 = 1 / (1 + exp(-2u)).
-      const float u2 = 1.5957691f * (z + 0.044715f * z * z * z);
-      return z / (1.f + __expf(-u2));
-    }
-    case AG_ACT_SILU: return z / (1.f + __expf(-z));
+    case AG_ACT_RELU: return act_value<AG_ACT_RELU>(z);
+    case AG_ACT_GELU: return act_value<AG_ACT_GELU>(z);
+    case AG_ACT_GELU_TANH: return act_value<AG_ACT_GELU_TANH>(z);
+    case AG_ACT_SILU: return act_value<AG_ACT_SILU>(z);
     default: return z;
   }
 }
-
 __device__ __forceinline__ float act_slope(float z, int act) {
   switch (act) {
-    case AG_ACT_RELU: return z > 0.f ? 1.f : 0.f;
-    case AG_ACT_GELU:
-      return 0.5f * (1.f + erff(z * 0.70710678f)) + z * 0.39894228f * __expf(-0.5f * z * z);
-    case AG_ACT_GELU_TANH: {
-      const float u2 = 1.5957691f * (z + 0.044715f * z * z * z);
-      const float p = 1.f / (1.f + __expf(-u2));
-      return p + z * p * (1.f - p) * 1.5957691f * (1.f + 0.134145f * z * z);
-    }
-    case AG_ACT_SILU: {
-      const float p = 1.f / (1.f + __expf(-z));
-      return p * (1.f + z * (1.f - p));
-    }
+    case AG_ACT_RELU: return act_slope<AG_ACT_RELU>(z);
+    case AG_ACT_GELU: return act_slope<AG_ACT_GELU>(z);
+    case AG_ACT_GELU_TANH: return act_slope<AG_ACT_GELU_TANH>(z);
+    case AG_ACT_SILU: return act_slope<AG_ACT_SILU>(z);
     default: return 1.f;
   }
 }

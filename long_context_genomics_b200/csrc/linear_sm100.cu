@@ -20,8 +20,12 @@
 // Roles per CTA: warp 0 loads, warp 1 issues the products (even CTA) or tells
 // the even CTA that this one's loads have landed (odd CTA), warps 4 to 11 take
 // over the accumulators and finish the tile.  Each of those holds 32 rows x
-// BN / 2 columns of sums in registers, turns them through shared memory 32
-// columns at a time, and applies the epilogue to whole rows' pieces.
+// BN / 2 columns of sums in registers, one row per lane.  Where every array of
+// the epilogue is one that TMA can address, a warp reads the residual (or the
+// pre-activation of a derivative) and writes the results as 32-row boxes of
+// shared memory, so that the tile's memory traffic is asynchronous and whole
+// lines; odd row strides take plain loads and stores, turned through shared
+// memory so that they are at least contiguous.
 //
 // A small C does not fill the GPU: the summed dimension is then split between
 // clusters, each writing float32 partial sums that a second kernel
@@ -47,17 +51,20 @@ static_assert(128 * kRegsLow + 256 * kRegsHigh <= kThreads * kRegsLaunch,
 
 template <int BN>
 struct Shape {
-  static constexpr int kStages = BN == 256 ? 6 : 8;
+  static constexpr int kStages = BN == 256 ? 5 : 6;
   static constexpr int kABytes = 128 * kStepBytes;
   static constexpr int kBBytes = BN / 2 * kStepBytes;
   static constexpr int kStageBytes = kABytes + kBBytes;
   static constexpr int kCols = 2 * BN;           // tensor-memory columns
 };
-constexpr int kStageOutBytes = kEpiWarps * 32 * 32 * 4;
+// Per epilogue warp: two boxes of 32 rows x 128 bytes.
+constexpr int kBoxBytes = 32 * 128;
+constexpr int kStageOutBytes = kEpiWarps * 2 * kBoxBytes;
 
 struct Barriers {
   uint64_t full[8], empty[8];
   uint64_t acc_full[2], acc_free[2];
+  uint64_t in_full[kEpiWarps][2];
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
@@ -69,15 +76,16 @@ constexpr size_t smem_bytes() {
 static_assert(smem_bytes<256>() <= 227 * 1024 && smem_bytes<128>() <= 227 * 1024, "shared memory");
 
 enum Site : unsigned {
-  kSiteLoad = 30, kSiteRelay = 31, kSiteIssue = 32, kSiteAccFree = 33, kSiteAccFull = 34
+  kSiteLoad = 30, kSiteRelay = 31, kSiteIssue = 32, kSiteAccFree = 33, kSiteAccFull = 34,
+  kSiteIn = 35
 };
 
 struct Params {
   int64_t M, N;               // rows and columns of C
   int64_t items;              // tiles x splits
   int tiles_m, tiles_n, k_tiles, splits;
-  float *partial;             // splits > 1: [splits][M][ld_partial]
-  int64_t ld_partial;
+  int boxes;                  // every array of the epilogue is TMA's to read or write
+  int wide;                   // the output is float32
   uint32_t idesc;
   unsigned *err;
   LinearEpilogue epi;
@@ -206,59 +214,258 @@ __device__ __forceinline__ void issue_role(uint8_t *ring, Barriers *bars, uint32
     if (globaltimer_ns() - t0 > kWaitLimitNs) break;
 }
 
-// 32 rows x 32 columns of sums (this lane's row in v) through the warp's part
-// of shared memory and out.  Float4 q of row r lies in slot q ^ (r % 8) of its
-// 128-byte row: neither the writes (8 lanes, 8 rows) nor the reads (4 pieces of
-// 2 rows) meet in a bank.
-template <int V>
-__device__ __forceinline__ void finish_piece(const Params &p, float *stage, int64_t row0,
-                                             int64_t col0, int split, int lane) {
-  const LinearEpilogue &e = p.epi;
-  constexpr int kLanes = 32 / V;                 // lanes per row
-  const int64_t col = col0 + (lane % kLanes) * V;
-  if (col >= p.N) return;
-  float bias[V];
+// Tensor maps of the epilogue's arrays (read when p.boxes): the output, or with
+// splits the partial sums [splits][M][N]; the residual or the pre-activation
+// that is read; the pre-activation that is written.
+struct EpiMaps {
+  CUtensorMap out, in, pre;
+};
+
+// Eight sums of a row -> the layer's eight results, in the order of the header:
+// bias, pre-activation, activation (or a derivative), residual.
+template <int ACT, bool SLOPE>
+__device__ __forceinline__ void finish8(float (&v)[8], const float (&bias)[8], const float (&in)[8],
+                                        bool residual) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) bias[i] = p.splits == 1 && e.bias ? __ldg(e.bias + col + i) : 0.f;
-#pragma unroll 1
-  for (int r = lane / kLanes; r < 32; r += 32 / kLanes) {
-    if (row0 + r >= p.M) break;
-    float v[V];
-#pragma unroll
-    for (int i = 0; i < V; i += 4) {
-      const int c = (lane % kLanes) * V + i;     // column within the piece
-      if constexpr (V == 8) {
-        const float4 f = *reinterpret_cast<const float4 *>(stage + r * 32 + (((c >> 2) ^ (r & 7)) << 2));
-        v[i] = f.x, v[i + 1] = f.y, v[i + 2] = f.z, v[i + 3] = f.w;
-      } else {
-        v[i] = stage[r * 32 + (((c >> 2) ^ (r & 7)) << 2) + (c & 3)];
-      }
+  for (int i = 0; i < 8; ++i) {
+    if constexpr (SLOPE) {
+      v[i] *= act_slope<ACT>(in[i]);
+    } else {
+      v[i] = act_value<ACT>(v[i]);
+      if (residual) v[i] += in[i];
     }
-    if (p.splits > 1)
-      store_values<V>(p.partial, (split * p.M + row0 + r) * p.ld_partial + col, AG_F32, v);
-    else
-      linear_finish<V>(e, v, bias, row0 + r, col);
   }
 }
 
-template <int BN>
-__device__ __forceinline__ void epilogue_role(float *stage, Barriers *bars, uint32_t tmem,
-                                              const Params &p, uint32_t rank, int warp, int lane,
-                                              volatile int *abort) {
+__device__ __forceinline__ uint4 pack8(const float (&v)[8], bool bf16) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (bf16) {
+      w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+    } else {
+      const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t *>(&h);
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void unpack8(uint4 u, bool bf16, float (&v)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (bf16) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    } else {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+      v[2 * i] = f.x, v[2 * i + 1] = f.y;
+    }
+  }
+}
+
+// One warp's 32 rows x COLS columns through boxes of 128-byte rows.  WIDE:
+// float32 results, 32 columns a box; otherwise 64 16-bit columns.  A box holds
+// the residual first and the results in its place after; a pre-activation has
+// the second box to itself (of 64-byte rows beside float32 results).
+template <int COLS, int ACT, bool SLOPE, bool WIDE>
+struct BoxEpilogue {
+  static constexpr int kWidth = WIDE ? 32 : 64, kPieces = COLS / kWidth;
+  const Params &p;
+  const EpiMaps *maps;
+  uint8_t *own;               // two boxes
+  uint64_t *in_full;          // their barriers
+  volatile int *abort;
+  int lane;
+  uint32_t phase = 0;         // bit b: parity of the next read of box b to wait for
+  uint32_t issued = 0;        // bit b: parity of the next read of box b to start
+  uint32_t turn = 0;          // pieces stored so far; without a pre_box() they alternate boxes
+
+  __device__ bool pre_box() const { return SLOPE || p.epi.pre_out; }
+  __device__ bool reads() const { return SLOPE || p.epi.residual; }
+  __device__ bool valid(int64_t row0, int64_t col0, int j) const {
+    return row0 < p.M && col0 + j * kWidth < p.N;
+  }
+
+  // Start reading piece j's residual or pre-activation, `ahead` pieces after
+  // the next one to be stored.  The earlier stores out of both boxes have been
+  // read out, and the box's earlier reads are ordered by the fence before those.
+  __device__ void start_read(int64_t row0, int64_t col0, int j, int ahead) {
+    if (!valid(row0, col0, j)) return;
+    const int box = pre_box() ? (SLOPE ? 1 : 0) : ((turn + ahead) & 1);
+    issued ^= 1u << box;
+    if (lane != 0) return;
+    bulk_wait_read_all();
+    mbar_arrive_expect_tx(&in_full[box], SLOPE && WIDE ? kBoxBytes / 2 : kBoxBytes);
+    tma_load_2d(own + box * kBoxBytes, &maps->in, &in_full[box], static_cast<int>(col0) + j * kWidth,
+                static_cast<int>(row0));
+  }
+  __device__ void begin(int64_t row0, int64_t col0) {
+    if (!reads()) return;
+    start_read(row0, col0, 0, 0);
+    if (!pre_box() && kPieces > 1) start_read(row0, col0, 1, 1);
+  }
+  // Every copy this warp started ends before the CTA does: its stores, and
+  // after a failure the boxes still being read.
+  __device__ void drain() {
+    if (lane == 0) {
+      for (int b = 0; b < 2; ++b) {
+        const uint64_t t0 = globaltimer_ns();
+        while (((issued ^ phase) >> b) & 1u) {
+          if (mbar_test(smem_u32(&in_full[b]), (phase >> b) & 1u)) break;
+          if (globaltimer_ns() - t0 > kWaitLimitNs) break;
+        }
+      }
+      bulk_wait_all();
+    }
+    __syncwarp();
+  }
+
+  __device__ bool finish(const float2 (&sum)[COLS / 2], int64_t row0, int64_t col0, int split) {
+    const bool bf16 = p.epi.dtype == AG_BF16, two = !pre_box(), in = reads();
+    const float *bias_p = p.splits == 1 ? p.epi.bias : nullptr;
+    const bool bias_vec = (reinterpret_cast<uintptr_t>(bias_p) & 15) == 0;
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j) {
+      if (!valid(row0, col0, j)) break;
+      const int64_t col = col0 + j * kWidth;
+      const int box = two ? (turn & 1) : 0;
+      uint8_t *y = own + box * kBoxBytes + lane * 128, *z = own + kBoxBytes;
+      if (in) {
+        const int ib = SLOPE ? 1 : box;
+        if (!mbar_wait_warp(&in_full[ib], (phase >> ib) & 1u, abort, p.err, kSiteIn)) return false;
+        phase ^= 1u << ib;  // (start_read has waited for the boxes' stores)
+      } else {
+        if (lane == 0) {
+          if (two) bulk_wait_read_but_one();
+          else bulk_wait_read_all();
+        }
+        __syncwarp();
+      }
+#pragma unroll
+      for (int g = 0; g < kWidth / 8; ++g) {
+        float v[8], b[8], x[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 s = sum[(j * kWidth + g * 8) / 2 + i];
+          v[2 * i] = s.x, v[2 * i + 1] = s.y;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) b[i] = 0.f, x[i] = 0.f;
+        if (bias_p) {
+          const int64_t c = col + g * 8;
+          if (bias_vec && c + 8 <= p.N) {
+            const float4 lo = __ldg(reinterpret_cast<const float4 *>(bias_p + c));
+            const float4 hi = __ldg(reinterpret_cast<const float4 *>(bias_p + c) + 1);
+            b[0] = lo.x, b[1] = lo.y, b[2] = lo.z, b[3] = lo.w;
+            b[4] = hi.x, b[5] = hi.y, b[6] = hi.z, b[7] = hi.w;
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (c + i < p.N) b[i] = __ldg(bias_p + c + i);
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] += b[i];
+        }
+        // 16-byte chunks of this lane's row: of 128 bytes with the 128-byte
+        // swizzle, of 64 bytes with the 64-byte one.
+        uint4 *y16 = reinterpret_cast<uint4 *>(y + ((g ^ (lane & 7)) << 4));
+        uint4 *z16 = reinterpret_cast<uint4 *>(
+            WIDE ? z + lane * 64 + ((g ^ ((lane >> 1) & 3)) << 4)
+                 : z + lane * 128 + ((g ^ (lane & 7)) << 4));
+        float4 *yw0 = reinterpret_cast<float4 *>(y + (((2 * g) ^ (lane & 7)) << 4));
+        float4 *yw1 = reinterpret_cast<float4 *>(y + (((2 * g + 1) ^ (lane & 7)) << 4));
+        if constexpr (SLOPE) {
+          unpack8(*z16, bf16, x);
+        } else {
+          if (p.epi.pre_out) *z16 = pack8(v, bf16);
+          if (in) {
+            if constexpr (WIDE) {
+              const float4 lo = *yw0, hi = *yw1;
+              x[0] = lo.x, x[1] = lo.y, x[2] = lo.z, x[3] = lo.w;
+              x[4] = hi.x, x[5] = hi.y, x[6] = hi.z, x[7] = hi.w;
+            } else {
+              unpack8(*y16, bf16, x);
+            }
+          }
+        }
+        finish8<ACT, SLOPE>(v, b, x, in);
+        if constexpr (WIDE) {
+          *yw0 = make_float4(v[0], v[1], v[2], v[3]);
+          *yw1 = make_float4(v[4], v[5], v[6], v[7]);
+        } else {
+          *y16 = pack8(v, bf16);
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        tma_store_3d(&maps->out, own + box * kBoxBytes, static_cast<int>(col),
+                     static_cast<int>(row0), split);
+        if (!SLOPE && p.epi.pre_out)
+          tma_store_3d(&maps->pre, z, static_cast<int>(col), static_cast<int>(row0), 0);
+        bulk_commit_group();
+      }
+      ++turn;
+      const int ahead = two ? 1 : 0;
+      if (in && j + 1 + ahead < kPieces) start_read(row0, col0, j + 1 + ahead, ahead);
+    }
+    return true;
+  }
+};
+
+// The same without boxes: 32 columns at a time through a box's memory (float4
+// q of row r in slot q ^ (r % 8)), then a lane per column, row by row.
+template <int COLS>
+__device__ __forceinline__ void plain_epilogue(const Params &p, const float2 (&sum)[COLS / 2],
+                                               float *stage, int64_t row0, int64_t col0, int lane) {
+#pragma unroll
+  for (int c = 0; c < COLS; c += 32) {
+    __syncwarp();
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const float2 a = sum[c / 2 + 2 * q], b = sum[c / 2 + 2 * q + 1];
+      *reinterpret_cast<float4 *>(stage + lane * 32 + ((q ^ (lane & 7)) << 2)) =
+          make_float4(a.x, a.y, b.x, b.y);
+    }
+    __syncwarp();
+    const int64_t col = col0 + c + lane;
+    if (col < p.N) {
+      const float bias[1] = {p.epi.bias ? __ldg(p.epi.bias + col) : 0.f};
+#pragma unroll 1
+      for (int r = 0; r < 32 && row0 + r < p.M; ++r) {
+        float v[1] = {stage[r * 32 + (((lane >> 2) ^ (r & 7)) << 2) + (lane & 3)]};
+        linear_finish<1>(p.epi, v, bias, row0 + r, col);
+      }
+    }
+  }
+}
+
+template <int BN, int ACT, bool SLOPE, bool WIDE, bool BOXES>
+__device__ __forceinline__ void epilogue_role(uint8_t *stage, Barriers *bars, uint32_t tmem,
+                                              const Params &p, const EpiMaps *maps, uint32_t rank,
+                                              int warp, int lane, volatile int *abort) {
   constexpr int kHalf = BN / 2;                  // columns per warp
   const int quarter = warp % 4, half = (warp - kFirstEpiWarp) / 4;
   const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
   const uint32_t free_bar = cluster_addr(&bars->acc_free[0], 0);
-  float *own = stage + (warp - kFirstEpiWarp) * 32 * 32;
+  uint8_t *own = stage + (warp - kFirstEpiWarp) * 2 * kBoxBytes;
+  BoxEpilogue<kHalf, ACT, SLOPE, WIDE> boxes{
+      p, maps, own, bars->in_full[warp - kFirstEpiWarp], abort, lane};
   uint32_t acc = 0;
-  for (int64_t i = blockIdx.x / 2; i < p.items; i += gridDim.x / 2) {
+  bool ok = true;
+  for (int64_t i = blockIdx.x / 2; ok && i < p.items; i += gridDim.x / 2) {
     const Item t = item_at(p, i);
-    float sum[kHalf];
+    const int64_t row0 = static_cast<int64_t>(t.tm) * 256 + rank * 128 + quarter * 32;
+    const int64_t col0 = static_cast<int64_t>(t.tn) * BN + kHalf * half;
+    if constexpr (BOXES) boxes.begin(row0, col0);
+    float2 sum[kHalf / 2];
 #pragma unroll
-    for (int c = 0; c < kHalf; ++c) sum[c] = 0.f;
+    for (int c = 0; c < kHalf / 2; ++c) sum[c] = make_float2(0.f, 0.f);
     for (int k0 = t.kb; k0 < t.ke; k0 += kPromote, ++acc) {
       const uint32_t b = acc & 1u;
-      if (!mbar_wait_warp(&bars->acc_full[b], (acc >> 1) & 1u, abort, p.err, kSiteAccFull)) return;
+      ok = mbar_wait_warp(&bars->acc_full[b], (acc >> 1) & 1u, abort, p.err, kSiteAccFull);
+      if (!ok) break;
       tc_fence_after();
       const uint32_t at = tmem + lanes + BN * b + kHalf * half;
 #pragma unroll
@@ -267,39 +474,34 @@ __device__ __forceinline__ void epilogue_role(float *stage, Barriers *bars, uint
         tmem_ld32(at + c, r);
         tmem_wait_ld(r);
 #pragma unroll
-        for (int q = 0; q < 32; ++q) sum[c + q] += __uint_as_float(r[q]);
+        for (int q = 0; q < 16; ++q)
+          sum[c / 2 + q] = __fadd2_rn(sum[c / 2 + q], make_float2(__uint_as_float(r[2 * q]),
+                                                                  __uint_as_float(r[2 * q + 1])));
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(free_bar + 8 * b);
     }
-    const int64_t row0 = static_cast<int64_t>(t.tm) * 256 + rank * 128 + quarter * 32;
-    const int64_t col0 = static_cast<int64_t>(t.tn) * BN + kHalf * half;
-#pragma unroll
-    for (int c = 0; c < kHalf; c += 32) {
-      __syncwarp();
-#pragma unroll
-      for (int q = 0; q < 8; ++q)
-        *reinterpret_cast<float4 *>(own + lane * 32 + ((q ^ (lane & 7)) << 2)) =
-            make_float4(sum[c + 4 * q], sum[c + 4 * q + 1], sum[c + 4 * q + 2], sum[c + 4 * q + 3]);
-      __syncwarp();
-      if (p.splits > 1 || p.epi.vec8)
-        finish_piece<8>(p, own, row0, col0 + c, t.split, lane);
-      else
-        finish_piece<1>(p, own, row0, col0 + c, t.split, lane);
+    if (!ok) break;
+    if constexpr (BOXES) {
+      ok = boxes.finish(sum, row0, col0, t.split);
+    } else {
+      plain_epilogue<kHalf>(p, sum, reinterpret_cast<float *>(own), row0, col0, lane);
     }
   }
+  if constexpr (BOXES) boxes.drain();
 }
 
-template <int BN, bool A_MN, bool B_MN>
+template <int BN, bool A_MN, bool B_MN, int ACT, bool SLOPE, bool BOXES>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     linear_gemm_kernel(const __grid_constant__ CUtensorMap ma,
-                       const __grid_constant__ CUtensorMap mb, const __grid_constant__ Params p) {
+                       const __grid_constant__ CUtensorMap mb,
+                       const __grid_constant__ EpiMaps maps, const __grid_constant__ Params p) {
   using S = Shape<BN>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  float *stage = reinterpret_cast<float *>(ring + S::kStages * S::kStageBytes);
-  Barriers *bars = reinterpret_cast<Barriers *>(reinterpret_cast<uint8_t *>(stage) + kStageOutBytes);
+  uint8_t *stage = ring + S::kStages * S::kStageBytes;
+  Barriers *bars = reinterpret_cast<Barriers *>(stage + kStageOutBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   if (threadIdx.x == 0) {
@@ -311,6 +513,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(&bars->acc_full[b], 1);
       mbar_init(&bars->acc_free[b], 2 * kEpiWarps);
     }
+    for (int w = 0; w < kEpiWarps; ++w)
+      for (int b = 0; b < 2; ++b) mbar_init(&bars->in_full[w][b], 1);
     mbar_init(&bars->drain, 1);
     bars->abort = 0;
     fence_mbar_init();
@@ -338,7 +542,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else {
     regs_inc<kRegsHigh>();
-    epilogue_role<BN>(stage, bars, tmem, p, rank, warp, lane, abort);
+    if (BOXES && p.wide)
+      epilogue_role<BN, ACT, SLOPE, true, BOXES>(stage, bars, tmem, p, &maps, rank, warp, lane,
+                                                 abort);
+    else
+      epilogue_role<BN, ACT, SLOPE, false, BOXES>(stage, bars, tmem, p, &maps, rank, warp, lane,
+                                                  abort);
   }
   __syncwarp();
   // Neither CTA leaves while the other may use its shared or tensor memory.
@@ -350,15 +559,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int BN, bool A_MN, bool B_MN>
-cudaError_t launch(const Gemm &g, const Params &p, const CUtensorMap &ma, const CUtensorMap &mb) {
+template <int BN, bool A_MN, bool B_MN, int ACT, bool SLOPE, bool BOXES>
+cudaError_t launch(const Gemm &g, const Params &p, const CUtensorMap &ma, const CUtensorMap &mb,
+                   const EpiMaps &maps) {
   static std::once_flag once[64];
   static cudaError_t once_err[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  auto *kernel = linear_gemm_kernel<BN, A_MN, B_MN>;
+  auto *kernel = linear_gemm_kernel<BN, A_MN, B_MN, ACT, SLOPE, BOXES>;
   std::call_once(once[dev], [&] {
     once_err[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(smem_bytes<BN>()));
@@ -370,21 +580,52 @@ cudaError_t launch(const Gemm &g, const Params &p, const CUtensorMap &ma, const 
   });
   if (once_err[dev] != cudaSuccess) return once_err[dev];
   const int64_t clusters = p.items < g.num_sms / 2 ? p.items : g.num_sms / 2;
-  kernel<<<static_cast<unsigned>(2 * clusters), kThreads, smem_bytes<BN>(), g.stream>>>(ma, mb, p);
+  kernel<<<static_cast<unsigned>(2 * clusters), kThreads, smem_bytes<BN>(), g.stream>>>(ma, mb, maps,
+                                                                                       p);
   return cudaGetLastError();
 }
 
-// A 16-bit operand [rows][cols] (cols dense, ld apart) as boxes of 64 columns
-// and `box_rows` rows.
-bool encode_map(const Gemm &g, CUtensorMap *m, const Operand &o, int box_rows) {
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(o.cols), static_cast<cuuint64_t>(o.rows)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(o.ld) * 2};
-  const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)};
-  const cuuint32_t step[2] = {1, 1};
-  return g.encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void *>(o.p), dims, strides, box,
-                  step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+template <int BN, bool A_MN, bool B_MN, bool SLOPE>
+cudaError_t launch_act(const Gemm &g, const Params &p, const CUtensorMap &ma, const CUtensorMap &mb,
+                       const EpiMaps &maps) {
+  // The activation is compiled into the box epilogue; the plain one looks it up.
+  // Partial sums have none yet.
+  if (!p.boxes) return launch<BN, A_MN, B_MN, AG_ACT_NONE, false, false>(g, p, ma, mb, maps);
+  if constexpr (A_MN) {
+    return launch<BN, A_MN, B_MN, AG_ACT_NONE, false, true>(g, p, ma, mb, maps);
+  } else {
+    switch (p.epi.act) {
+      case AG_ACT_RELU: return launch<BN, A_MN, B_MN, AG_ACT_RELU, SLOPE, true>(g, p, ma, mb, maps);
+      case AG_ACT_GELU: return launch<BN, A_MN, B_MN, AG_ACT_GELU, SLOPE, true>(g, p, ma, mb, maps);
+      case AG_ACT_GELU_TANH:
+        return launch<BN, A_MN, B_MN, AG_ACT_GELU_TANH, SLOPE, true>(g, p, ma, mb, maps);
+      case AG_ACT_SILU: return launch<BN, A_MN, B_MN, AG_ACT_SILU, SLOPE, true>(g, p, ma, mb, maps);
+      default: return launch<BN, A_MN, B_MN, AG_ACT_NONE, false, true>(g, p, ma, mb, maps);
+    }
+  }
+}
+
+// A matrix [parts][rows][cols] (cols dense, ld apart) in boxes of `box_rows`
+// rows x `box_cols` columns, whose rows are 64 or 128 bytes.
+bool encode_map(const Gemm &g, CUtensorMap *m, const void *at, int size, int64_t parts, int64_t rows,
+                int64_t cols, int64_t ld, int box_rows, int box_cols) {
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
+                              static_cast<cuuint64_t>(parts)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * size,
+                                 static_cast<cuuint64_t>(ld) * size * rows};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows), 1};
+  const cuuint32_t step[3] = {1, 1, 1};
+  return g.encode(m,
+                  size == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16,
+                  parts ? 3 : 2, const_cast<void *>(at), dims, strides, box, step,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  box_cols * size == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool boxable(const void *p, int64_t ld, int size) {
+  return !p || (aligned(p, 16) && ld * size % 16 == 0);
 }
 
 }  // namespace gemm
@@ -398,20 +639,43 @@ cudaError_t launch_gemm(const Gemm &g) {
   p.k_tiles = static_cast<int>((g.K + 63) / 64);
   p.splits = g.plan.splits;
   p.items = static_cast<int64_t>(p.tiles_m) * p.tiles_n * p.splits;
-  p.partial = g.partial, p.ld_partial = partial_ld(g.N);
   p.idesc = idesc_half_f32(256, g.plan.bn, g.epi.dtype == AG_BF16, g.a_mn, g.b_mn);
   p.err = g.err;
   p.epi = g.epi;
-  CUtensorMap ma, mb;
-  if (!encode_map(g, &ma, g.A, g.a_mn ? 64 : 128) ||
-      !encode_map(g, &mb, g.B, g.b_mn ? 64 : g.plan.bn / 2))
-    return cudaErrorInvalidValue;
-  if (g.plan.bn == 256) {
-    if (g.a_mn) return launch<256, true, true>(g, p, ma, mb);
-    return g.b_mn ? launch<256, false, true>(g, p, ma, mb) : launch<256, false, false>(g, p, ma, mb);
+  if (p.splits > 1) {  // plain float32 sums; linear_join_kernel does the rest
+    p.epi = LinearEpilogue{};
+    p.epi.out = g.partial, p.epi.ld_out = partial_ld(g.N);
+    p.epi.out_dtype = AG_F32, p.epi.dtype = g.epi.dtype;
   }
-  if (g.a_mn) return launch<128, true, true>(g, p, ma, mb);
-  return g.b_mn ? launch<128, false, true>(g, p, ma, mb) : launch<128, false, false>(g, p, ma, mb);
+  const LinearEpilogue &e = p.epi;
+  const int out_size = e.out_dtype == AG_F32 ? 4 : 2;
+  p.wide = e.out_dtype == AG_F32;
+  p.boxes = boxable(e.out, e.ld_out, out_size) && boxable(e.residual, e.ld_res, out_size) &&
+            boxable(e.pre_in, e.ld_pre_in, 2) && boxable(e.pre_out, e.ld_pre_out, 2);
+  CUtensorMap ma, mb;
+  EpiMaps maps{};
+  const Operand &A = g.A, &B = g.B;
+  bool ok = encode_map(g, &ma, A.p, 2, 0, A.rows, A.cols, A.ld, g.a_mn ? 64 : 128, 64) &&
+            encode_map(g, &mb, B.p, 2, 0, B.rows, B.cols, B.ld, g.b_mn ? 64 : g.plan.bn / 2, 64);
+  if (p.boxes) {
+    const int width = p.wide ? 32 : 64;
+    ok = ok && encode_map(g, &maps.out, e.out, out_size, p.splits, g.M, g.N, e.ld_out, 32, width);
+    if (e.residual)
+      ok = ok && encode_map(g, &maps.in, e.residual, out_size, 0, g.M, g.N, e.ld_res, 32, width);
+    if (e.pre_in)
+      ok = ok && encode_map(g, &maps.in, e.pre_in, 2, 0, g.M, g.N, e.ld_pre_in, 32, width);
+    if (e.pre_out)
+      ok = ok && encode_map(g, &maps.pre, e.pre_out, 2, 1, g.M, g.N, e.ld_pre_out, 32, width);
+  }
+  if (!ok) return cudaErrorInvalidValue;
+  if (g.plan.bn == 256) {
+    if (g.a_mn) return launch_act<256, true, true, false>(g, p, ma, mb, maps);
+    return g.b_mn ? launch_act<256, false, true, true>(g, p, ma, mb, maps)
+                  : launch_act<256, false, false, false>(g, p, ma, mb, maps);
+  }
+  if (g.a_mn) return launch_act<128, true, true, false>(g, p, ma, mb, maps);
+  return g.b_mn ? launch_act<128, false, true, true>(g, p, ma, mb, maps)
+                : launch_act<128, false, false, false>(g, p, ma, mb, maps);
 }
 
 }  // namespace ag
