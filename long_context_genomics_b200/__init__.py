@@ -418,7 +418,7 @@ def _code(table: dict, value, name: str) -> int:
 def _on_gpu(t, name: str, dtypes) -> None:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be on a CUDA device")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
@@ -427,7 +427,7 @@ def _on_gpu(t, name: str, dtypes) -> None:
 def _matrix(t, name: str, dtypes, rows: int, cols: int) -> int:
     """Checks a row-major matrix (its rows may be apart) and returns its row stride."""
     _on_gpu(t, name, dtypes)
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+    if t.shape != (rows, cols):
         raise ValueError(f"{name} must be [{rows},{cols}], got {list(t.shape)}")
     ld, inner = t.stride()
     if inner != 1 and cols > 1:
@@ -455,6 +455,11 @@ def _workspace(query, dev: torch.device, name: str, *args):
         return None, None, 0
     t = torch.empty(n.value, dtype=torch.uint8, device=dev)
     return t, t.data_ptr(), n.value
+
+
+def _check_status(st: int, name: str) -> None:
+    if st != AG_OK:
+        raise AgError(name, st)
 
 
 def ag_linear_fwd(x: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = None,
@@ -761,12 +766,15 @@ def ag_grad_clip(grads, max_norm: float, eps: float = 1e-6,
     if not grads:
         raise ValueError("grads has no tensor")
     for g in grads:
-        _on_gpu(g, "every gradient", DTYPES)
-        if g.layout != torch.strided or not _is_dense(g):
-            raise ValueError("every gradient must be dense")
+        if not (isinstance(g, torch.Tensor) and g.is_cuda and g.dtype in DTYPES
+                and g.layout == torch.strided and g.is_contiguous()):
+            _on_gpu(g, "every gradient", DTYPES)
+            if g.layout != torch.strided or not _is_dense(g):
+                raise ValueError("every gradient must be dense")
     n = len(grads)
     dev = grads[0].device if norm is None else _one_device(grads[0], norm)
-    _one_device(*grads)
+    if len({g.get_device() for g in grads}) > 1:
+        _one_device(*grads)
     ptrs = (ctypes.c_void_p * n)(*[g.data_ptr() for g in grads])
     counts = (ctypes.c_int64 * n)(*[g.numel() for g in grads])
     types = (ctypes.c_int * n)(*[DTYPES[g.dtype] for g in grads])

@@ -12,7 +12,7 @@ namespace ag {
 namespace {
 
 constexpr int64_t kMaxRows = int64_t(1) << 26, kMaxCols = int64_t(1) << 20,
-                  kMaxStride = int64_t(1) << 28;
+                  kMaxStride = int64_t(1) << 28, kMaxMatrix = int64_t(1) << 38;
 
 bool is_dtype(int d) { return d == AG_F32 || d == AG_BF16 || d == AG_F16; }
 int size_of(int d) { return d == AG_F32 ? 4 : 2; }
@@ -47,6 +47,9 @@ ag_status check_ld(int64_t ld, int64_t cols) {
 ag_status check_linear_sizes(int64_t M, int64_t N, int64_t K) {
   if (M < 0 || N < 1 || K < 1) return AG_ERR_SHAPE;
   if (M > kMaxRows || N > kMaxCols || K > kMaxCols) return AG_ERR_UNSUPPORTED;
+  // Keeps a product's tiles (of at least 2^15 outputs, in up to 32 splits)
+  // below 2^31; the longest sum, over M, has at most 2^20 64-deep tiles.
+  if (M * N > kMaxMatrix || M * K > kMaxMatrix || N * K > kMaxMatrix) return AG_ERR_UNSUPPORTED;
   return AG_OK;
 }
 

@@ -118,8 +118,10 @@ __global__ void __launch_bounds__(kThreads)
   // Written so that a NaN stays a NaN.
   const float c = ratio >= 1.0 ? 1.f : static_cast<float>(ratio);
   if (c == 1.f) return;
-  for (uint32_t q = blockIdx.x; q < list.first[list.n]; q += gridDim.x) {
-    const Chunk k = chunk_of(list, q);
+  // From the end: what the first pass read last is still in L2.
+  const uint32_t chunks = list.first[list.n];
+  for (uint32_t q = blockIdx.x; q < chunks; q += gridDim.x) {
+    const Chunk k = chunk_of(list, chunks - 1 - q);
     const int head = head_of(k), body = (k.len - head) / 8;
     for (int i = threadIdx.x; i < body; i += kThreads) {
       float v[8];

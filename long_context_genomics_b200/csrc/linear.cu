@@ -5,7 +5,7 @@
 //
 // The products go to the tensor cores (linear_sm100.cu), planned here; beside
 // them are the kernels that join split sums, copy operands whose rows TMA cannot
-// read, and sum dy's columns.
+// read, sum dy's columns, and multiply a few rows without the tensor cores.
 #include "ag_internal.h"
 #include "linear_epilogue.cuh"
 #include "linear_gemm.h"
@@ -66,27 +66,140 @@ __global__ void __launch_bounds__(256)
     for (int64_t c = threadIdx.x; c < cols; c += 256) to[r * ld_to + c] = from[r * ld_from + c];
 }
 
-// db[n] = sum_m dy[m, n]: 32 columns per block, 8 lanes over the rows.
+// db[n] = sum_m dy[m, n].  A block takes 32 V columns and a part of the rows:
+// lanes over the columns (V each), warps over the rows.  With one part it writes
+// db, otherwise partial sums [part][N] that column_join_kernel adds in order.
+template <int V>
 __global__ void __launch_bounds__(256)
-    column_sum_kernel(const uint16_t *__restrict__ dy, int64_t ld, int64_t M, int64_t N,
-                      int dtype, float *__restrict__ db) {
-  __shared__ float part[8][32];
-  const int c = threadIdx.x % 32, r = threadIdx.x / 32;
-  const int64_t n = static_cast<int64_t>(blockIdx.x) * 32 + c;
-  double s = 0.0;
-  if (n < N)
-    for (int64_t m = r; m < M; m += 8) {
-      float v[1];
-      load_values<1>(dy, m * ld + n, dtype, v);
-      s += v[0];
+    column_sum_kernel(const uint16_t *__restrict__ dy, int64_t ld, int64_t M, int64_t N, int dtype,
+                      int parts, float *__restrict__ out) {
+  __shared__ float part[8][32 * V];
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int64_t col = (static_cast<int64_t>(blockIdx.x) * 32 + lane) * V;
+  const int64_t from = M * blockIdx.y / parts, to = M * (blockIdx.y + 1) / parts;
+  float s[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) s[i] = 0.f;
+  if (col < N) {
+#pragma unroll 4
+    for (int64_t m = from + warp; m < to; m += 8) {
+      float v[V];
+      load_values<V>(dy, m * ld + col, dtype, v);
+#pragma unroll
+      for (int i = 0; i < V; ++i) s[i] += v[i];
     }
-  part[r][c] = static_cast<float>(s);
-  __syncthreads();
-  if (r == 0 && n < N) {
-    float t = 0.f;
-    for (int i = 0; i < 8; ++i) t += part[i][c];
-    db[n] = t;
   }
+#pragma unroll
+  for (int i = 0; i < V; ++i) part[warp][i * 32 + lane] = s[i];
+  __syncthreads();
+  if (static_cast<int>(threadIdx.x) < 32 * V) {
+    float t = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) t += part[w][threadIdx.x];
+    const int64_t n = (static_cast<int64_t>(blockIdx.x) * 32 + lane) * V + warp;
+    if (n < N) out[blockIdx.y * N + n] = t;
+  }
+}
+__global__ void __launch_bounds__(256)
+    column_join_kernel(const float *__restrict__ partial, int parts, int64_t N,
+                       float *__restrict__ db) {
+  __shared__ float sums[8][32];
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int64_t n = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+  float s = 0.f;
+  if (n < N)
+    for (int i = warp; i < parts; i += 8) s += partial[i * N + n];
+  sums[warp][lane] = s;
+  __syncthreads();
+  if (warp == 0 && n < N) {
+#pragma unroll
+    for (int w = 1; w < 8; ++w) s += sums[w][lane];
+    db[n] = s;
+  }
+}
+
+// --------------------------------------------------------------------------
+// Up to 8 rows of x: the weights' one pass through the SMs sets the time, and a
+// tile of 256 rows would be almost empty.  A warp takes kRowsW rows of W at a
+// time, its lanes 8 consecutive terms each (V == 1: one, for rows that 16-byte
+// loads cannot read), and the warps of a block first share out the summed
+// dimension, so that even a small W has all its loads in flight at once.  Each
+// block writes its outputs itself: no workspace and one launch.
+constexpr int kSkinnyRows = 8;
+constexpr int kRowsW = 4;
+
+template <int MT, int V>
+__global__ void __launch_bounds__(256)
+    linear_skinny_kernel(const uint16_t *__restrict__ x, int64_t ldx,
+                         const uint16_t *__restrict__ W, int64_t ldw, int M, int64_t N, int64_t K,
+                         int warps_k, const LinearEpilogue e) {
+  __shared__ float part[8][kRowsW * MT];
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int wk = warp % warps_k, group = warp / warps_k;
+  const int64_t n0 = (static_cast<int64_t>(blockIdx.x) * (8 / warps_k) + group) * kRowsW;
+  float acc[kRowsW][MT];
+#pragma unroll
+  for (int r = 0; r < kRowsW; ++r)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) acc[r][m] = 0.f;
+  if (n0 < N) {
+    // Rows past the last repeat it; what they give is not written.
+    const uint16_t *w_row[kRowsW], *x_row[MT];
+#pragma unroll
+    for (int r = 0; r < kRowsW; ++r) w_row[r] = W + min(n0 + r, N - 1) * ldw;
+#pragma unroll
+    for (int m = 0; m < MT; ++m) x_row[m] = x + static_cast<int64_t>(min(m, M - 1)) * ldx;
+#pragma unroll 2
+    for (int64_t k = (static_cast<int64_t>(wk) * 32 + lane) * V; k < K; k += warps_k * 32 * V) {
+      float w[kRowsW][V];
+#pragma unroll
+      for (int r = 0; r < kRowsW; ++r) load_values<V>(w_row[r], k, e.dtype, w[r]);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        float v[V];
+        load_values<V>(x_row[m], k, e.dtype, v);
+#pragma unroll
+        for (int r = 0; r < kRowsW; ++r)
+#pragma unroll
+          for (int i = 0; i < V; ++i) acc[r][m] = fmaf(w[r][i], v[i], acc[r][m]);
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < kRowsW; ++r)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      float s = acc[r][m];
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      if (lane == 0) part[warp][r * MT + m] = s;
+    }
+  __syncthreads();
+  if (wk == 0 && lane < kRowsW * MT) {
+    float v[1] = {0.f};
+    for (int i = 0; i < warps_k; ++i) v[0] += part[warp + i][lane];
+    const int64_t n = n0 + lane / MT;
+    const int m = lane % MT;
+    if (n < N && m < M) {
+      const float bias[1] = {e.bias ? e.bias[n] : 0.f};
+      linear_finish<1>(e, v, bias, m, n);
+    }
+  }
+}
+
+template <int MT>
+cudaError_t launch_skinny(const LinearFwd &a) {
+  const bool vec = a.K % 8 == 0 && a.ldx % 8 == 0 && a.ldw % 8 == 0 && aligned(a.x, 16) &&
+                   aligned(a.W, 16);
+  int warps_k = 1;
+  while (warps_k < 8 && static_cast<int64_t>(warps_k) * 32 * (vec ? 8 : 1) < a.K) warps_k *= 2;
+  const int64_t rows = static_cast<int64_t>(8 / warps_k) * kRowsW;
+  const unsigned blocks = static_cast<unsigned>((a.N + rows - 1) / rows);
+  auto *kernel = vec ? linear_skinny_kernel<MT, 8> : linear_skinny_kernel<MT, 1>;
+  kernel<<<blocks, 256, 0, a.stream>>>(static_cast<const uint16_t *>(a.x), a.ldx,
+                                       static_cast<const uint16_t *>(a.W), a.ldw,
+                                       static_cast<int>(a.M), a.N, a.K, warps_k, a.epi);
+  return cudaGetLastError();
 }
 
 // --------------------------------------------------------------------------
@@ -156,10 +269,21 @@ FwdLayout fwd_layout(const LinearFwd &a, Workspace &ws) {
   return l;
 }
 
+// In how many parts of its rows dy is summed: enough blocks for every SM, at
+// least 64 rows each.
+int column_parts(int64_t M, int64_t N, bool vec, int num_sms) {
+  const int64_t blocks = (N + (vec ? 255 : 31)) / (vec ? 256 : 32);
+  int64_t parts = (4 * num_sms + blocks - 1) / blocks;
+  if (parts > (M + 63) / 64) parts = (M + 63) / 64;
+  return static_cast<int>(parts < 1 ? 1 : parts);
+}
+
 struct BwdLayout {
   Packed dy, x, W;
   GemmPlan dx_plan, dW_plan;
-  float *partial;  // of dx, then of dW
+  float *partial;  // of dx, then of dW, then of db
+  int db_parts;
+  bool db_vec;
 };
 BwdLayout bwd_layout(const LinearBwd &a, Workspace &ws) {
   BwdLayout l{};
@@ -176,6 +300,12 @@ BwdLayout bwd_layout(const LinearBwd &a, Workspace &ws) {
     const int64_t b = partial_bytes(l.dW_plan, a.N, a.K);
     partial = b > partial ? b : partial;
   }
+  if (a.db) {
+    l.db_vec = a.N % 8 == 0 && tma_readable(a.dy, a.lddy);
+    l.db_parts = column_parts(a.M, a.N, l.db_vec, a.num_sms);
+    const int64_t b = l.db_parts > 1 ? l.db_parts * a.N * 4 : 0;
+    partial = b > partial ? b : partial;
+  }
   l.partial = static_cast<float *>(ws.take(partial));
   return l;
 }
@@ -184,12 +314,17 @@ BwdLayout bwd_layout(const LinearBwd &a, Workspace &ws) {
 
 cudaError_t linear_fwd_workspace(const LinearFwd &a, int64_t *bytes) {
   Workspace ws{nullptr};
-  fwd_layout(a, ws);
+  if (a.M > kSkinnyRows) fwd_layout(a, ws);
   *bytes = ws.used;
   return cudaSuccess;
 }
 
 cudaError_t launch_linear_fwd(const LinearFwd &a) {
+  if (a.M <= kSkinnyRows)
+    return a.M == 1   ? launch_skinny<1>(a)
+           : a.M == 2 ? launch_skinny<2>(a)
+           : a.M <= 4 ? launch_skinny<4>(a)
+                      : launch_skinny<8>(a);
   Workspace ws{static_cast<char *>(a.workspace)};
   const FwdLayout l = fwd_layout(a, ws);
   cudaError_t e = fill(l.x, a.x, a.ldx, a.num_sms, a.stream);
@@ -224,9 +359,18 @@ cudaError_t launch_linear_bwd(const LinearBwd &a) {
     e = run(g);
   }
   if (e == cudaSuccess && a.db) {
-    column_sum_kernel<<<static_cast<unsigned>((a.N + 31) / 32), 256, 0, a.stream>>>(
-        static_cast<const uint16_t *>(a.dy), a.lddy, a.M, a.N, a.dx.dtype, a.db);
+    const int cols = l.db_vec ? 256 : 32;
+    const dim3 grid(static_cast<unsigned>((a.N + cols - 1) / cols), l.db_parts);
+    float *to = l.db_parts > 1 ? l.partial : a.db;
+    auto *kernel = l.db_vec ? column_sum_kernel<8> : column_sum_kernel<1>;
+    kernel<<<grid, 256, 0, a.stream>>>(static_cast<const uint16_t *>(a.dy), a.lddy, a.M, a.N,
+                                       a.dx.dtype, l.db_parts, to);
     e = cudaGetLastError();
+    if (e == cudaSuccess && l.db_parts > 1) {
+      column_join_kernel<<<static_cast<unsigned>((a.N + 31) / 32), 256, 0, a.stream>>>(
+          l.partial, l.db_parts, a.N, a.db);
+      e = cudaGetLastError();
+    }
   }
   return e;
 }

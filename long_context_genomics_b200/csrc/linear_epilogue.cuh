@@ -12,64 +12,89 @@
 
 namespace ag {
 
+__device__ __forceinline__ float2 both(float c) { return make_float2(c, c); }
+
+// Activations and their derivatives (AG_ACT_*) of two values at a time, in the
+// two-lane float32 instructions.
+//
 // Phi(-|z|), the tail of the normal distribution, and exp(-z^2 / 2):
 // Abramowitz and Stegun 7.1.26 for erfc(|z| / sqrt 2) / 2, within 7e-8 (so the
 // GELU within 2.2e-7).  Two special-function instructions, shared by the GELU
 // and its derivative; erff and expf cost some 40 instructions an element, which
 // made the epilogue of a feed-forward layer slower than its product.
 struct NormalTail {
-  float tail, exp;
+  float2 tail, exp;
 };
-__device__ __forceinline__ NormalTail normal_tail(float x) {  // x = |z|
-  const float t = rcp_approx(fmaf(0.23164189f, x, 1.f));      // 0.3275911 / sqrt 2
+__device__ __forceinline__ NormalTail normal_tail(float2 x) {   // x = |z|
+  const float2 d = __ffma2_rn(both(0.23164189f), x, both(1.f));  // 0.3275911 / sqrt 2
+  const float2 t = make_float2(rcp_approx(d.x), rcp_approx(d.y));
+  const float2 h = __fmul2_rn(__fmul2_rn(both(-0.72134752f), x), x);  // log2(e) / 2
   NormalTail n;
-  n.exp = ex2_approx(-0.72134752f * x * x);                   // log2(e) / 2
-  float q = fmaf(0.5307027145f, t, -0.7265760135f);           // halves of the published a5 .. a1
-  q = fmaf(q, t, 0.7107068705f);
-  q = fmaf(q, t, -0.142248368f);
-  q = fmaf(q, t, 0.127414796f);
-  n.tail = q * t * n.exp;
+  n.exp = make_float2(ex2_approx(h.x), ex2_approx(h.y));
+  float2 q = __ffma2_rn(both(0.5307027145f), t, both(-0.7265760135f));  // halves of a5 .. a1
+  q = __ffma2_rn(q, t, both(0.7107068705f));
+  q = __ffma2_rn(q, t, both(-0.142248368f));
+  q = __ffma2_rn(q, t, both(0.127414796f));
+  n.tail = __fmul2_rn(__fmul2_rn(q, t), n.exp);
   return n;
 }
-__device__ __forceinline__ float logistic(float u) {
-  return rcp_approx(1.f + ex2_approx(-1.44269504f * u));
+// 1 / (1 + 2^u).
+__device__ __forceinline__ float2 logistic2(float2 u) {
+  const float2 d = __fadd2_rn(make_float2(ex2_approx(u.x), ex2_approx(u.y)), both(1.f));
+  return make_float2(rcp_approx(d.x), rcp_approx(d.y));
+}
+// -2 log2(e) sqrt(2 / pi) (z + 0.044715 z^3): (1 + tanh) / 2 = logistic2 of it.
+__device__ __forceinline__ float2 tanh_argument(float2 z) {
+  const float2 w = __ffma2_rn(__fmul2_rn(both(-0.10294324f), z), z, both(-2.3022082f));
+  return __fmul2_rn(w, z);
 }
 
-// Activations and their derivatives (AG_ACT_*).  In the GELU, |z| beyond 30
-// counts as 30 beside a tail that is zero there, so that an infinity gives its
-// limit.
 template <int ACT>
-__device__ __forceinline__ float act_value(float z) {
-  if constexpr (ACT == AG_ACT_RELU) return z > 0.f ? z : (z != z ? z : 0.f);
+__device__ __forceinline__ float2 act_value2(float2 z) {
+  if constexpr (ACT == AG_ACT_RELU)
+    return make_float2(z.x > 0.f ? z.x : (z.x != z.x ? z.x : 0.f),
+                       z.y > 0.f ? z.y : (z.y != z.y ? z.y : 0.f));
   if constexpr (ACT == AG_ACT_GELU) {
-    const float x = fminf(fabsf(z), 30.f);
-    // z Phi(z) = max(z, 0) - |z| Phi(-|z|); z - z keeps a NaN.
-    return fmaf(-x, normal_tail(x).tail, z > 0.f ? z : (z != z ? z : 0.f));
+    // z Phi(z) = max(z, 0) - |z| Phi(-|z|).  The factor |z| stops at 30, where
+    // the tail is zero, so that an infinity gives its limit; a NaN comes
+    // through the tail.
+    const float2 x = make_float2(fabsf(z.x), fabsf(z.y));
+    return __ffma2_rn(make_float2(-fminf(x.x, 30.f), -fminf(x.y, 30.f)), normal_tail(x).tail,
+                      make_float2(fmaxf(z.x, 0.f), fmaxf(z.y, 0.f)));
   }
-  if constexpr (ACT == AG_ACT_GELU_TANH)  // (1 + tanh u) / 2 is the logistic of 2u
-    return z * logistic(1.5957691f * z * fmaf(0.044715f * z, z, 1.f));
-  if constexpr (ACT == AG_ACT_SILU) return z * logistic(z);
+  if constexpr (ACT == AG_ACT_GELU_TANH) return __fmul2_rn(z, logistic2(tanh_argument(z)));
+  if constexpr (ACT == AG_ACT_SILU)
+    return __fmul2_rn(z, logistic2(__fmul2_rn(both(-1.44269504f), z)));
   return z;
 }
 template <int ACT>
-__device__ __forceinline__ float act_slope(float z) {
-  if constexpr (ACT == AG_ACT_RELU) return z > 0.f ? 1.f : 0.f;
+__device__ __forceinline__ float2 act_slope2(float2 z) {
+  if constexpr (ACT == AG_ACT_RELU) return make_float2(z.x > 0.f ? 1.f : 0.f, z.y > 0.f ? 1.f : 0.f);
   if constexpr (ACT == AG_ACT_GELU) {
-    const float x = fminf(fabsf(z), 30.f);
+    const float2 x = make_float2(fabsf(z.x), fabsf(z.y));
     const NormalTail n = normal_tail(x);
-    return fmaf(copysignf(x, z) * 0.39894228f, n.exp,
-                z > 0.f ? 1.f - n.tail : (z != z ? z : n.tail));
+    const float2 c = make_float2(copysignf(fminf(x.x, 30.f), z.x), copysignf(fminf(x.y, 30.f), z.y));
+    return __ffma2_rn(__fmul2_rn(both(0.39894228f), c), n.exp,
+                      make_float2(z.x > 0.f ? 1.f - n.tail.x : n.tail.x,
+                                  z.y > 0.f ? 1.f - n.tail.y : n.tail.y));
   }
   if constexpr (ACT == AG_ACT_GELU_TANH) {
-    const float p = logistic(1.5957691f * z * fmaf(0.044715f * z, z, 1.f));
-    return fmaf(z * p * (1.f - p), 1.5957691f * fmaf(0.134145f * z, z, 1.f), p);
+    const float2 p = logistic2(tanh_argument(z));
+    const float2 r = __ffma2_rn(make_float2(-p.x, -p.y), p, p);  // p (1 - p)
+    const float2 k = __ffma2_rn(__fmul2_rn(both(0.21406850f), z), z, both(1.5957691f));
+    return __ffma2_rn(__fmul2_rn(z, r), k, p);
   }
   if constexpr (ACT == AG_ACT_SILU) {
-    const float p = logistic(z);
-    return p * fmaf(z, 1.f - p, 1.f);
+    const float2 p = logistic2(__fmul2_rn(both(-1.44269504f), z));
+    const float2 r = __ffma2_rn(make_float2(-p.x, -p.y), p, p);
+    return __ffma2_rn(z, r, p);
   }
-  return 1.f;
+  return both(1.f);
 }
+template <int ACT>
+__device__ __forceinline__ float act_value(float z) { return act_value2<ACT>(both(z)).x; }
+template <int ACT>
+__device__ __forceinline__ float act_slope(float z) { return act_slope2<ACT>(both(z)).x; }
 __device__ __forceinline__ float act_value(float z, int act) {
   switch (act) {
     case AG_ACT_RELU: return act_value<AG_ACT_RELU>(z);

@@ -17,10 +17,11 @@
 // with the next 512 terms meanwhile, so this costs no time: the same path also
 // overlaps one tile's epilogue with the next tile's products.
 //
-// Roles per CTA: warp 0 loads, warp 1 issues the products (even CTA) or tells
-// the even CTA that this one's loads have landed (odd CTA), warps 4 to 11 take
-// over the accumulators and finish the tile.  Each of those holds 32 rows x
-// BN / 2 columns of sums in registers, one row per lane.  Where every array of
+// Roles per CTA: warp 0 loads, warp 1 of the even CTA issues the products (both
+// CTAs' loads count on its barriers), warps 4 to 19 take over the accumulators and finish the tile (with eight such warps instead of
+// sixteen their latencies, not the products, set the pace: 142 us against
+// TIME_HERE us for 16384 x 4096 x 1024 with a GELU).  Each of those holds 32 rows x
+// BN / 4 columns of sums in registers, one row per lane.  Where every array of
 // the epilogue is one that TMA can address, a warp reads the residual (or the
 // pre-activation of a derivative) and writes the results as 32-row boxes of
 // shared memory, so that the tile's memory traffic is asynchronous and whole
@@ -40,13 +41,13 @@
 namespace ag {
 namespace gemm {
 
-constexpr int kThreads = 384;
-constexpr int kEpiWarps = 8;
+constexpr int kThreads = 640;
+constexpr int kEpiWarps = 16;
 constexpr int kFirstEpiWarp = 4;
 constexpr int kStepBytes = 128;                  // 64 16-bit terms
 constexpr int kPromote = 8;                      // k tiles per accumulator: 512 terms
-constexpr uint32_t kRegsLaunch = 168, kRegsLow = 72, kRegsHigh = 216;
-static_assert(128 * kRegsLow + 256 * kRegsHigh <= kThreads * kRegsLaunch,
+constexpr uint32_t kRegsLaunch = 96, kRegsLow = 56, kRegsHigh = 104;
+static_assert(128 * kRegsLow + 32 * kEpiWarps * kRegsHigh <= kThreads * kRegsLaunch,
               "the epilogue's registers come out of the role warps' release");
 
 template <int BN>
@@ -57,14 +58,14 @@ struct Shape {
   static constexpr int kStageBytes = kABytes + kBBytes;
   static constexpr int kCols = 2 * BN;           // tensor-memory columns
 };
-// Per epilogue warp: two boxes of 32 rows x 128 bytes.
+// Per epilogue warp: a box of 32 rows x 128 bytes.
 constexpr int kBoxBytes = 32 * 128;
-constexpr int kStageOutBytes = kEpiWarps * 2 * kBoxBytes;
+constexpr int kStageOutBytes = kEpiWarps * kBoxBytes;
 
 struct Barriers {
   uint64_t full[8], empty[8];
   uint64_t acc_full[2], acc_free[2];
-  uint64_t in_full[kEpiWarps][2];
+  uint64_t in_full[kEpiWarps];
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
@@ -76,13 +77,13 @@ constexpr size_t smem_bytes() {
 static_assert(smem_bytes<256>() <= 227 * 1024 && smem_bytes<128>() <= 227 * 1024, "shared memory");
 
 enum Site : unsigned {
-  kSiteLoad = 30, kSiteRelay = 31, kSiteIssue = 32, kSiteAccFree = 33, kSiteAccFull = 34,
+  kSiteLoad = 30, kSiteIssue = 32, kSiteAccFree = 33, kSiteAccFull = 34,
   kSiteIn = 35
 };
 
 struct Params {
   int64_t M, N;               // rows and columns of C
-  int64_t items;              // tiles x splits
+  int items;                  // tiles x splits (below 2^31: see check_linear_sizes)
   int tiles_m, tiles_n, k_tiles, splits;
   int boxes;                  // every array of the epilogue is TMA's to read or write
   int wide;                   // the output is float32
@@ -91,34 +92,37 @@ struct Params {
   LinearEpilogue epi;
 };
 
-// Work item -> tile and range of k tiles.  Tiles along M come first, so that
-// the clusters at work share B's tiles and pass over A together.
+// Work item -> tile and range of k tiles.  Tiles go in groups of 8 along M, a
+// group's tiles along M first: the clusters at work then cover about 8 x 9
+// tiles, so that what they read between them stays in L2.
 struct Item {
   int tm, tn, split, kb, ke;
 };
-__device__ __forceinline__ Item item_at(const Params &p, int64_t i) {
+constexpr int kGroup = 8;
+__device__ __forceinline__ Item item_at(const Params &p, int i) {
   Item t;
-  const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
-  t.split = static_cast<int>(i / tiles);
-  const int64_t r = i - t.split * tiles;
-  t.tn = static_cast<int>(r / p.tiles_m);
-  t.tm = static_cast<int>(r - static_cast<int64_t>(t.tn) * p.tiles_m);
-  t.kb = static_cast<int>(static_cast<int64_t>(p.k_tiles) * t.split / p.splits);
-  t.ke = static_cast<int>(static_cast<int64_t>(p.k_tiles) * (t.split + 1) / p.splits);
+  const int tiles = p.tiles_m * p.tiles_n, per_group = kGroup * p.tiles_n;
+  t.split = i / tiles;
+  const int r = i - t.split * tiles, group = r / per_group;
+  const int rest = r - group * per_group, high = min(kGroup, p.tiles_m - group * kGroup);
+  t.tn = rest / high;
+  t.tm = group * kGroup + rest - t.tn * high;
+  t.kb = p.k_tiles * t.split / p.splits;  // k_tiles <= 2^20, splits <= 32
+  t.ke = p.k_tiles * (t.split + 1) / p.splits;
   return t;
 }
 
 // One 64-deep tile of `rows` rows of an operand: K-major, one box of 64 terms
 // x rows; MN-major, boxes of 64 rows x 64 terms.
 template <bool MN, int ROWS>
-__device__ __forceinline__ void load_tile(uint8_t *dst, const CUtensorMap *map, uint64_t *bar,
+__device__ __forceinline__ void load_tile(uint8_t *dst, const CUtensorMap *map, uint32_t bar,
                                           int row, int k) {
   if constexpr (MN) {
 #pragma unroll
     for (int q = 0; q < ROWS / 64; ++q)
-      tma_load_2d(dst + q * 64 * kStepBytes, map, bar, row + 64 * q, k);
+      tma_load_2d_pair(dst + q * 64 * kStepBytes, map, bar, row + 64 * q, k);
   } else {
-    tma_load_2d(dst, map, bar, k, row);
+    tma_load_2d_pair(dst, map, bar, k, row);
   }
 }
 
@@ -127,9 +131,10 @@ __device__ __forceinline__ void load_role(const CUtensorMap *ma, const CUtensorM
                                           uint8_t *ring, Barriers *bars, const Params &p,
                                           uint32_t rank, volatile int *abort) {
   using S = Shape<BN>;
+  const uint32_t full0 = cluster_addr(&bars->full[0], 0);
   uint32_t n = 0;
   bool ok = true;
-  for (int64_t i = blockIdx.x / 2; ok && i < p.items; i += gridDim.x / 2) {
+  for (int i = blockIdx.x / 2; ok && i < p.items; i += gridDim.x / 2) {
     const Item t = item_at(p, i);
     const int row_a = t.tm * 256 + static_cast<int>(rank) * 128;
     const int row_b = t.tn * BN + static_cast<int>(rank) * (BN / 2);
@@ -138,32 +143,28 @@ __device__ __forceinline__ void load_role(const CUtensorMap *ma, const CUtensorM
       ok = mbar_wait(&bars->empty[s], ((n / S::kStages) & 1u) ^ 1u, abort, p.err, kSiteLoad);
       if (!ok) break;
       uint8_t *at = ring + s * S::kStageBytes;
-      mbar_arrive_expect_tx(&bars->full[s], S::kStageBytes);
-      load_tile<A_MN, 128>(at, ma, &bars->full[s], row_a, k * 64);
-      load_tile<B_MN, BN / 2>(at + S::kABytes, mb, &bars->full[s], row_b, k * 64);
+      // Both CTAs' bytes count on the even CTA's barrier.  The odd CTA's may
+      // come first: the phase cannot end before the even CTA's arrival.
+      const uint32_t bar = full0 + 8 * s;
+      if (rank == 0) mbar_arrive_expect_tx(&bars->full[s], 2 * S::kStageBytes);
+      load_tile<A_MN, 128>(at, ma, bar, row_a, k * 64);
+      load_tile<B_MN, BN / 2>(at + S::kABytes, mb, bar, row_b, k * 64);
       ++n;
     }
   }
-  // Every copy this thread started lands before the CTA exits.
-  for (uint32_t i = n > S::kStages ? n - S::kStages : 0; i < n; ++i) {
-    const uint32_t a = smem_u32(&bars->full[i % S::kStages]);
-    const uint64_t t0 = globaltimer_ns();
-    while (!mbar_test(a, (i / S::kStages) & 1u))
-      if (globaltimer_ns() - t0 > kWaitLimitNs) break;
-  }
-}
-
-template <int BN>
-__device__ __forceinline__ void relay_role(Barriers *bars, const Params &p, volatile int *abort) {
-  using S = Shape<BN>;
-  uint32_t n = 0;
-  for (int64_t i = blockIdx.x / 2; i < p.items; i += gridDim.x / 2) {
-    const Item t = item_at(p, i);
-    for (int k = t.kb; k < t.ke; ++k, ++n) {
-      const uint32_t s = n % S::kStages;
-      if (!mbar_wait(&bars->full[s], (n / S::kStages) & 1u, abort, p.err, kSiteRelay)) return;
-      mbar_arrive_cluster(cluster_addr(&bars->full[s], 0));
+  // Every copy of the pair lands before its CTAs exit: the products wait for
+  // all of them, so only after a failure may some be on their way.
+  if (ok) return;
+  if (rank == 0) {
+    for (uint32_t i = n > S::kStages ? n - S::kStages : 0; i < n; ++i) {
+      const uint32_t a = smem_u32(&bars->full[i % S::kStages]);
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_test(a, (i / S::kStages) & 1u))
+        if (globaltimer_ns() - t0 > kWaitLimitNs) break;
     }
+  }
+  const uint64_t t0 = globaltimer_ns();  // loads that the even CTA never counted
+  while (globaltimer_ns() - t0 < kWaitLimitNs / 1000) {
   }
 }
 
@@ -179,7 +180,7 @@ __device__ __forceinline__ void issue_role(uint8_t *ring, Barriers *bars, uint32
   constexpr uint32_t kBStep = (B_MN ? 16 * kStepBytes : 32) >> 4;
   uint32_t n = 0, acc = 0;
   bool ok = true;
-  for (int64_t i = blockIdx.x / 2; ok && i < p.items; i += gridDim.x / 2) {
+  for (int i = blockIdx.x / 2; ok && i < p.items; i += gridDim.x / 2) {
     const Item t = item_at(p, i);
     for (int k0 = t.kb; ok && k0 < t.ke; k0 += kPromote, ++acc) {
       const uint32_t b = acc & 1u, use = acc >> 1;
@@ -221,198 +222,179 @@ struct EpiMaps {
   CUtensorMap out, in, pre;
 };
 
-// Eight sums of a row -> the layer's eight results, in the order of the header:
-// bias, pre-activation, activation (or a derivative), residual.
-template <int ACT, bool SLOPE>
-__device__ __forceinline__ void finish8(float (&v)[8], const float (&bias)[8], const float (&in)[8],
-                                        bool residual) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if constexpr (SLOPE) {
-      v[i] *= act_slope<ACT>(in[i]);
-    } else {
-      v[i] = act_value<ACT>(v[i]);
-      if (residual) v[i] += in[i];
-    }
-  }
+__device__ __forceinline__ uint32_t pack2(float2 v, bool bf16) {
+  if (bf16) return pack_bf16x2(v.x, v.y);
+  const __half2 h = __floats2half2_rn(v.x, v.y);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ float2 unpack2(uint32_t w, bool bf16) {
+  if (bf16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  return __half22float2(*reinterpret_cast<const __half2 *>(&w));
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&v)[8], bool bf16) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (bf16) {
-      w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
-    } else {
-      const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t *>(&h);
-    }
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-__device__ __forceinline__ void unpack8(uint4 u, bool bf16, float (&v)[8]) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (bf16) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    } else {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
-      v[2 * i] = f.x, v[2 * i + 1] = f.y;
-    }
-  }
-}
-
-// One warp's 32 rows x COLS columns through boxes of 128-byte rows.  WIDE:
-// float32 results, 32 columns a box; otherwise 64 16-bit columns.  A box holds
-// the residual first and the results in its place after; a pre-activation has
-// the second box to itself (of 64-byte rows beside float32 results).
+// One warp's 32 rows x COLS columns through its box, kWidth columns at a time:
+// the residual or the pre-activation is read into the box while the products
+// run, each lane replaces its row's values by the results, and the box is
+// stored.  (A pre-activation to be written goes through the box before.)
+// WIDE: float32 results.
 template <int COLS, int ACT, bool SLOPE, bool WIDE>
 struct BoxEpilogue {
-  static constexpr int kWidth = WIDE ? 32 : 64, kPieces = COLS / kWidth;
+  static constexpr int kWidth = WIDE ? 32 : COLS, kPieces = COLS / kWidth;
+  static constexpr int kRow = kWidth * (WIDE ? 4 : 2), kPreRow = kWidth * 2;  // bytes
+  static_assert(kRow == 128 || kRow == 64, "a box row is a swizzle span");
   const Params &p;
   const EpiMaps *maps;
-  uint8_t *own;               // two boxes
-  uint64_t *in_full;          // their barriers
+  uint8_t *own;
+  uint64_t *in_full;
   volatile int *abort;
   int lane;
-  uint32_t phase = 0;         // bit b: parity of the next read of box b to wait for
-  uint32_t issued = 0;        // bit b: parity of the next read of box b to start
-  uint32_t turn = 0;          // pieces stored so far; without a pre_box() they alternate boxes
+  uint32_t started = 0, waited = 0;  // reads into the box
 
-  __device__ bool pre_box() const { return SLOPE || p.epi.pre_out; }
+  __device__ bool writes_pre() const { return !SLOPE && p.epi.pre_out; }
   __device__ bool reads() const { return SLOPE || p.epi.residual; }
   __device__ bool valid(int64_t row0, int64_t col0, int j) const {
     return row0 < p.M && col0 + j * kWidth < p.N;
   }
-
-  // Start reading piece j's residual or pre-activation, `ahead` pieces after
-  // the next one to be stored.  The earlier stores out of both boxes have been
-  // read out, and the box's earlier reads are ordered by the fence before those.
-  __device__ void start_read(int64_t row0, int64_t col0, int j, int ahead) {
+  // 16-byte chunk c of this lane's row, as TMA's swizzle places it.
+  template <int ROW>
+  __device__ uint4 *chunk(int c) const {
+    const int s = ROW == 128 ? c ^ (lane & 7) : c ^ ((lane >> 1) & 3);
+    return reinterpret_cast<uint4 *>(own + lane * ROW + (s << 4));
+  }
+  __device__ void box_free() const {
+    if (lane == 0) bulk_wait_read_all();
+    __syncwarp();
+  }
+  __device__ void store(const CUtensorMap *map, int64_t row0, int64_t col, int part) const {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      tma_store_3d(map, own, static_cast<int>(col), static_cast<int>(row0), part);
+      bulk_commit_group();
+    }
+  }
+  // The box's earlier stores have been read out; its earlier reads by the lanes
+  // are ordered by the fence before those stores.
+  __device__ void start_read(int64_t row0, int64_t col0, int j) {
     if (!valid(row0, col0, j)) return;
-    const int box = pre_box() ? (SLOPE ? 1 : 0) : ((turn + ahead) & 1);
-    issued ^= 1u << box;
+    ++started;
     if (lane != 0) return;
     bulk_wait_read_all();
-    mbar_arrive_expect_tx(&in_full[box], SLOPE && WIDE ? kBoxBytes / 2 : kBoxBytes);
-    tma_load_2d(own + box * kBoxBytes, &maps->in, &in_full[box], static_cast<int>(col0) + j * kWidth,
+    mbar_arrive_expect_tx(in_full, 32 * (SLOPE ? kPreRow : kRow));
+    tma_load_2d(own, &maps->in, in_full, static_cast<int>(col0) + j * kWidth,
                 static_cast<int>(row0));
   }
   __device__ void begin(int64_t row0, int64_t col0) {
-    if (!reads()) return;
-    start_read(row0, col0, 0, 0);
-    if (!pre_box() && kPieces > 1) start_read(row0, col0, 1, 1);
+    if (reads() && !writes_pre()) start_read(row0, col0, 0);
   }
-  // Every copy this warp started ends before the CTA does: its stores, and
-  // after a failure the boxes still being read.
-  __device__ void drain() {
+  // Every copy this warp started ends before the CTA does.
+  __device__ void drain() const {
     if (lane == 0) {
-      for (int b = 0; b < 2; ++b) {
-        const uint64_t t0 = globaltimer_ns();
-        while (((issued ^ phase) >> b) & 1u) {
-          if (mbar_test(smem_u32(&in_full[b]), (phase >> b) & 1u)) break;
-          if (globaltimer_ns() - t0 > kWaitLimitNs) break;
-        }
-      }
+      const uint64_t t0 = globaltimer_ns();
+      while (started != waited && !mbar_test(smem_u32(in_full), waited & 1u))
+        if (globaltimer_ns() - t0 > kWaitLimitNs) break;
       bulk_wait_all();
     }
     __syncwarp();
   }
 
-  __device__ bool finish(const float2 (&sum)[COLS / 2], int64_t row0, int64_t col0, int split) {
-    const bool bf16 = p.epi.dtype == AG_BF16, two = !pre_box(), in = reads();
-    const float *bias_p = p.splits == 1 ? p.epi.bias : nullptr;
-    const bool bias_vec = (reinterpret_cast<uintptr_t>(bias_p) & 15) == 0;
+  __device__ bool finish(const float2 (&sum)[COLS / 2], int64_t row0, int64_t col0, int part) {
+    const bool bf16 = p.epi.dtype == AG_BF16;
 #pragma unroll
     for (int j = 0; j < kPieces; ++j) {
       if (!valid(row0, col0, j)) break;
       const int64_t col = col0 + j * kWidth;
-      const int box = two ? (turn & 1) : 0;
-      uint8_t *y = own + box * kBoxBytes + lane * 128, *z = own + kBoxBytes;
-      if (in) {
-        const int ib = SLOPE ? 1 : box;
-        if (!mbar_wait_warp(&in_full[ib], (phase >> ib) & 1u, abort, p.err, kSiteIn)) return false;
-        phase ^= 1u << ib;  // (start_read has waited for the boxes' stores)
-      } else {
-        if (lane == 0) {
-          if (two) bulk_wait_read_but_one();
-          else bulk_wait_read_all();
+      const float2 *s = sum + j * kWidth / 2;
+      if (writes_pre()) {
+        box_free();
+#pragma unroll
+        for (int c = 0; c < kWidth / 8; ++c)
+          *chunk<kPreRow>(c) = make_uint4(pack2(s[4 * c], bf16), pack2(s[4 * c + 1], bf16),
+                                          pack2(s[4 * c + 2], bf16), pack2(s[4 * c + 3], bf16));
+        store(&maps->pre, row0, col, 0);
+        if (reads()) start_read(row0, col0, j);
+      }
+      uint4 pre[kPreRow / 16];
+      if (reads()) {
+        if (!mbar_wait_warp(in_full, waited & 1u, abort, p.err, kSiteIn)) return false;
+        ++waited;
+        if constexpr (SLOPE && kRow != kPreRow) {
+          // Rows of another length: all are read before any is replaced.
+#pragma unroll
+          for (int c = 0; c < kPreRow / 16; ++c) pre[c] = *chunk<kPreRow>(c);
+          __syncwarp();
         }
-        __syncwarp();
+      } else {
+        box_free();
       }
 #pragma unroll
-      for (int g = 0; g < kWidth / 8; ++g) {
-        float v[8], b[8], x[8];
+      for (int c = 0; c < kRow / 16; ++c) {
+        if constexpr (WIDE) {
+          float2 v[2] = {s[2 * c], s[2 * c + 1]};
+          if constexpr (SLOPE) {
+            const uint32_t w[2] = {c & 1 ? pre[c / 2].z : pre[c / 2].x,
+                                   c & 1 ? pre[c / 2].w : pre[c / 2].y};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 s = sum[(j * kWidth + g * 8) / 2 + i];
-          v[2 * i] = s.x, v[2 * i + 1] = s.y;
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) b[i] = 0.f, x[i] = 0.f;
-        if (bias_p) {
-          const int64_t c = col + g * 8;
-          if (bias_vec && c + 8 <= p.N) {
-            const float4 lo = __ldg(reinterpret_cast<const float4 *>(bias_p + c));
-            const float4 hi = __ldg(reinterpret_cast<const float4 *>(bias_p + c) + 1);
-            b[0] = lo.x, b[1] = lo.y, b[2] = lo.z, b[3] = lo.w;
-            b[4] = hi.x, b[5] = hi.y, b[6] = hi.z, b[7] = hi.w;
+            for (int i = 0; i < 2; ++i) v[i] = __fmul2_rn(v[i], act_slope2<ACT>(unpack2(w[i], bf16)));
           } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (c + i < p.N) b[i] = __ldg(bias_p + c + i);
-          }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] += b[i];
-        }
-        // 16-byte chunks of this lane's row: of 128 bytes with the 128-byte
-        // swizzle, of 64 bytes with the 64-byte one.
-        uint4 *y16 = reinterpret_cast<uint4 *>(y + ((g ^ (lane & 7)) << 4));
-        uint4 *z16 = reinterpret_cast<uint4 *>(
-            WIDE ? z + lane * 64 + ((g ^ ((lane >> 1) & 3)) << 4)
-                 : z + lane * 128 + ((g ^ (lane & 7)) << 4));
-        float4 *yw0 = reinterpret_cast<float4 *>(y + (((2 * g) ^ (lane & 7)) << 4));
-        float4 *yw1 = reinterpret_cast<float4 *>(y + (((2 * g + 1) ^ (lane & 7)) << 4));
-        if constexpr (SLOPE) {
-          unpack8(*z16, bf16, x);
-        } else {
-          if (p.epi.pre_out) *z16 = pack8(v, bf16);
-          if (in) {
-            if constexpr (WIDE) {
-              const float4 lo = *yw0, hi = *yw1;
-              x[0] = lo.x, x[1] = lo.y, x[2] = lo.z, x[3] = lo.w;
-              x[4] = hi.x, x[5] = hi.y, x[6] = hi.z, x[7] = hi.w;
-            } else {
-              unpack8(*y16, bf16, x);
+            for (int i = 0; i < 2; ++i) v[i] = act_value2<ACT>(v[i]);
+            if (p.epi.residual) {
+              const float4 r = *reinterpret_cast<const float4 *>(chunk<kRow>(c));
+              v[0] = __fadd2_rn(v[0], make_float2(r.x, r.y));
+              v[1] = __fadd2_rn(v[1], make_float2(r.z, r.w));
             }
           }
-        }
-        finish8<ACT, SLOPE>(v, b, x, in);
-        if constexpr (WIDE) {
-          *yw0 = make_float4(v[0], v[1], v[2], v[3]);
-          *yw1 = make_float4(v[4], v[5], v[6], v[7]);
+          *reinterpret_cast<float4 *>(chunk<kRow>(c)) = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
         } else {
-          *y16 = pack8(v, bf16);
+          uint4 in = make_uint4(0, 0, 0, 0);
+          if (reads()) in = *chunk<kRow>(c);
+          const uint32_t w[4] = {in.x, in.y, in.z, in.w};
+          uint32_t o[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float2 v = s[4 * c + i];
+            if constexpr (SLOPE) {
+              v = __fmul2_rn(v, act_slope2<ACT>(unpack2(w[i], bf16)));
+            } else {
+              v = act_value2<ACT>(v);
+              if (p.epi.residual) v = __fadd2_rn(v, unpack2(w[i], bf16));
+            }
+            o[i] = pack2(v, bf16);
+          }
+          *chunk<kRow>(c) = make_uint4(o[0], o[1], o[2], o[3]);
         }
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        tma_store_3d(&maps->out, own + box * kBoxBytes, static_cast<int>(col),
-                     static_cast<int>(row0), split);
-        if (!SLOPE && p.epi.pre_out)
-          tma_store_3d(&maps->pre, z, static_cast<int>(col), static_cast<int>(row0), 0);
-        bulk_commit_group();
-      }
-      ++turn;
-      const int ahead = two ? 1 : 0;
-      if (in && j + 1 + ahead < kPieces) start_read(row0, col0, j + 1 + ahead, ahead);
+      store(&maps->out, row0, col, part);
+      if (reads() && !writes_pre() && j + 1 < kPieces) start_read(row0, col0, j + 1);
     }
     return true;
   }
 };
+
+// The sums start from the bias (its loads run while the products do).
+template <int COLS>
+__device__ __forceinline__ void start_sums(float2 (&sum)[COLS / 2], const float *bias, int64_t col0,
+                                           int64_t N) {
+  const bool vec = (reinterpret_cast<uintptr_t>(bias) & 15) == 0;
+#pragma unroll
+  for (int c = 0; c < COLS; c += 4) {
+    float4 b = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (bias && col0 + c < N) {
+      const float *at = bias + col0 + c;
+      if (vec && col0 + c + 4 <= N) {
+        b = __ldg(reinterpret_cast<const float4 *>(at));
+      } else {
+        b.x = __ldg(at);
+        if (col0 + c + 1 < N) b.y = __ldg(at + 1);
+        if (col0 + c + 2 < N) b.z = __ldg(at + 2);
+        if (col0 + c + 3 < N) b.w = __ldg(at + 3);
+      }
+    }
+    sum[c / 2] = make_float2(b.x, b.y);
+    sum[c / 2 + 1] = make_float2(b.z, b.w);
+  }
+}
 
 // The same without boxes: 32 columns at a time through a box's memory (float4
 // q of row r in slot q ^ (r % 8)), then a lane per column, row by row.
@@ -431,7 +413,7 @@ __device__ __forceinline__ void plain_epilogue(const Params &p, const float2 (&s
     __syncwarp();
     const int64_t col = col0 + c + lane;
     if (col < p.N) {
-      const float bias[1] = {p.epi.bias ? __ldg(p.epi.bias + col) : 0.f};
+      const float bias[1] = {0.f};  // the sums started from it
 #pragma unroll 1
       for (int r = 0; r < 32 && row0 + r < p.M; ++r) {
         float v[1] = {stage[r * 32 + (((lane >> 2) ^ (r & 7)) << 2) + (lane & 3)]};
@@ -445,36 +427,35 @@ template <int BN, int ACT, bool SLOPE, bool WIDE, bool BOXES>
 __device__ __forceinline__ void epilogue_role(uint8_t *stage, Barriers *bars, uint32_t tmem,
                                               const Params &p, const EpiMaps *maps, uint32_t rank,
                                               int warp, int lane, volatile int *abort) {
-  constexpr int kHalf = BN / 2;                  // columns per warp
-  const int quarter = warp % 4, half = (warp - kFirstEpiWarp) / 4;
+  constexpr int kCols = BN / 4;                  // columns per warp
+  const int quarter = warp % 4, part = (warp - kFirstEpiWarp) / 4;
   const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
   const uint32_t free_bar = cluster_addr(&bars->acc_free[0], 0);
-  uint8_t *own = stage + (warp - kFirstEpiWarp) * 2 * kBoxBytes;
-  BoxEpilogue<kHalf, ACT, SLOPE, WIDE> boxes{
-      p, maps, own, bars->in_full[warp - kFirstEpiWarp], abort, lane};
+  uint8_t *own = stage + (warp - kFirstEpiWarp) * kBoxBytes;
+  BoxEpilogue<kCols, ACT, SLOPE, WIDE> boxes{
+      p, maps, own, &bars->in_full[warp - kFirstEpiWarp], abort, lane};
   uint32_t acc = 0;
   bool ok = true;
-  for (int64_t i = blockIdx.x / 2; ok && i < p.items; i += gridDim.x / 2) {
+  for (int i = blockIdx.x / 2; ok && i < p.items; i += gridDim.x / 2) {
     const Item t = item_at(p, i);
     const int64_t row0 = static_cast<int64_t>(t.tm) * 256 + rank * 128 + quarter * 32;
-    const int64_t col0 = static_cast<int64_t>(t.tn) * BN + kHalf * half;
+    const int64_t col0 = static_cast<int64_t>(t.tn) * BN + kCols * part;
     if constexpr (BOXES) boxes.begin(row0, col0);
-    float2 sum[kHalf / 2];
-#pragma unroll
-    for (int c = 0; c < kHalf / 2; ++c) sum[c] = make_float2(0.f, 0.f);
+    float2 sum[kCols / 2];
+    start_sums<kCols>(sum, p.epi.bias, col0, p.N);
     for (int k0 = t.kb; k0 < t.ke; k0 += kPromote, ++acc) {
       const uint32_t b = acc & 1u;
       ok = mbar_wait_warp(&bars->acc_full[b], (acc >> 1) & 1u, abort, p.err, kSiteAccFull);
       if (!ok) break;
       tc_fence_after();
-      const uint32_t at = tmem + lanes + BN * b + kHalf * half;
+      const uint32_t at = tmem + lanes + BN * b + kCols * part;
 #pragma unroll
-      for (int c = 0; c < kHalf; c += 32) {
-        uint32_t r[32];
-        tmem_ld32(at + c, r);
-        tmem_wait_ld(r);
+      for (int c = 0; c < kCols; c += 16) {  // (32 at a time would not fit the registers)
+        uint32_t r[16];
+        tmem_ld16(at + c, r);
+        tmem_wait_ld16(r);
 #pragma unroll
-        for (int q = 0; q < 16; ++q)
+        for (int q = 0; q < 8; ++q)
           sum[c / 2 + q] = __fadd2_rn(sum[c / 2 + q], make_float2(__uint_as_float(r[2 * q]),
                                                                   __uint_as_float(r[2 * q + 1])));
       }
@@ -486,7 +467,7 @@ __device__ __forceinline__ void epilogue_role(uint8_t *stage, Barriers *bars, ui
     if constexpr (BOXES) {
       ok = boxes.finish(sum, row0, col0, t.split);
     } else {
-      plain_epilogue<kHalf>(p, sum, reinterpret_cast<float *>(own), row0, col0, lane);
+      plain_epilogue<kCols>(p, sum, reinterpret_cast<float *>(own), row0, col0, lane);
     }
   }
   if constexpr (BOXES) boxes.drain();
@@ -506,15 +487,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t rank = cluster_ctarank();
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::kStages; ++s) {
-      mbar_init(&bars->full[s], rank == 0 ? 2 : 1);  // own loads (+ the odd CTA's relay)
+      mbar_init(&bars->full[s], 1);
       mbar_init(&bars->empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&bars->acc_full[b], 1);
       mbar_init(&bars->acc_free[b], 2 * kEpiWarps);
     }
-    for (int w = 0; w < kEpiWarps; ++w)
-      for (int b = 0; b < 2; ++b) mbar_init(&bars->in_full[w][b], 1);
+    for (int w = 0; w < kEpiWarps; ++w) mbar_init(&bars->in_full[w], 1);
     mbar_init(&bars->drain, 1);
     bars->abort = 0;
     fence_mbar_init();
@@ -534,11 +514,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     regs_dec<kRegsLow>();
     if (warp == 1 && rank == 0) {
       issue_role<BN, A_MN, B_MN>(ring, bars, tmem, p, abort);
-    } else if (lane == 0) {
-      if (warp == 0)
-        load_role<BN, A_MN, B_MN>(&ma, &mb, ring, bars, p, rank, abort);
-      else if (warp == 1)
-        relay_role<BN>(bars, p, abort);
+    } else if (warp == 0 && lane == 0) {
+      load_role<BN, A_MN, B_MN>(&ma, &mb, ring, bars, p, rank, abort);
     }
   } else {
     regs_inc<kRegsHigh>();
@@ -579,7 +556,7 @@ cudaError_t launch(const Gemm &g, const Params &p, const CUtensorMap &ma, const 
       once_err[dev] = cudaErrorInvalidConfiguration;
   });
   if (once_err[dev] != cudaSuccess) return once_err[dev];
-  const int64_t clusters = p.items < g.num_sms / 2 ? p.items : g.num_sms / 2;
+  const int clusters = p.items < g.num_sms / 2 ? p.items : g.num_sms / 2;
   kernel<<<static_cast<unsigned>(2 * clusters), kThreads, smem_bytes<BN>(), g.stream>>>(ma, mb, maps,
                                                                                        p);
   return cudaGetLastError();
@@ -638,7 +615,7 @@ cudaError_t launch_gemm(const Gemm &g) {
   p.tiles_n = static_cast<int>((g.N + g.plan.bn - 1) / g.plan.bn);
   p.k_tiles = static_cast<int>((g.K + 63) / 64);
   p.splits = g.plan.splits;
-  p.items = static_cast<int64_t>(p.tiles_m) * p.tiles_n * p.splits;
+  p.items = p.tiles_m * p.tiles_n * p.splits;
   p.idesc = idesc_half_f32(256, g.plan.bn, g.epi.dtype == AG_BF16, g.a_mn, g.b_mn);
   p.err = g.err;
   p.epi = g.epi;
@@ -658,7 +635,7 @@ cudaError_t launch_gemm(const Gemm &g) {
   bool ok = encode_map(g, &ma, A.p, 2, 0, A.rows, A.cols, A.ld, g.a_mn ? 64 : 128, 64) &&
             encode_map(g, &mb, B.p, 2, 0, B.rows, B.cols, B.ld, g.b_mn ? 64 : g.plan.bn / 2, 64);
   if (p.boxes) {
-    const int width = p.wide ? 32 : 64;
+    const int width = p.wide ? 32 : g.plan.bn / 4;
     ok = ok && encode_map(g, &maps.out, e.out, out_size, p.splits, g.M, g.N, e.ld_out, 32, width);
     if (e.residual)
       ok = ok && encode_map(g, &maps.in, e.residual, out_size, 0, g.M, g.N, e.ld_res, 32, width);

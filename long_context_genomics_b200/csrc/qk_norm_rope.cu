@@ -7,8 +7,19 @@
 //   dx = r (d - n mean(d n) - mean d)
 //
 // Bound by memory: every element is read once and written once (the backward
-// reads x and dout and writes dx).  A block takes kPos positions with all
-// their heads, so each position's angles are formed once for all heads.
+// reads x and dout and writes dx).
+//
+// Rows kernels (heads of a multiple of 8 up to 256 elements, at addresses that
+// 4 elements' loads can take): a warp takes one position with all its heads, so
+// that the position's angles are formed once for them, and no other warp waits
+// for it.  A row lies in D / 8 lanes, eight elements each in two quads; where
+// halves are rotated, a lane's quads are 4 elements of the first half and their
+// partners in the second, so no lane needs another's values but for the norm's
+// sums.  All of a position's rows are loaded before any is worked on (the
+// forward takes four, the backward two row steps at a time): that many bytes in
+// flight is what the memory's rate asks for.
+//
+// General kernels: one warp per row through shared memory, any size or stride.
 #include "ag_internal.h"
 #include "linear_epilogue.cuh"
 
@@ -83,7 +94,265 @@ __device__ __forceinline__ void row_stats(const float *row, int D, int norm, flo
   r = 1.f / sqrtf(warp_sum(q) / D + eps);
 }
 
-// One warp per (position, head) row, any D and any strides.
+// --------------------------------------------------------------------------
+// Rows kernels.
+
+__device__ __forceinline__ float4 load4(const void *p, int64_t at, int dtype) {
+  if (dtype == AG_F32) return *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + at);
+  const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p) + at);
+  if (dtype == AG_BF16)
+    return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u),
+                       __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xFFFF0000u));
+  const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&w.x));
+  const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&w.y));
+  return make_float4(a.x, a.y, b.x, b.y);
+}
+__device__ __forceinline__ void store4(void *p, int64_t at, int dtype, float4 v) {
+  if (dtype == AG_F32) {
+    *reinterpret_cast<float4 *>(static_cast<float *>(p) + at) = v;
+    return;
+  }
+  uint2 w;
+  if (dtype == AG_BF16) {
+    w.x = pack_bf16x2(v.x, v.y), w.y = pack_bf16x2(v.z, v.w);
+  } else {
+    const __half2 a = __floats2half2_rn(v.x, v.y), b = __floats2half2_rn(v.z, v.w);
+    w.x = *reinterpret_cast<const uint32_t *>(&a), w.y = *reinterpret_cast<const uint32_t *>(&b);
+  }
+  *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p) + at) = w;
+}
+
+// A lane's eight elements of a row: two quads, at a and b.
+struct Eight {
+  float v[8];
+};
+__device__ __forceinline__ Eight load8(const void *p, int64_t row, int a, int b, int dtype) {
+  const float4 x = load4(p, row + a, dtype), y = load4(p, row + b, dtype);
+  return {{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w}};
+}
+__device__ __forceinline__ void store8(void *p, int64_t row, int a, int b, int dtype, const Eight &e) {
+  store4(p, row + a, dtype, make_float4(e.v[0], e.v[1], e.v[2], e.v[3]));
+  store4(p, row + b, dtype, make_float4(e.v[4], e.v[5], e.v[6], e.v[7]));
+}
+// Sum over the LPR lanes of a row.
+template <int LPR>
+__device__ __forceinline__ float row_sum(float v) {
+#pragma unroll
+  for (int o = LPR / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ Eight param8(const float *p, int a, int b, float otherwise) {
+  Eight e;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) e.v[i] = p ? __ldg(p + (i < 4 ? a + i : b + i - 4)) : otherwise;
+  return e;
+}
+
+// Where a lane's quads lie, and whether they turn.
+struct Lane {
+  int a, b;
+  bool in, turns;
+};
+template <int LPR>
+__device__ __forceinline__ Lane lane_of(int lane, int D, int R, int rope) {
+  const int l = lane % LPR;
+  Lane t;
+  t.in = 8 * l < D;
+  t.turns = 8 * l < R;
+  if (rope == AG_ROPE_HALVES && t.turns)
+    t.a = 4 * l, t.b = R / 2 + 4 * l;
+  else
+    t.a = 8 * l, t.b = 8 * l + 4;
+  return t;
+}
+// The lane's four pairs turned by the position's angles; sign -1: back.
+__device__ __forceinline__ void turn_pairs(Eight &e, const float4 *cs, int rope, float sign) {
+  const float4 p = cs[0], q = cs[1];  // (cos, sin) of four angles
+  const float c[4] = {p.x, p.z, q.x, q.z};
+  const float s[4] = {sign * p.y, sign * p.w, sign * q.y, sign * q.w};
+  const bool halves = rope == AG_ROPE_HALVES;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float x = halves ? e.v[i] : e.v[2 * i], y = halves ? e.v[i + 4] : e.v[2 * i + 1];
+    const float u = fmaf(x, c[i], -y * s[i]), w = fmaf(y, c[i], x * s[i]);
+    if (halves) e.v[i] = u, e.v[i + 4] = w;
+    else e.v[2 * i] = u, e.v[2 * i + 1] = w;
+  }
+}
+
+// The position's angles into the warp's own shared memory.
+__device__ __forceinline__ void warp_angles(const QkArgs &a, float2 *cs, int64_t b, int64_t l,
+                                            int lane) {
+  __syncwarp();
+  const long long pos = a.positions ? a.positions[b * a.pos_sb + l] : l;
+  for (int i = lane; i < a.R / 2; i += 32) cs[i] = turn(pos, a.inv_freq[i]);
+  __syncwarp();
+}
+
+// n = (x - mean) r in place; r.
+template <int LPR>
+__device__ __forceinline__ float normalise(Eight &e, const QkArgs &a, bool in) {
+  if (a.norm == AG_NORM_NONE) return 1.f;
+  float mean = 0.f;
+  if (a.norm == AG_NORM_LAYER) {
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s += e.v[i];
+    mean = row_sum<LPR>(s) / a.D;
+  }
+  float q = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    e.v[i] = in ? e.v[i] - mean : 0.f;
+    q = fmaf(e.v[i], e.v[i], q);
+  }
+  const float r = 1.f / sqrtf(row_sum<LPR>(q) / a.D + a.eps);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) e.v[i] *= r;
+  return r;
+}
+
+template <int LPR>
+__global__ void __launch_bounds__(kThreads, 3) qk_fwd_rows_kernel(const QkArgs a) {
+  extern __shared__ float smem[];
+  constexpr int kAtOnce = 32 / LPR, kSteps = 4;  // rows per step; steps loaded together
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  float2 *cs = reinterpret_cast<float2 *>(smem) + warp * (a.R / 2);
+  const Lane t = lane_of<LPR>(lane, a.D, a.R, a.rope);
+  for (int64_t pos = static_cast<int64_t>(blockIdx.x) * kWarps + warp; pos < a.positions_total;
+       pos += static_cast<int64_t>(gridDim.x) * kWarps) {
+    const int64_t b = pos / a.L, l = pos - b * a.L;
+    if (a.R) warp_angles(a, cs, b, l, lane);
+    const float4 *angles = reinterpret_cast<const float4 *>(cs) + 2 * (lane % LPR);
+#pragma unroll 1
+    for (int which = 0; which < 2; ++which) {
+      const QkSide &s = a.side[which];
+      const int64_t from = b * s.sb + l * s.sl, to = (b * s.H * a.L + l) * a.D;
+      const Eight w = t.in ? param8(s.w, t.a, t.b, 1.f) : Eight{}, bias = t.in ? param8(s.b, t.a, t.b, 0.f) : Eight{};
+#pragma unroll 1
+      for (int h0 = 0; h0 < s.H; h0 += kAtOnce * kSteps) {
+        Eight x[kSteps];
+#pragma unroll
+        for (int u = 0; u < kSteps; ++u) {
+          const int h = h0 + u * kAtOnce + lane / LPR;
+          x[u] = Eight{};
+          if (t.in && h < s.H) x[u] = load8(s.x, from + h * s.sh, t.a, t.b, a.x_dtype);
+        }
+#pragma unroll
+        for (int u = 0; u < kSteps; ++u) {
+          if (h0 + u * kAtOnce >= s.H) break;
+          const int h = h0 + u * kAtOnce + lane / LPR;
+          normalise<LPR>(x[u], a, t.in);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[u].v[i] = fmaf(x[u].v[i], w.v[i], bias.v[i]);
+          if (t.turns) turn_pairs(x[u], angles, a.rope, 1.f);
+          if (t.in && h < s.H) store8(s.out, to + h * a.L * a.D, t.a, t.b, a.o_dtype, x[u]);
+        }
+      }
+    }
+  }
+}
+
+// Backward.  A lane's elements are the same in every row it meets, so it sums
+// the parameter gradients of a position's heads in registers and adds them to
+// shared memory of its own, [w and b of both sides][two quads][lane]; the block
+// adds its lanes' and warps' at the end, in a fixed order, and writes one
+// partial.
+template <int LPR>
+__global__ void __launch_bounds__(kThreads, 2) qk_bwd_rows_kernel(const QkArgs a) {
+  extern __shared__ float smem[];
+  constexpr int kAtOnce = 32 / LPR, kSteps = 2;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  float2 *cs = reinterpret_cast<float2 *>(smem) + warp * (a.R / 2);
+  float4 *sums = reinterpret_cast<float4 *>(smem + kWarps * a.R);  // [kWarps][8][32]
+  float4 *own = sums + warp * 8 * 32 + lane;
+  if (a.partial)
+#pragma unroll
+    for (int q = 0; q < 8; ++q) own[q * 32] = make_float4(0.f, 0.f, 0.f, 0.f);
+  const Lane t = lane_of<LPR>(lane, a.D, a.R, a.rope);
+  const float4 *angles = reinterpret_cast<const float4 *>(cs) + 2 * (lane % LPR);
+  for (int64_t pos = static_cast<int64_t>(blockIdx.x) * kWarps + warp; pos < a.positions_total;
+       pos += static_cast<int64_t>(gridDim.x) * kWarps) {
+    const int64_t b = pos / a.L, l = pos - b * a.L;
+    bool angles_ready = a.R == 0;
+#pragma unroll 1
+    for (int which = 0; which < 2; ++which) {
+      const QkSide &s = a.side[which];
+      if (s.H == 0) continue;
+      const int64_t x_at = b * s.sb + l * s.sl, g_at = (b * s.H * a.L + l) * a.D,
+                    dx_at = b * s.dxb + l * s.dxl;
+      const Eight w = t.in ? param8(s.w, t.a, t.b, 1.f) : Eight{};
+      Eight dw{}, db{};
+#pragma unroll 1
+      for (int h0 = 0; h0 < s.H; h0 += kAtOnce * kSteps) {
+        Eight x[kSteps], g[kSteps];
+#pragma unroll
+        for (int u = 0; u < kSteps; ++u) {
+          const int h = h0 + u * kAtOnce + lane / LPR;
+          x[u] = Eight{}, g[u] = Eight{};
+          if (t.in && h < s.H) {
+            x[u] = load8(s.x, x_at + h * s.sh, t.a, t.b, a.x_dtype);
+            g[u] = load8(s.g, g_at + h * a.L * a.D, t.a, t.b, a.o_dtype);
+          }
+        }
+        if (!angles_ready) {  // while the first rows are on their way
+          warp_angles(a, cs, b, l, lane);
+          angles_ready = true;
+        }
+#pragma unroll
+        for (int u = 0; u < kSteps; ++u) {
+          if (h0 + u * kAtOnce >= s.H) break;
+          const int h = h0 + u * kAtOnce + lane / LPR;
+          const bool mine = t.in && h < s.H;
+          const float r = normalise<LPR>(x[u], a, t.in);
+          if (t.turns) turn_pairs(g[u], angles, a.rope, -1.f);
+          float along = 0.f, total = 0.f;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            // (A row of this step past the last head counts for nothing, also
+            // when eps is zero and its norm is not a number.)
+            if (mine) dw.v[i] = fmaf(g[u].v[i], x[u].v[i], dw.v[i]), db.v[i] += g[u].v[i];
+            g[u].v[i] *= w.v[i];
+            along = fmaf(g[u].v[i], x[u].v[i], along);
+            total += g[u].v[i];
+          }
+          along = a.norm == AG_NORM_NONE ? 0.f : row_sum<LPR>(along) / a.D;
+          total = a.norm == AG_NORM_LAYER ? row_sum<LPR>(total) / a.D : 0.f;
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            g[u].v[i] = r * (fmaf(-x[u].v[i], along, g[u].v[i]) - total);
+          if (mine) store8(s.dx, dx_at + h * s.dxh, t.a, t.b, a.x_dtype, g[u]);
+        }
+      }
+      if (a.partial) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float *v = (q < 2 ? dw.v : db.v) + 4 * (q & 1);
+          float4 &o = own[(which * 4 + q) * 32];
+          const float4 was = o;
+          o = make_float4(was.x + v[0], was.y + v[1], was.z + v[2], was.w + v[3]);
+        }
+      }
+    }
+  }
+  if (!a.partial) return;
+  __syncthreads();
+  for (int i = threadIdx.x; i < 4 * a.D; i += kThreads) {
+    // Element e of array `which` lies in quad `quad` of lane `at` (lane_of).
+    const int which = i / a.D, e = i % a.D;
+    const bool half = a.rope == AG_ROPE_HALVES && e < a.R;
+    const int quad = half ? e / (a.R / 2) : (e % 8) / 4, at = half ? e % (a.R / 2) / 4 : e / 8;
+    const float *from = reinterpret_cast<const float *>(sums + (which * 2 + quad) * 32 + at) + e % 4;
+    float v = 0.f;
+    for (int w = 0; w < kWarps; ++w)
+#pragma unroll
+      for (int row = 0; row < kAtOnce; ++row) v += from[(w * 8 * 32 + row * LPR) * 4];
+    a.partial[static_cast<int64_t>(blockIdx.x) * 4 * a.D + i] = v;
+  }
+}
+
+// --------------------------------------------------------------------------
+// General kernels.  One warp per (position, head) row, any D and any strides.
 __global__ void __launch_bounds__(kThreads) qk_fwd_kernel(const QkArgs a) {
   extern __shared__ float smem[];
   const int half = a.R >> 1, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -221,10 +490,29 @@ __global__ void __launch_bounds__(256)
   if (to) to[n % D] = static_cast<float>(t);
 }
 
+// A quad of elements can be loaded at every address of the tensor.
+bool quads(const void *p, int dtype, int64_t s0, int64_t s1, int64_t s2) {
+  return aligned(p, dtype == AG_F32 ? 16 : 8) && s0 % 4 == 0 && s1 % 4 == 0 && s2 % 4 == 0;
+}
+// Whether the rows kernels can take the call.
+bool by_rows(const QkArgs &a, bool backward) {
+  if (a.D % 8 || a.D > 256 || a.R % 8) return false;
+  for (const QkSide &s : a.side) {
+    if (s.H == 0) continue;
+    if (!quads(s.x, a.x_dtype, s.sb, s.sl, s.sh)) return false;
+    if (backward ? !quads(s.g, a.o_dtype, 0, 0, 0) || !quads(s.dx, a.x_dtype, s.dxb, s.dxl, s.dxh)
+                 : !quads(s.out, a.o_dtype, 0, 0, 0))
+      return false;
+  }
+  return true;
+}
+
 int bwd_warps(int D) { return D <= 512 ? 8 : 4; }
-int bwd_blocks(int64_t total, int num_sms) {
-  const int64_t turns = (total + kPos - 1) / kPos;
-  return static_cast<int>(turns < 4 * num_sms ? turns : 4 * num_sms);
+// Blocks of a backward, as many as its partial sums: the rows kernel's two to an
+// SM, the general one's four, but no more than have work.
+int bwd_blocks(int64_t total, int64_t each, int per_sm, int num_sms) {
+  const int64_t turns = (total + each - 1) / each;
+  return static_cast<int>(turns < per_sm * num_sms ? turns : per_sm * num_sms);
 }
 
 cudaError_t allow_smem(const void *kernel, size_t bytes) {
@@ -236,11 +524,20 @@ cudaError_t allow_smem(const void *kernel, size_t bytes) {
 }  // namespace
 
 int64_t qk_bwd_workspace(int64_t positions_total, int64_t D, int num_sms) {
-  return static_cast<int64_t>(bwd_blocks(positions_total, num_sms)) * 4 * D * 4;
+  return static_cast<int64_t>(bwd_blocks(positions_total, kPos, 4, num_sms)) * 4 * D * 4;
 }
 
 cudaError_t launch_qk_fwd(const QkArgs &a, int num_sms, cudaStream_t stream) {
-  (void)num_sms;
+  if (by_rows(a, false)) {
+    auto *kernel = a.D <= 32    ? qk_fwd_rows_kernel<4>
+                   : a.D <= 64  ? qk_fwd_rows_kernel<8>
+                   : a.D <= 128 ? qk_fwd_rows_kernel<16>
+                                : qk_fwd_rows_kernel<32>;
+    const int64_t blocks = (a.positions_total + kWarps - 1) / kWarps;
+    kernel<<<static_cast<unsigned>(blocks < 24 * num_sms ? blocks : 24 * num_sms), kThreads,
+             kWarps * a.R * 4, stream>>>(a);
+    return cudaGetLastError();
+  }
   const size_t smem = (static_cast<size_t>(kPos) * a.R + kWarps * static_cast<size_t>(a.D)) * 4;
   cudaError_t e = allow_smem(reinterpret_cast<const void *>(qk_fwd_kernel), smem);
   if (e != cudaSuccess) return e;
@@ -250,12 +547,23 @@ cudaError_t launch_qk_fwd(const QkArgs &a, int num_sms, cudaStream_t stream) {
 }
 
 cudaError_t launch_qk_bwd(const QkArgs &a, int num_sms, cudaStream_t stream) {
-  const int warps = bwd_warps(a.D), blocks = bwd_blocks(a.positions_total, num_sms);
-  const size_t smem = (static_cast<size_t>(kPos) * a.R + warps * 6 * static_cast<size_t>(a.D)) * 4;
-  cudaError_t e = allow_smem(reinterpret_cast<const void *>(qk_bwd_kernel), smem);
-  if (e != cudaSuccess) return e;
-  qk_bwd_kernel<<<blocks, warps * 32, smem, stream>>>(a, warps);
-  e = cudaGetLastError();
+  int blocks;
+  if (by_rows(a, true)) {
+    auto *kernel = a.D <= 32    ? qk_bwd_rows_kernel<4>
+                   : a.D <= 64  ? qk_bwd_rows_kernel<8>
+                   : a.D <= 128 ? qk_bwd_rows_kernel<16>
+                                : qk_bwd_rows_kernel<32>;
+    blocks = bwd_blocks(a.positions_total, kWarps, 2, num_sms);
+    kernel<<<blocks, kThreads, kWarps * (a.R + 8 * 32 * 4) * 4, stream>>>(a);
+  } else {
+    const int warps = bwd_warps(a.D);
+    blocks = bwd_blocks(a.positions_total, kPos, 4, num_sms);
+    const size_t smem = (static_cast<size_t>(kPos) * a.R + warps * 6 * static_cast<size_t>(a.D)) * 4;
+    const cudaError_t e = allow_smem(reinterpret_cast<const void *>(qk_bwd_kernel), smem);
+    if (e != cudaSuccess) return e;
+    qk_bwd_kernel<<<blocks, warps * 32, smem, stream>>>(a, warps);
+  }
+  const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !a.partial) return e;
   qk_params_kernel<<<(4 * a.D + 31) / 32, 256, 0, stream>>>(
       a.partial, blocks, a.D, a.side[0].dw, a.side[0].db, a.side[1].dw, a.side[1].db);
