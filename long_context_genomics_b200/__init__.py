@@ -21,7 +21,6 @@ replacement") with a softmax over all keys.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 import os
@@ -387,7 +386,11 @@ ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 NORMS = {"none": 0, "rms": 1, "layer": 2}
 ROPES = {"halves": 0, "interleaved": 1}
 _HALF = (torch.bfloat16, torch.float16)
-_NOTHING = contextlib.nullcontext()
+
+
+def _elsewhere(dev: torch.device, stream) -> bool:
+    """Whether a call for tensors on dev has to enter _site first."""
+    return stream is not None or torch._C._cuda_getDevice() != dev.index
 
 
 def _site(dev: torch.device, stream):
@@ -396,7 +399,7 @@ def _site(dev: torch.device, stream):
     current stream).  Workspaces belong to that stream, so a later call on it
     may take their memory over, and no other stream does."""
     if stream is None:
-        return _NOTHING if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+        return torch.cuda.device(dev)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=dev)
     if stream.device != dev:
@@ -424,25 +427,36 @@ def _on_gpu(t, name: str, dtypes) -> None:
         raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
 
 
-def _matrix(t, name: str, dtypes, rows: int, cols: int) -> int:
-    """Checks a row-major matrix (its rows may be apart) and returns its row stride."""
-    _on_gpu(t, name, dtypes)
-    if t.shape != (rows, cols):
-        raise ValueError(f"{name} must be [{rows},{cols}], got {list(t.shape)}")
-    ld, inner = t.stride()
-    if inner != 1 and cols > 1:
+def _same_device(t, name: str, dev: torch.device) -> None:
+    if t.device != dev:
+        raise ValueError(f"all tensors of a call must be on {dev}; {name} is on {t.device}")
+
+
+def _matrix(t, name: str, dtype, rows: int, cols: int, dev: torch.device) -> int:
+    """Checks a row-major matrix (its rows may be apart) and returns its row
+    stride.  (The checks of the layers' calls are written for the case that
+    all is well: at a few rows they cost as much as the kernel.)"""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == (rows, cols) \
+            and t.device == dev:
+        ld, inner = t.stride()
+        if inner == 1 or cols == 1:
+            return ld if rows > 1 or ld > cols else cols
         raise ValueError(f"the rows of {name} must be dense")
-    return ld if rows > 1 else max(ld, cols)
+    _on_gpu(t, name, (dtype,))
+    _same_device(t, name, dev)
+    raise ValueError(f"{name} must be [{rows},{cols}], got {list(t.shape)}")
 
 
-def _vector(t, name: str, n: int):
+def _vector(t, name: str, n: int, dev: torch.device):
     """Checks an optional dense float32 vector of n and returns its pointer."""
     if t is None:
         return None
+    if isinstance(t, torch.Tensor) and t.dtype is torch.float32 and t.shape == (n,) \
+            and t.device == dev and t.is_contiguous():
+        return t.data_ptr()
     _on_gpu(t, name, (torch.float32,))
-    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous [{n}]")
-    return t.data_ptr()
+    _same_device(t, name, dev)
+    raise ValueError(f"{name} must be a contiguous [{n}]")
 
 
 def _workspace(query, dev: torch.device, name: str, *args):
@@ -457,11 +471,6 @@ def _workspace(query, dev: torch.device, name: str, *args):
     return t, t.data_ptr(), n.value
 
 
-def _check_status(st: int, name: str) -> None:
-    if st != AG_OK:
-        raise AgError(name, st)
-
-
 def ag_linear_fwd(x: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = None,
                   act: str = "none", residual: torch.Tensor | None = None, preact=False,
                   out: torch.Tensor | None = None, out_dtype: torch.dtype | None = None,
@@ -474,38 +483,39 @@ def ag_linear_fwd(x: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = 
     x's type to write) also returns x W^T + bias, which ag_linear_bwd of the
     next layer takes: (y, preact).  out may be the residual itself."""
     _on_gpu(x, "x", _HALF)
-    if x.dim() != 2 or not isinstance(W, torch.Tensor) or W.dim() != 2:
+    if x.ndim != 2 or not isinstance(W, torch.Tensor) or W.ndim != 2:
         raise ValueError("x must be [M,K] and W [N,K]")
-    (M, K), N, T, dev = x.shape, W.shape[0], x.dtype, x.device
-    ldx = _matrix(x, "x", (T,), M, K)
-    ldw = _matrix(W, "W", (T,), N, K)
+    dev = x.device
+    if _elsewhere(dev, stream):
+        with _site(dev, stream):
+            return ag_linear_fwd(x, W, bias, act, residual, preact, out, out_dtype)
+    (M, K), N, T = x.shape, W.shape[0], x.dtype
+    ldx, ldw = _matrix(x, "x", T, M, K, dev), _matrix(W, "W", T, N, K, dev)
     code = _code(ACTIVATIONS, act, "act")
     if out_dtype is None:
         out_dtype = T if out is None else out.dtype
-    if out_dtype not in (T, torch.float32):
+    if out_dtype is not T and out_dtype is not torch.float32:
         raise TypeError(f"out_dtype must be {T} or torch.float32, got {out_dtype}")
-    used = [x, W]
-    b = _vector(bias, "bias", N)
-    ldr = 0 if residual is None else _matrix(residual, "residual", (out_dtype,), M, N)
-    used += [t for t in (bias, residual) if t is not None]
-    with _site(dev, stream):
-        if out is None:
-            out = torch.empty((M, N), dtype=out_dtype, device=dev)
-        ldy = _matrix(out, "out", (out_dtype,), M, N)
-        used.append(out)
-        z = None
-        if preact is not False and preact is not None:
-            z = torch.empty((M, N), dtype=T, device=dev) if preact is True else preact
-            used.append(z)
-        ldz = 0 if z is None else _matrix(z, "preact", (T,), M, N)
-        _one_device(*used)
-        xp, wp = x.data_ptr(), W.data_ptr()
+    b = _vector(bias, "bias", N, dev)
+    r, ldr, z, zp, ldz = None, 0, None, None, 0
+    if residual is not None:
+        ldr, r = _matrix(residual, "residual", out_dtype, M, N, dev), residual.data_ptr()
+    if out is None:
+        out, ldy = x.new_empty((M, N), dtype=out_dtype), N
+    else:
+        ldy = _matrix(out, "out", out_dtype, M, N, dev)
+    if preact is not False and preact is not None:
+        z = x.new_empty((M, N)) if preact is True else preact
+        ldz, zp = _matrix(z, "preact", T, M, N, dev), z.data_ptr()
+    xp, wp, yp, t, yt = x.data_ptr(), W.data_ptr(), out.data_ptr(), DTYPES[T], DTYPES[out_dtype]
+    # Most calls need no workspace; the others say so before they do anything.
+    st = lib.ag_linear_fwd(xp, ldx, wp, ldw, b, r, ldr, M, N, K, t, code, zp, ldz, yp, ldy, yt,
+                           None, 0, _current(dev))
+    if st == 9:
         ws, wsp, n = _workspace(lib.ag_linear_fwd_workspace, dev, "ag_linear_fwd_workspace", xp,
                                 ldx, wp, ldw, M, N, K)
-        st = lib.ag_linear_fwd(xp, ldx, wp, ldw, b, None if residual is None else
-                               residual.data_ptr(), ldr, M, N, K, DTYPES[T], code,
-                               None if z is None else z.data_ptr(), ldz, out.data_ptr(), ldy,
-                               DTYPES[out_dtype], wsp, n, _current(dev))
+        st = lib.ag_linear_fwd(xp, ldx, wp, ldw, b, r, ldr, M, N, K, t, code, zp, ldz, yp, ldy,
+                               yt, wsp, n, _current(dev))
     if st != AG_OK:
         raise AgError("ag_linear_fwd", st)
     return out if z is None else (out, z)
@@ -524,45 +534,48 @@ def ag_linear_bwd(dy: torch.Tensor, x: torch.Tensor, W: torch.Tensor, act: str =
     fp32; dW_dtype: fp32 (default) or x's type.  dx and dW may be given to
     write into.  The gradient of ag_linear_fwd's residual is dy itself."""
     _on_gpu(dy, "dy", _HALF)
-    if dy.dim() != 2 or not isinstance(x, torch.Tensor) or x.dim() != 2:
+    if dy.ndim != 2 or not isinstance(x, torch.Tensor) or x.ndim != 2:
         raise ValueError("dy must be [M,N] and x [M,K]")
-    (M, N), K, T, dev = dy.shape, x.shape[1], dy.dtype, dy.device
-    lddy = _matrix(dy, "dy", (T,), M, N)
-    ldx = _matrix(x, "x", (T,), M, K)
-    ldw = _matrix(W, "W", (T,), N, K)
+    dev = dy.device
+    if _elsewhere(dev, stream):
+        with _site(dev, stream):
+            return ag_linear_bwd(dy, x, W, act, preact, need_dx, need_dW, need_db, dx_dtype,
+                                 dW_dtype, dx, dW)
+    (M, N), K, T = dy.shape, x.shape[1], dy.dtype
+    lddy, ldx = _matrix(dy, "dy", T, M, N, dev), _matrix(x, "x", T, M, K, dev)
+    ldw = _matrix(W, "W", T, N, K, dev)
     code = _code(ACTIVATIONS, act, "act")
-    ldz = 0 if preact is None else _matrix(preact, "preact", (T,), M, K)
+    ldz = 0 if preact is None else _matrix(preact, "preact", T, M, K, dev)
     if code and preact is None:
         raise ValueError(f"act {act} needs the preact of x")
-    used = [t for t in (dy, x, W, preact) if t is not None]
-    with _site(dev, stream):
-        lddx = lddw = 0
-        if need_dx:
-            if dx is None:
-                dx = torch.empty((M, K), dtype=dx_dtype or T, device=dev)
-            lddx = _matrix(dx, "dx", (dx_dtype,) if dx_dtype else (T, torch.float32), M, K)
-            used.append(dx)
-        else:
-            dx = None
-        if need_dW:
-            if dW is None:
-                dW = torch.empty((N, K), dtype=dW_dtype, device=dev)
-            lddw = _matrix(dW, "dW", (T, torch.float32), N, K)
-            used.append(dW)
-        else:
-            dW = None
-        db = torch.empty(N, dtype=torch.float32, device=dev) if need_db else None
-        _one_device(*used)
-        p = [None if t is None else t.data_ptr() for t in (dy, x, W, preact, dx, dW, db)]
-        ws, wsp, n = _workspace(lib.ag_linear_bwd_workspace, dev, "ag_linear_bwd_workspace", p[0],
-                                lddy, p[1], ldx, p[2], ldw, M, N, K, p[4], p[5], p[6])
-        st = lib.ag_linear_bwd(p[0], lddy, p[1], ldx, p[2], ldw, p[3], ldz, code, M, N, K,
-                               DTYPES[T], p[4], lddx, DTYPES[dx.dtype] if need_dx else 0, p[5],
-                               lddw, DTYPES[dW.dtype] if need_dW else 0, p[6], wsp, n,
-                               _current(dev))
+    dxp = dwp = dbp = None
+    lddx = lddw = dxt = dwt = 0
+    if need_dx:
+        dx_dtype = dx_dtype or (T if dx is None else dx.dtype)
+        if dx_dtype is not T and dx_dtype is not torch.float32:
+            raise TypeError(f"dx_dtype must be {T} or torch.float32, got {dx_dtype}")
+        if dx is None:
+            dx = dy.new_empty((M, K), dtype=dx_dtype)
+        lddx, dxp, dxt = _matrix(dx, "dx", dx_dtype, M, K, dev), dx.data_ptr(), DTYPES[dx_dtype]
+    if need_dW:
+        dW_dtype = dW_dtype if dW is None else dW.dtype
+        if dW_dtype is not T and dW_dtype is not torch.float32:
+            raise TypeError(f"dW_dtype must be {T} or torch.float32, got {dW_dtype}")
+        if dW is None:
+            dW = dy.new_empty((N, K), dtype=dW_dtype)
+        lddw, dwp, dwt = _matrix(dW, "dW", dW_dtype, N, K, dev), dW.data_ptr(), DTYPES[dW_dtype]
+    db = dy.new_empty(N, dtype=torch.float32) if need_db else None
+    if need_db:
+        dbp = db.data_ptr()
+    dyp, xp, wp = dy.data_ptr(), x.data_ptr(), W.data_ptr()
+    ws, wsp, n = _workspace(lib.ag_linear_bwd_workspace, dev, "ag_linear_bwd_workspace", dyp,
+                            lddy, xp, ldx, wp, ldw, M, N, K, dxp, dwp, dbp)
+    st = lib.ag_linear_bwd(dyp, lddy, xp, ldx, wp, ldw,
+                           None if preact is None else preact.data_ptr(), ldz, code, M, N, K,
+                           DTYPES[T], dxp, lddx, dxt, dwp, lddw, dwt, dbp, wsp, n, _current(dev))
     if st != AG_OK:
         raise AgError("ag_linear_bwd", st)
-    return dx, dW, db
+    return dx if need_dx else None, dW if need_dW else None, db
 
 
 def ag_rope_frequencies(rotary_dim: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
@@ -572,81 +585,61 @@ def ag_rope_frequencies(rotary_dim: int, base: float = 10000.0, device="cuda") -
     return (float(base) ** (-p / rotary_dim)).to(device)
 
 
-def _heads(t, name: str, dtypes, B=None, L=None, H=None, D=None):
-    """Checks a [B,L,H,D] (or [B,L,D]: one head) tensor with dense heads.
-    Returns its sizes and its (b, l, h) strides."""
-    _on_gpu(t, name, dtypes)
-    if t.dim() not in (3, 4):
+def _heads(t, name: str, dtype, B: int, L: int, D: int, dev: torch.device):
+    """Checks a [B,L,H,D] (or [B,L,D]: one head) tensor with dense heads;
+    returns H, pointer and the strides over b, l and h."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == dev:
+        s = t.shape
+        if len(s) == 4 and s[0] == B and s[1] == L and s[3] == D:
+            sb, sl, sh, sd = t.stride()
+            if sd == 1 or D == 1:
+                return s[2], t.data_ptr(), sb, sl, sh
+            raise ValueError(f"the heads of {name} must be dense")
+        if s == (B, L, D):
+            sb, sl, sd = t.stride()
+            if sd == 1 or D == 1:
+                return 1, t.data_ptr(), sb, sl, 0
+            raise ValueError(f"the heads of {name} must be dense")
+    _on_gpu(t, name, (dtype,))
+    _same_device(t, name, dev)
+    raise ValueError(f"{name} must be [{B},{L},H,{D}] or [{B},{L},{D}], got {list(t.shape)}")
+
+
+def _qk_first(q, k):
+    """Type, device and sizes of a call, from the queries or else the keys."""
+    first, name = (q, "q") if q is not None else (k, "k")
+    if first is None:
+        raise ValueError("q and k are both None")
+    _on_gpu(first, name, DTYPES)
+    if first.ndim not in (3, 4):
         raise ValueError(f"{name} must be [B,L,H,D] or [B,L,D]")
-    shape, stride = tuple(t.shape), t.stride()
-    if t.dim() == 3:
-        shape, stride = shape[:2] + (1,) + shape[2:], stride[:2] + (0,) + stride[2:]
-    for got, want in zip(shape, (B, L, H, D)):
-        if want is not None and got != want:
-            raise ValueError(f"{name} must be {[B, L, H, D]}, got {list(shape)}")
-    if stride[3] != 1 and shape[3] > 1:
-        raise ValueError(f"the heads of {name} must be dense")
-    return shape, stride[:3]
+    return first, first.dtype, first.device, first.shape[0], first.shape[1], first.shape[-1]
 
 
-class _QkCall:
-    """The arguments that the two directions of ag_qk_norm_rope share."""
+def _rotation(inv_freq, rope, positions, B: int, L: int, dev: torch.device):
+    """The rotation's arguments: inv_freq, R, rope, positions, their stride over b."""
+    code, freq, R, where, pos_sb = _code(ROPES, rope, "rope"), None, 0, None, 0
+    if inv_freq is not None:
+        _on_gpu(inv_freq, "inv_freq", (torch.float64,))
+        _same_device(inv_freq, "inv_freq", dev)
+        if inv_freq.ndim != 1 or not inv_freq.is_contiguous():
+            raise ValueError("inv_freq must be a contiguous [R/2]")
+        R, freq = 2 * inv_freq.shape[0], inv_freq.data_ptr()
+    if positions is not None:
+        _on_gpu(positions, "positions", (torch.int64,))
+        _same_device(positions, "positions", dev)
+        if positions.shape != (L,) and positions.shape != (B, L):
+            raise ValueError(f"positions must be [{L}] or [{B},{L}], got {list(positions.shape)}")
+        s = positions.stride()
+        if L > 1 and s[-1] != 1:
+            raise ValueError("the rows of positions must be dense")
+        where = positions.data_ptr()
+        if len(s) == 2 and B > 1:
+            pos_sb = s[0]
+    return freq, R, code, where, pos_sb
 
-    def __init__(self, q, k, q_weight, k_weight, q_bias, k_bias, norm, eps, inv_freq, rope,
-                 positions):
-        first = q if q is not None else k
-        if first is None:
-            raise ValueError("q and k are both None")
-        (self.B, self.L, _, self.D), _ = _heads(first, "q" if q is not None else "k", DTYPES)
-        self.T, self.dev = first.dtype, first.device
-        self.used, self.inputs, self.H, self.flat = [], [], [], []
-        for t, name in ((q, "q"), (k, "k")):
-            if t is None:
-                self.inputs += [None, 0, 0, 0]
-                self.H.append(0)
-                self.flat.append(False)
-                continue
-            shape, strides = _heads(t, name, (self.T,), B=self.B, L=self.L, D=self.D)
-            self.inputs += [t.data_ptr(), *strides]
-            self.H.append(shape[2])
-            self.flat.append(t.dim() == 3)
-            self.used.append(t)
-        self.weights = [_vector(t, n, self.D) for t, n in ((q_weight, "q_weight"),
-                                                           (k_weight, "k_weight"))]
-        self.biases = [_vector(t, n, self.D) for t, n in ((q_bias, "q_bias"), (k_bias, "k_bias"))]
-        self.used += [t for t in (q_weight, k_weight, q_bias, k_bias) if t is not None]
-        self.norm, self.rope = _code(NORMS, norm, "norm"), _code(ROPES, rope, "rope")
-        self.eps, self.R, freq = float(eps), 0, None
-        if inv_freq is not None:
-            _on_gpu(inv_freq, "inv_freq", (torch.float64,))
-            if inv_freq.dim() != 1 or not inv_freq.is_contiguous():
-                raise ValueError("inv_freq must be a contiguous [R/2]")
-            self.R, freq = 2 * inv_freq.shape[0], inv_freq.data_ptr()
-            self.used.append(inv_freq)
-        where, pos_sb = None, 0
-        if positions is not None:
-            _on_gpu(positions, "positions", (torch.int64,))
-            if tuple(positions.shape) not in ((self.L,), (self.B, self.L)):
-                raise ValueError(f"positions must be [{self.L}] or [{self.B},{self.L}]")
-            if self.L > 1 and positions.stride(-1) != 1:
-                raise ValueError("the rows of positions must be dense")
-            where = positions.data_ptr()
-            pos_sb = positions.stride(0) if positions.dim() == 2 and self.B > 1 else 0
-            self.used.append(positions)
-        self.rotation = [freq, self.R, self.rope, where, pos_sb]
-        self.sizes = [self.B, self.H[0], self.H[1], self.L, self.D]
 
-    def layout(self, side: int):
-        """The attention's layout of a side: [B,H,L,D], or [B,L,D] for a [B,L,D] input."""
-        B, L, D, H = self.B, self.L, self.D, self.H[side]
-        return (B, L, D) if self.flat[side] else (B, H, L, D)
-
-    def dense(self, t, name: str, dtypes, side: int) -> int:
-        _on_gpu(t, name, dtypes)
-        if tuple(t.shape) != self.layout(side) or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous {list(self.layout(side))}")
-        self.used.append(t)
-        return t.data_ptr()
+_NO_HEADS = (0, None, 0, 0, 0)
 
 
 def ag_qk_norm_rope_fwd(q: torch.Tensor | None, k: torch.Tensor | None,
@@ -670,25 +663,51 @@ def ag_qk_norm_rope_fwd(q: torch.Tensor | None, k: torch.Tensor | None,
     ag_rope_frequencies; None: no rotation); positions int64 [L] or [B,L]
     (default 0 .. L-1).  Returns (q_out [B,H,L,D], k_out [B,L,D] or
     [B,Hk,L,D]); q or k may be None."""
-    c = _QkCall(q, k, q_weight, k_weight, q_bias, k_bias, norm, eps, inv_freq, rope, positions)
-    if out_dtype not in DTYPES:
-        raise TypeError(f"out_dtype must be one of {', '.join(map(str, DTYPES))}, got {out_dtype}")
-    with _site(c.dev, stream):
-        outs, ptrs = [q_out, k_out], [None, None]
-        for i, (t, name) in enumerate(((q, "q_out"), (k, "k_out"))):
-            if t is None:
-                outs[i] = None
-                continue
-            if outs[i] is None:
-                outs[i] = torch.empty(c.layout(i), dtype=out_dtype, device=c.dev)
-            ptrs[i] = c.dense(outs[i], name, (out_dtype,), i)
-        _one_device(*c.used)
-        st = lib.ag_qk_norm_rope_fwd(*c.inputs, DTYPES[c.T], c.weights[0], c.biases[0],
-                                     c.weights[1], c.biases[1], c.norm, c.eps, *c.rotation,
-                                     *c.sizes, *ptrs, DTYPES[out_dtype], _current(c.dev))
+    first, T, dev, B, L, D = _qk_first(q, k)
+    if _elsewhere(dev, stream):
+        with _site(dev, stream):
+            return ag_qk_norm_rope_fwd(q, k, q_weight, k_weight, q_bias, k_bias, norm, eps,
+                                       inv_freq, rope, positions, out_dtype, q_out, k_out)
+    Hq, qp, qb, ql, qh = _NO_HEADS if q is None else _heads(q, "q", T, B, L, D, dev)
+    Hk, kp, kb, kl, kh = _NO_HEADS if k is None else _heads(k, "k", T, B, L, D, dev)
+    ot = _code(DTYPES, out_dtype, "out_dtype")
+    qo = ko = None
+    if q is None:
+        q_out = None
+    else:
+        shape = (B, Hq, L, D) if q.ndim == 4 else (B, L, D)
+        if q_out is None:
+            q_out = first.new_empty(shape, dtype=out_dtype)
+            qo = q_out.data_ptr()
+        else:
+            qo = _dense(q_out, "q_out", out_dtype, shape, dev)
+    if k is None:
+        k_out = None
+    else:
+        shape = (B, Hk, L, D) if k.ndim == 4 else (B, L, D)
+        if k_out is None:
+            k_out = first.new_empty(shape, dtype=out_dtype)
+            ko = k_out.data_ptr()
+        else:
+            ko = _dense(k_out, "k_out", out_dtype, shape, dev)
+    st = lib.ag_qk_norm_rope_fwd(
+        qp, qb, ql, qh, kp, kb, kl, kh, DTYPES[T], _vector(q_weight, "q_weight", D, dev),
+        _vector(q_bias, "q_bias", D, dev), _vector(k_weight, "k_weight", D, dev),
+        _vector(k_bias, "k_bias", D, dev), _code(NORMS, norm, "norm"), eps,
+        *_rotation(inv_freq, rope, positions, B, L, dev), B, Hq, Hk, L, D, qo, ko, ot,
+        _current(dev))
     if st != AG_OK:
         raise AgError("ag_qk_norm_rope_fwd", st)
-    return outs[0], outs[1]
+    return q_out, k_out
+
+
+def _dense(t, name: str, dtype, shape: tuple, dev: torch.device) -> int:
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape \
+            and t.device == dev and t.is_contiguous():
+        return t.data_ptr()
+    _on_gpu(t, name, (dtype,))
+    _same_device(t, name, dev)
+    raise ValueError(f"{name} must be a contiguous {list(shape)}, got {list(t.shape)}")
 
 
 def ag_qk_norm_rope_bwd(dq_out: torch.Tensor | None, dk_out: torch.Tensor | None,
@@ -708,37 +727,57 @@ def ag_qk_norm_rope_bwd(dq_out: torch.Tensor | None, dk_out: torch.Tensor | None
     written into the tensors given (which may be slices of one fused
     projection's gradient) or new ones; the others [D] fp32, None where the
     forward had none."""
-    c = _QkCall(q, k, q_weight, k_weight, q_bias, k_bias, norm, eps, inv_freq, rope, positions)
-    g_dtype = next((t.dtype for t in (dq_out, dk_out) if isinstance(t, torch.Tensor)), None)
-    ups = [None if t is None else c.dense(g, name, (g_dtype,), i)
-           for i, (t, g, name) in enumerate(((q, dq_out, "dq_out"), (k, dk_out, "dk_out")))]
-    gt = _code(DTYPES, g_dtype, "the type of dq_out and dk_out")
-    with _site(c.dev, stream):
-        grads, outs = [dq, dk], []
-        for i, (t, name) in enumerate(((q, "dq"), (k, "dk"))):
-            if t is None:
-                grads[i] = None
-                outs += [None, 0, 0, 0]
-                continue
-            if grads[i] is None:
-                grads[i] = torch.empty(tuple(t.shape), dtype=c.T, device=c.dev)
-            if grads[i].dim() != t.dim():
-                raise ValueError(f"{name} must have the shape of {name[1:]}")
-            _, strides = _heads(grads[i], name, (c.T,), B=c.B, L=c.L, H=c.H[i], D=c.D)
-            outs += [grads[i].data_ptr(), *strides]
-            c.used.append(grads[i])
-        params = [None if t is None else torch.empty(c.D, dtype=torch.float32, device=c.dev)
-                  for t in (q_weight, q_bias, k_weight, k_bias)]
-        _one_device(*c.used)
+    first, T, dev, B, L, D = _qk_first(q, k)
+    if _elsewhere(dev, stream):
+        with _site(dev, stream):
+            return ag_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, q_bias, k_bias,
+                                       norm, eps, inv_freq, rope, positions, dq, dk)
+    Hq, qp, qb, ql, qh = _NO_HEADS if q is None else _heads(q, "q", T, B, L, D, dev)
+    Hk, kp, kb, kl, kh = _NO_HEADS if k is None else _heads(k, "k", T, B, L, D, dev)
+    g = dq_out if q is not None else dk_out
+    G = g.dtype if isinstance(g, torch.Tensor) else None
+    gt = _code(DTYPES, G, "the type of dq_out and dk_out")
+    gq = gk = None
+    (_, dqp, dqb, dql, dqh), (_, dkp, dkb, dkl, dkh) = _NO_HEADS, _NO_HEADS
+    if q is None:
+        dq = None
+    else:
+        gq = _dense(dq_out, "dq_out", G, (B, Hq, L, D) if q.ndim == 4 else (B, L, D), dev)
+        if dq is None:
+            dq = first.new_empty(q.shape)
+        elif dq.shape != q.shape:
+            raise ValueError(f"dq must be {list(q.shape)}, got {list(dq.shape)}")
+        _, dqp, dqb, dql, dqh = _heads(dq, "dq", T, B, L, D, dev)
+    if k is None:
+        dk = None
+    else:
+        gk = _dense(dk_out, "dk_out", G, (B, Hk, L, D) if k.ndim == 4 else (B, L, D), dev)
+        if dk is None:
+            dk = first.new_empty(k.shape)
+        elif dk.shape != k.shape:
+            raise ValueError(f"dk must be {list(k.shape)}, got {list(dk.shape)}")
+        _, dkp, dkb, dkl, dkh = _heads(dk, "dk", T, B, L, D, dev)
+    inputs = (q_weight, k_weight, q_bias, k_bias)
+    used = [_vector(t, n, D, dev) for t, n in zip(inputs, ("q_weight", "k_weight", "q_bias",
+                                                           "k_bias"))]
+    wanted = sum(t is not None for t in inputs)
+    params, p = [None] * 4, [None] * 4
+    ws = wsp = None
+    n = 0
+    if wanted:
+        rows = iter(torch.empty((wanted, D), dtype=torch.float32, device=dev).unbind(0))
+        params = [None if t is None else next(rows) for t in inputs]
         p = [None if t is None else t.data_ptr() for t in params]
-        ws, wsp, n = _workspace(lib.ag_qk_norm_rope_bwd_workspace, c.dev,
-                                "ag_qk_norm_rope_bwd_workspace", c.B, c.L, c.D,
-                                int(any(p)))
-        st = lib.ag_qk_norm_rope_bwd(*ups, gt, *c.inputs, DTYPES[c.T], *c.weights, c.norm, c.eps,
-                                     *c.rotation, *c.sizes, *outs, *p, wsp, n, _current(c.dev))
+        ws, wsp, n = _workspace(lib.ag_qk_norm_rope_bwd_workspace, dev,
+                                "ag_qk_norm_rope_bwd_workspace", B, L, D, 1)
+    st = lib.ag_qk_norm_rope_bwd(
+        gq, gk, gt, qp, qb, ql, qh, kp, kb, kl, kh, DTYPES[T], used[0], used[1],
+        _code(NORMS, norm, "norm"), eps, *_rotation(inv_freq, rope, positions, B, L, dev), B, Hq,
+        Hk, L, D, dqp, dqb, dql, dqh, dkp, dkb, dkl, dkh, p[0], p[2], p[1], p[3], wsp, n,
+        _current(dev))
     if st != AG_OK:
         raise AgError("ag_qk_norm_rope_bwd", st)
-    return grads[0], grads[1], params[0], params[2], params[1], params[3]
+    return dq, dk, params[0], params[1], params[2], params[3]
 
 
 def _is_dense(t: torch.Tensor) -> bool:
@@ -765,28 +804,36 @@ def ag_grad_clip(grads, max_norm: float, eps: float = 1e-6,
     grads = [g for g in grads if g is not None]
     if not grads:
         raise ValueError("grads has no tensor")
-    for g in grads:
-        if not (isinstance(g, torch.Tensor) and g.is_cuda and g.dtype in DTYPES
-                and g.layout == torch.strided and g.is_contiguous()):
+    _on_gpu(grads[0], "every gradient", DTYPES)
+    dev = grads[0].device
+    if _elsewhere(dev, stream):
+        with _site(dev, stream):
+            return ag_grad_clip(grads, max_norm, eps, norm)
+    n, index = len(grads), dev.index
+    try:
+        types = [DTYPES[g.dtype] for g in grads]
+        well = all([g.get_device() == index and g.is_contiguous() for g in grads])
+    except (AttributeError, KeyError, RuntimeError):
+        well = False
+    if not well:
+        for g in grads:
             _on_gpu(g, "every gradient", DTYPES)
+            _same_device(g, "one", dev)
             if g.layout != torch.strided or not _is_dense(g):
                 raise ValueError("every gradient must be dense")
-    n = len(grads)
-    dev = grads[0].device if norm is None else _one_device(grads[0], norm)
-    if len({g.get_device() for g in grads}) > 1:
-        _one_device(*grads)
     ptrs = (ctypes.c_void_p * n)(*[g.data_ptr() for g in grads])
     counts = (ctypes.c_int64 * n)(*[g.numel() for g in grads])
-    types = (ctypes.c_int * n)(*[DTYPES[g.dtype] for g in grads])
-    with _site(dev, stream):
-        if norm is None:
-            norm = torch.empty((), dtype=torch.float32, device=dev)
+    codes = (ctypes.c_int * n)(*types)
+    if norm is None:
+        norm = torch.empty((), dtype=torch.float32, device=dev)
+    else:
         _on_gpu(norm, "norm", (torch.float32,))
+        _same_device(norm, "norm", dev)
         if norm.numel() != 1:
             raise ValueError("norm must have one element")
-        ws, wsp, size = _workspace(lib.ag_grad_clip_workspace, dev, "ag_grad_clip_workspace", n)
-        st = lib.ag_grad_clip(ptrs, counts, types, n, float(max_norm), float(eps),
-                              norm.data_ptr(), wsp, size, _current(dev))
+    ws, wsp, size = _workspace(lib.ag_grad_clip_workspace, dev, "ag_grad_clip_workspace", n)
+    st = lib.ag_grad_clip(ptrs, counts, codes, n, max_norm, eps, norm.data_ptr(), wsp, size,
+                          _current(dev))
     if st != AG_OK:
         raise AgError("ag_grad_clip", st)
     return norm

@@ -18,14 +18,17 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kChunk = 16384;         // elements
-constexpr int kMaxTensors = 512;      // per launch: the list travels as a kernel argument
+// Tensors per launch: the list travels as a kernel argument.  A list of 32
+// (0.7 KB) launches faster than one of 512 (10.8 KB); measured below.
+constexpr int kFewTensors = 32, kMaxTensors = 512;
 constexpr int kBlocksPerSm = 4;
 
+template <int MOST>
 struct TensorList {
-  void *ptr[kMaxTensors];
-  int64_t count[kMaxTensors];
-  uint32_t first[kMaxTensors + 1];    // first chunk of each tensor
-  uint8_t dtype[kMaxTensors];
+  void *ptr[MOST];
+  int64_t count[MOST];
+  uint32_t first[MOST + 1];           // first chunk of each tensor
+  uint8_t dtype[MOST];
   int n;
 };
 
@@ -34,7 +37,8 @@ struct Chunk {
   int64_t at;
   int len, dtype;
 };
-__device__ __forceinline__ Chunk chunk_of(const TensorList &list, uint32_t c) {
+template <int MOST>
+__device__ __forceinline__ Chunk chunk_of(const TensorList<MOST> &list, uint32_t c) {
   int lo = 0, hi = list.n;            // first[lo] <= c < first[hi]
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -71,8 +75,9 @@ __device__ __forceinline__ double block_sum(double s) {
   return t;
 }
 
+template <int MOST>
 __global__ void __launch_bounds__(kThreads)
-    square_sum_kernel(const __grid_constant__ TensorList list, double *partial) {
+    square_sum_kernel(const __grid_constant__ TensorList<MOST> list, double *partial) {
   double s = 0.0;
   for (uint32_t c = blockIdx.x; c < list.first[list.n]; c += gridDim.x) {
     const Chunk k = chunk_of(list, c);
@@ -108,8 +113,9 @@ __global__ void __launch_bounds__(kThreads)
   if (threadIdx.x == 0) *total = t;
 }
 
+template <int MOST>
 __global__ void __launch_bounds__(kThreads)
-    scale_kernel(const __grid_constant__ TensorList list, const double *partial, int slots,
+    scale_kernel(const __grid_constant__ TensorList<MOST> list, const double *partial, int slots,
                  float max_norm, float eps, float *norm_out) {
   const double norm = sqrt(total_of(partial, slots));
   if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = static_cast<float>(norm);
@@ -145,13 +151,14 @@ __global__ void __launch_bounds__(kThreads)
 // Takes tensors [from, n) that are not empty into `list` up to its capacity;
 // returns the next index.  The entry point's limits (2^42 elements, 2^20
 // tensors) keep the chunks of a launch below 2^29.
-int64_t fill(TensorList &list, void *const *grads, const int64_t *counts, const int *dtypes,
+template <int MOST>
+int64_t fill(TensorList<MOST> &list, void *const *grads, const int64_t *counts, const int *dtypes,
              int64_t from, int64_t n) {
   list.n = 0;
   list.first[0] = 0;
   int64_t chunks = 0;
   int64_t i = from;
-  for (; i < n && list.n < kMaxTensors; ++i) {
+  for (; i < n && list.n < MOST; ++i) {
     if (counts[i] == 0) continue;
     list.ptr[list.n] = grads[i];
     list.count[list.n] = counts[i];
@@ -170,11 +177,13 @@ int64_t grad_clip_workspace(int64_t n, int num_sms) {
   return (launches * num_sms * kBlocksPerSm + 1) * static_cast<int64_t>(sizeof(double));
 }
 
-cudaError_t launch_grad_clip(void *const *grads, const int64_t *counts, const int *dtypes,
-                             int64_t n, float max_norm, float eps, float *norm_out,
-                             double *workspace, int num_sms, cudaStream_t stream) {
-  const int most = num_sms * kBlocksPerSm;
-  TensorList list;
+namespace {
+
+template <int MOST>
+cudaError_t clip(void *const *grads, const int64_t *counts, const int *dtypes, int64_t n,
+                 float max_norm, float eps, float *norm_out, double *workspace, int most,
+                 cudaStream_t stream) {
+  TensorList<MOST> list;
   int slots = 0, launches = 0;
   for (int64_t i = 0; i < n;) {
     i = fill(list, grads, counts, dtypes, i, n);
@@ -199,7 +208,8 @@ cudaError_t launch_grad_clip(void *const *grads, const int64_t *counts, const in
   int64_t i = 0;
   bool first = true;
   do {
-    i = fill(list, grads, counts, dtypes, i, n);
+    if (launches != 1) i = fill(list, grads, counts, dtypes, i, n);
+    else i = n;  // the list still holds them all
     if (list.n == 0 && !first) break;
     const unsigned chunks = list.first[list.n];
     int blocks = chunks < static_cast<unsigned>(most) ? static_cast<int>(chunks) : most;
@@ -211,6 +221,18 @@ cudaError_t launch_grad_clip(void *const *grads, const int64_t *counts, const in
     first = false;
   } while (i < n && !std::isinf(max_norm));
   return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t launch_grad_clip(void *const *grads, const int64_t *counts, const int *dtypes,
+                             int64_t n, float max_norm, float eps, float *norm_out,
+                             double *workspace, int num_sms, cudaStream_t stream) {
+  const int most = num_sms * kBlocksPerSm;
+  return n <= kFewTensors ? clip<kFewTensors>(grads, counts, dtypes, n, max_norm, eps, norm_out,
+                                              workspace, most, stream)
+                          : clip<kMaxTensors>(grads, counts, dtypes, n, max_norm, eps, norm_out,
+                                              workspace, most, stream);
 }
 
 }  // namespace ag

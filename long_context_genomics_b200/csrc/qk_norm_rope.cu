@@ -97,42 +97,66 @@ __device__ __forceinline__ void row_stats(const float *row, int D, int norm, flo
 // --------------------------------------------------------------------------
 // Rows kernels.
 
-__device__ __forceinline__ float4 load4(const void *p, int64_t at, int dtype) {
-  if (dtype == AG_F32) return *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + at);
-  const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p) + at);
-  if (dtype == AG_BF16)
-    return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u),
-                       __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xFFFF0000u));
-  const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&w.x));
-  const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&w.y));
-  return make_float4(a.x, a.y, b.x, b.y);
-}
-__device__ __forceinline__ void store4(void *p, int64_t at, int dtype, float4 v) {
-  if (dtype == AG_F32) {
-    *reinterpret_cast<float4 *>(static_cast<float *>(p) + at) = v;
-    return;
-  }
-  uint2 w;
-  if (dtype == AG_BF16) {
-    w.x = pack_bf16x2(v.x, v.y), w.y = pack_bf16x2(v.z, v.w);
-  } else {
-    const __half2 a = __floats2half2_rn(v.x, v.y), b = __floats2half2_rn(v.z, v.w);
-    w.x = *reinterpret_cast<const uint32_t *>(&a), w.y = *reinterpret_cast<const uint32_t *>(&b);
-  }
-  *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p) + at) = w;
-}
-
-// A lane's eight elements of a row: two quads, at a and b.
+// A lane's eight elements of a row, two quads at a and b, as loaded (WIDE:
+// float32) and as numbers.  Loading and widening are apart so that nothing
+// waits for a load before all of them have been issued.
+template <bool WIDE>
+struct Raw;
+template <>
+struct Raw<true> {
+  float4 a, b;
+};
+template <>
+struct Raw<false> {
+  uint2 a, b;
+};
 struct Eight {
   float v[8];
 };
-__device__ __forceinline__ Eight load8(const void *p, int64_t row, int a, int b, int dtype) {
-  const float4 x = load4(p, row + a, dtype), y = load4(p, row + b, dtype);
-  return {{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w}};
+
+template <bool WIDE>
+__device__ __forceinline__ Raw<WIDE> load8(const void *p, int64_t row, int a, int b) {
+  if constexpr (WIDE) {
+    const float *q = static_cast<const float *>(p) + row;
+    return {*reinterpret_cast<const float4 *>(q + a), *reinterpret_cast<const float4 *>(q + b)};
+  } else {
+    const uint16_t *q = static_cast<const uint16_t *>(p) + row;
+    return {*reinterpret_cast<const uint2 *>(q + a), *reinterpret_cast<const uint2 *>(q + b)};
+  }
 }
-__device__ __forceinline__ void store8(void *p, int64_t row, int a, int b, int dtype, const Eight &e) {
-  store4(p, row + a, dtype, make_float4(e.v[0], e.v[1], e.v[2], e.v[3]));
-  store4(p, row + b, dtype, make_float4(e.v[4], e.v[5], e.v[6], e.v[7]));
+__device__ __forceinline__ float2 widen2(uint32_t w, bool bf16) {
+  if (bf16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+}
+template <bool WIDE>
+__device__ __forceinline__ Eight widen(const Raw<WIDE> &r, bool bf16) {
+  if constexpr (WIDE) {
+    return {{r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w}};
+  } else {
+    const float2 p = widen2(r.a.x, bf16), q = widen2(r.a.y, bf16), s = widen2(r.b.x, bf16),
+                 t = widen2(r.b.y, bf16);
+    return {{p.x, p.y, q.x, q.y, s.x, s.y, t.x, t.y}};
+  }
+}
+__device__ __forceinline__ uint32_t narrow2(float x, float y, bool bf16) {
+  if (bf16) return pack_bf16x2(x, y);
+  const __half2 h = __floats2half2_rn(x, y);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+template <bool WIDE>
+__device__ __forceinline__ void store8(void *p, int64_t row, int a, int b, const Eight &e, bool bf16) {
+  const float *v = e.v;
+  if constexpr (WIDE) {
+    float *q = static_cast<float *>(p) + row;
+    *reinterpret_cast<float4 *>(q + a) = make_float4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<float4 *>(q + b) = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+    uint16_t *q = static_cast<uint16_t *>(p) + row;
+    *reinterpret_cast<uint2 *>(q + a) =
+        make_uint2(narrow2(v[0], v[1], bf16), narrow2(v[2], v[3], bf16));
+    *reinterpret_cast<uint2 *>(q + b) =
+        make_uint2(narrow2(v[4], v[5], bf16), narrow2(v[6], v[7], bf16));
+  }
 }
 // Sum over the LPR lanes of a row.
 template <int LPR>
@@ -191,14 +215,14 @@ __device__ __forceinline__ void warp_angles(const QkArgs &a, float2 *cs, int64_t
 
 // n = (x - mean) r in place; r.
 template <int LPR>
-__device__ __forceinline__ float normalise(Eight &e, const QkArgs &a, bool in) {
+__device__ __forceinline__ float normalise(Eight &e, const QkArgs &a, float inv_d, bool in) {
   if (a.norm == AG_NORM_NONE) return 1.f;
   float mean = 0.f;
   if (a.norm == AG_NORM_LAYER) {
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) s += e.v[i];
-    mean = row_sum<LPR>(s) / a.D;
+    mean = row_sum<LPR>(s) * inv_d;
   }
   float q = 0.f;
 #pragma unroll
@@ -206,22 +230,25 @@ __device__ __forceinline__ float normalise(Eight &e, const QkArgs &a, bool in) {
     e.v[i] = in ? e.v[i] - mean : 0.f;
     q = fmaf(e.v[i], e.v[i], q);
   }
-  const float r = 1.f / sqrtf(row_sum<LPR>(q) / a.D + a.eps);
+  const float r = 1.f / sqrtf(fmaf(row_sum<LPR>(q), inv_d, a.eps));
 #pragma unroll
   for (int i = 0; i < 8; ++i) e.v[i] *= r;
   return r;
 }
 
-template <int LPR>
+template <int LPR, bool X32, bool O32>
 __global__ void __launch_bounds__(kThreads, 3) qk_fwd_rows_kernel(const QkArgs a) {
   extern __shared__ float smem[];
   constexpr int kAtOnce = 32 / LPR, kSteps = 4;  // rows per step; steps loaded together
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   float2 *cs = reinterpret_cast<float2 *>(smem) + warp * (a.R / 2);
   const Lane t = lane_of<LPR>(lane, a.D, a.R, a.rope);
-  for (int64_t pos = static_cast<int64_t>(blockIdx.x) * kWarps + warp; pos < a.positions_total;
-       pos += static_cast<int64_t>(gridDim.x) * kWarps) {
-    const int64_t b = pos / a.L, l = pos - b * a.L;
+  const float inv_d = 1.f / a.D;
+  const bool x_bf16 = a.x_dtype == AG_BF16, o_bf16 = a.o_dtype == AG_BF16;
+  const uint32_t L = static_cast<uint32_t>(a.L), total = static_cast<uint32_t>(a.positions_total);
+  for (uint32_t pos = blockIdx.x * kWarps + warp; pos < total; pos += gridDim.x * kWarps) {
+    const uint32_t b32 = pos / L;
+    const int64_t b = b32, l = pos - b32 * L;
     if (a.R) warp_angles(a, cs, b, l, lane);
     const float4 *angles = reinterpret_cast<const float4 *>(cs) + 2 * (lane % LPR);
 #pragma unroll 1
@@ -231,22 +258,23 @@ __global__ void __launch_bounds__(kThreads, 3) qk_fwd_rows_kernel(const QkArgs a
       const Eight w = t.in ? param8(s.w, t.a, t.b, 1.f) : Eight{}, bias = t.in ? param8(s.b, t.a, t.b, 0.f) : Eight{};
 #pragma unroll 1
       for (int h0 = 0; h0 < s.H; h0 += kAtOnce * kSteps) {
-        Eight x[kSteps];
+        Raw<X32> raw[kSteps];
 #pragma unroll
         for (int u = 0; u < kSteps; ++u) {
           const int h = h0 + u * kAtOnce + lane / LPR;
-          x[u] = Eight{};
-          if (t.in && h < s.H) x[u] = load8(s.x, from + h * s.sh, t.a, t.b, a.x_dtype);
+          raw[u] = Raw<X32>{};
+          if (t.in && h < s.H) raw[u] = load8<X32>(s.x, from + h * s.sh, t.a, t.b);
         }
 #pragma unroll
         for (int u = 0; u < kSteps; ++u) {
           if (h0 + u * kAtOnce >= s.H) break;
           const int h = h0 + u * kAtOnce + lane / LPR;
-          normalise<LPR>(x[u], a, t.in);
+          Eight x = widen<X32>(raw[u], x_bf16);
+          normalise<LPR>(x, a, inv_d, t.in);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x[u].v[i] = fmaf(x[u].v[i], w.v[i], bias.v[i]);
-          if (t.turns) turn_pairs(x[u], angles, a.rope, 1.f);
-          if (t.in && h < s.H) store8(s.out, to + h * a.L * a.D, t.a, t.b, a.o_dtype, x[u]);
+          for (int i = 0; i < 8; ++i) x.v[i] = fmaf(x.v[i], w.v[i], bias.v[i]);
+          if (t.turns) turn_pairs(x, angles, a.rope, 1.f);
+          if (t.in && h < s.H) store8<O32>(s.out, to + h * a.L * a.D, t.a, t.b, x, o_bf16);
         }
       }
     }
@@ -258,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 3) qk_fwd_rows_kernel(const QkArgs a
 // shared memory of its own, [w and b of both sides][two quads][lane]; the block
 // adds its lanes' and warps' at the end, in a fixed order, and writes one
 // partial.
-template <int LPR>
+template <int LPR, bool X32, bool G32>
 __global__ void __launch_bounds__(kThreads, 2) qk_bwd_rows_kernel(const QkArgs a) {
   extern __shared__ float smem[];
   constexpr int kAtOnce = 32 / LPR, kSteps = 2;
@@ -271,9 +299,12 @@ __global__ void __launch_bounds__(kThreads, 2) qk_bwd_rows_kernel(const QkArgs a
     for (int q = 0; q < 8; ++q) own[q * 32] = make_float4(0.f, 0.f, 0.f, 0.f);
   const Lane t = lane_of<LPR>(lane, a.D, a.R, a.rope);
   const float4 *angles = reinterpret_cast<const float4 *>(cs) + 2 * (lane % LPR);
-  for (int64_t pos = static_cast<int64_t>(blockIdx.x) * kWarps + warp; pos < a.positions_total;
-       pos += static_cast<int64_t>(gridDim.x) * kWarps) {
-    const int64_t b = pos / a.L, l = pos - b * a.L;
+  const float inv_d = 1.f / a.D;
+  const bool x_bf16 = a.x_dtype == AG_BF16, g_bf16 = a.o_dtype == AG_BF16;
+  const uint32_t L = static_cast<uint32_t>(a.L), total = static_cast<uint32_t>(a.positions_total);
+  for (uint32_t pos = blockIdx.x * kWarps + warp; pos < total; pos += gridDim.x * kWarps) {
+    const uint32_t b32 = pos / L;
+    const int64_t b = b32, l = pos - b32 * L;
     bool angles_ready = a.R == 0;
 #pragma unroll 1
     for (int which = 0; which < 2; ++which) {
@@ -285,14 +316,15 @@ __global__ void __launch_bounds__(kThreads, 2) qk_bwd_rows_kernel(const QkArgs a
       Eight dw{}, db{};
 #pragma unroll 1
       for (int h0 = 0; h0 < s.H; h0 += kAtOnce * kSteps) {
-        Eight x[kSteps], g[kSteps];
+        Raw<X32> raw_x[kSteps];
+        Raw<G32> raw_g[kSteps];
 #pragma unroll
         for (int u = 0; u < kSteps; ++u) {
           const int h = h0 + u * kAtOnce + lane / LPR;
-          x[u] = Eight{}, g[u] = Eight{};
+          raw_x[u] = Raw<X32>{}, raw_g[u] = Raw<G32>{};
           if (t.in && h < s.H) {
-            x[u] = load8(s.x, x_at + h * s.sh, t.a, t.b, a.x_dtype);
-            g[u] = load8(s.g, g_at + h * a.L * a.D, t.a, t.b, a.o_dtype);
+            raw_x[u] = load8<X32>(s.x, x_at + h * s.sh, t.a, t.b);
+            raw_g[u] = load8<G32>(s.g, g_at + h * a.L * a.D, t.a, t.b);
           }
         }
         if (!angles_ready) {  // while the first rows are on their way
@@ -304,24 +336,24 @@ __global__ void __launch_bounds__(kThreads, 2) qk_bwd_rows_kernel(const QkArgs a
           if (h0 + u * kAtOnce >= s.H) break;
           const int h = h0 + u * kAtOnce + lane / LPR;
           const bool mine = t.in && h < s.H;
-          const float r = normalise<LPR>(x[u], a, t.in);
-          if (t.turns) turn_pairs(g[u], angles, a.rope, -1.f);
+          Eight x = widen<X32>(raw_x[u], x_bf16), g = widen<G32>(raw_g[u], g_bf16);
+          const float r = normalise<LPR>(x, a, inv_d, t.in);
+          if (t.turns) turn_pairs(g, angles, a.rope, -1.f);
           float along = 0.f, total = 0.f;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             // (A row of this step past the last head counts for nothing, also
             // when eps is zero and its norm is not a number.)
-            if (mine) dw.v[i] = fmaf(g[u].v[i], x[u].v[i], dw.v[i]), db.v[i] += g[u].v[i];
-            g[u].v[i] *= w.v[i];
-            along = fmaf(g[u].v[i], x[u].v[i], along);
-            total += g[u].v[i];
+            if (mine) dw.v[i] = fmaf(g.v[i], x.v[i], dw.v[i]), db.v[i] += g.v[i];
+            g.v[i] *= w.v[i];
+            along = fmaf(g.v[i], x.v[i], along);
+            total += g.v[i];
           }
-          along = a.norm == AG_NORM_NONE ? 0.f : row_sum<LPR>(along) / a.D;
-          total = a.norm == AG_NORM_LAYER ? row_sum<LPR>(total) / a.D : 0.f;
+          along = a.norm == AG_NORM_NONE ? 0.f : row_sum<LPR>(along) * inv_d;
+          total = a.norm == AG_NORM_LAYER ? row_sum<LPR>(total) * inv_d : 0.f;
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            g[u].v[i] = r * (fmaf(-x[u].v[i], along, g[u].v[i]) - total);
-          if (mine) store8(s.dx, dx_at + h * s.dxh, t.a, t.b, a.x_dtype, g[u]);
+          for (int i = 0; i < 8; ++i) g.v[i] = r * (fmaf(-x.v[i], along, g.v[i]) - total);
+          if (mine) store8<X32>(s.dx, dx_at + h * s.dxh, t.a, t.b, g, x_bf16);
         }
       }
       if (a.partial) {
@@ -527,15 +559,35 @@ int64_t qk_bwd_workspace(int64_t positions_total, int64_t D, int num_sms) {
   return static_cast<int64_t>(bwd_blocks(positions_total, kPos, 4, num_sms)) * 4 * D * 4;
 }
 
+namespace {
+
+using QkKernel = void (*)(QkArgs);
+template <bool X32, bool O32>
+QkKernel rows_kernel(int D, bool backward) {
+  if (backward)
+    return D <= 32    ? qk_bwd_rows_kernel<4, X32, O32>
+           : D <= 64  ? qk_bwd_rows_kernel<8, X32, O32>
+           : D <= 128 ? qk_bwd_rows_kernel<16, X32, O32>
+                      : qk_bwd_rows_kernel<32, X32, O32>;
+  return D <= 32    ? qk_fwd_rows_kernel<4, X32, O32>
+         : D <= 64  ? qk_fwd_rows_kernel<8, X32, O32>
+         : D <= 128 ? qk_fwd_rows_kernel<16, X32, O32>
+                    : qk_fwd_rows_kernel<32, X32, O32>;
+}
+QkKernel rows_kernel(const QkArgs &a, bool backward) {
+  const bool o32 = a.o_dtype == AG_F32;
+  if (a.x_dtype == AG_F32)
+    return o32 ? rows_kernel<true, true>(a.D, backward) : rows_kernel<true, false>(a.D, backward);
+  return o32 ? rows_kernel<false, true>(a.D, backward) : rows_kernel<false, false>(a.D, backward);
+}
+
+}  // namespace
+
 cudaError_t launch_qk_fwd(const QkArgs &a, int num_sms, cudaStream_t stream) {
   if (by_rows(a, false)) {
-    auto *kernel = a.D <= 32    ? qk_fwd_rows_kernel<4>
-                   : a.D <= 64  ? qk_fwd_rows_kernel<8>
-                   : a.D <= 128 ? qk_fwd_rows_kernel<16>
-                                : qk_fwd_rows_kernel<32>;
     const int64_t blocks = (a.positions_total + kWarps - 1) / kWarps;
-    kernel<<<static_cast<unsigned>(blocks < 24 * num_sms ? blocks : 24 * num_sms), kThreads,
-             kWarps * a.R * 4, stream>>>(a);
+    rows_kernel(a, false)<<<static_cast<unsigned>(blocks < 24 * num_sms ? blocks : 24 * num_sms),
+                            kThreads, kWarps * a.R * 4, stream>>>(a);
     return cudaGetLastError();
   }
   const size_t smem = (static_cast<size_t>(kPos) * a.R + kWarps * static_cast<size_t>(a.D)) * 4;
@@ -549,12 +601,8 @@ cudaError_t launch_qk_fwd(const QkArgs &a, int num_sms, cudaStream_t stream) {
 cudaError_t launch_qk_bwd(const QkArgs &a, int num_sms, cudaStream_t stream) {
   int blocks;
   if (by_rows(a, true)) {
-    auto *kernel = a.D <= 32    ? qk_bwd_rows_kernel<4>
-                   : a.D <= 64  ? qk_bwd_rows_kernel<8>
-                   : a.D <= 128 ? qk_bwd_rows_kernel<16>
-                                : qk_bwd_rows_kernel<32>;
     blocks = bwd_blocks(a.positions_total, kWarps, 2, num_sms);
-    kernel<<<blocks, kThreads, kWarps * (a.R + 8 * 32 * 4) * 4, stream>>>(a);
+    rows_kernel(a, true)<<<blocks, kThreads, kWarps * (a.R + 8 * 32 * 4) * 4, stream>>>(a);
   } else {
     const int warps = bwd_warps(a.D);
     blocks = bwd_blocks(a.positions_total, kPos, 4, num_sms);
