@@ -401,8 +401,7 @@ ag_status ag_qk_norm_rope_fwd(const void *q, int64_t q_sb, int64_t q_sl, int64_t
   a.positions_total = B * L, a.B = B, a.L = L;
   a.D = static_cast<int>(D), a.R = static_cast<int>(R);
   a.norm = norm, a.rope = rope, a.x_dtype = x_dtype, a.o_dtype = out_dtype, a.eps = eps;
-  return ag::from_cuda(
-      ag::launch_qk_fwd(a, dev->num_sms, static_cast<cudaStream_t>(stream)));
+  return ag::from_cuda(ag::launch_qk_fwd(a, static_cast<cudaStream_t>(stream)));
 }
 
 ag_status ag_qk_norm_rope_bwd_workspace(int64_t B, int64_t L, int64_t D, int wants_params,

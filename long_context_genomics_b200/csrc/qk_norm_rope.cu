@@ -10,7 +10,7 @@
 // reads x and dout and writes dx).
 //
 // Rows kernels (heads of a multiple of 8 up to 256 elements, at addresses that
-// 4 elements' loads can take): a warp takes one position with all its heads, so
+// 4 elements' loads can take; weights and biases 16-byte aligned): a warp takes one position with all its heads, so
 // that the position's angles are formed once for them, and no other warp waits
 // for it.  A row lies in D / 8 lanes, eight elements each in two quads; where
 // halves are rotated, a lane's quads are 4 elements of the first half and their
@@ -30,16 +30,18 @@ constexpr int kPos = 4;        // positions per block and turn
 constexpr int kThreads = 256;  // 8 warps
 constexpr int kWarps = kThreads / 32;
 
-// cos and sin of position * frequency.  The product and its reduction to one
-// turn are in 64 bits (two-part 2 pi), so the phase of a far position is as
-// exact as the frequency; the reduced angle then goes through float32.
+// cos and sin of position * frequency.  The product and its reduction to
+// [-pi, pi] are in 64 bits (two-part 2 pi), so the phase of a far position is as
+// exact as the frequency; there the special-function unit's sine and cosine are
+// within 2^-21 (CUDA's bound for the fast functions), which a rotated float32
+// value of the row shares.
 __device__ __forceinline__ float2 turn(long long pos, double freq) {
   const double a = static_cast<double>(pos) * freq;
   const double n = rint(a * 0.15915494309189535);
   double r = fma(n, -6.283185307179586, a);
   r = fma(n, -2.4492935982947064e-16, r);
   float s, c;
-  sincospif(static_cast<float>(r * 0.3183098861837907), &s, &c);
+  __sincosf(static_cast<float>(r), &s, &c);
   return make_float2(c, s);
 }
 
@@ -97,185 +99,217 @@ __device__ __forceinline__ void row_stats(const float *row, int D, int norm, flo
 // --------------------------------------------------------------------------
 // Rows kernels.
 
-// A lane's eight elements of a row, two quads at a and b, as loaded (WIDE:
-// float32) and as numbers.  Loading and widening are apart so that nothing
-// waits for a load before all of them have been issued.
-template <bool WIDE>
-struct Raw;
-template <>
-struct Raw<true> {
-  float4 a, b;
-};
-template <>
-struct Raw<false> {
+// A lane's eight elements of a row, as loaded (of type T) from two places
+// and as numbers: four pairs (A[i], B[i]) that turn together, A in v[0] and
+// v[1], B in v[2] and v[3].  HALVES: the first place holds A and the second B;
+// otherwise A are the even and B the odd elements of both.  Loading and
+// widening are apart so that nothing waits for a load before all of them have
+// been issued.
+template <int T>
+struct Raw {
   uint2 a, b;
 };
+template <>
+struct Raw<AG_F32> {
+  float4 a, b;
+};
 struct Eight {
-  float v[8];
+  float2 v[4];
 };
 
-template <bool WIDE>
-__device__ __forceinline__ Raw<WIDE> load8(const void *p, int64_t row, int a, int b) {
-  if constexpr (WIDE) {
-    const float *q = static_cast<const float *>(p) + row;
-    return {*reinterpret_cast<const float4 *>(q + a), *reinterpret_cast<const float4 *>(q + b)};
-  } else {
-    const uint16_t *q = static_cast<const uint16_t *>(p) + row;
-    return {*reinterpret_cast<const uint2 *>(q + a), *reinterpret_cast<const uint2 *>(q + b)};
-  }
+// Bytes of n elements of a type.
+template <int T>
+__device__ __forceinline__ int64_t bytes_of(int64_t n) {
+  return T == AG_F32 ? n * 4 : n * 2;
 }
-__device__ __forceinline__ float2 widen2(uint32_t w, bool bf16) {
-  if (bf16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+// From the row's bytes at p, where the lane's first quad lies; its second is
+// `apart` bytes on.
+template <int T>
+__device__ __forceinline__ Raw<T> load8(const char *p, int apart) {
+  using Quad = decltype(Raw<T>::a);
+  return {*reinterpret_cast<const Quad *>(p), *reinterpret_cast<const Quad *>(p + apart)};
+}
+template <int T>
+__device__ __forceinline__ float2 widen2(uint32_t w) {
+  if constexpr (T == AG_BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
   return __half22float2(*reinterpret_cast<const __half2 *>(&w));
 }
-template <bool WIDE>
-__device__ __forceinline__ Eight widen(const Raw<WIDE> &r, bool bf16) {
-  if constexpr (WIDE) {
-    return {{r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w}};
-  } else {
-    const float2 p = widen2(r.a.x, bf16), q = widen2(r.a.y, bf16), s = widen2(r.b.x, bf16),
-                 t = widen2(r.b.y, bf16);
-    return {{p.x, p.y, q.x, q.y, s.x, s.y, t.x, t.y}};
-  }
+template <bool HALVES>
+__device__ __forceinline__ Eight arrange(float2 p, float2 q, float2 s, float2 t) {
+  if constexpr (HALVES) return {{p, q, s, t}};
+  return {{make_float2(p.x, q.x), make_float2(s.x, t.x), make_float2(p.y, q.y),
+           make_float2(s.y, t.y)}};
 }
-__device__ __forceinline__ uint32_t narrow2(float x, float y, bool bf16) {
-  if (bf16) return pack_bf16x2(x, y);
-  const __half2 h = __floats2half2_rn(x, y);
+template <int T, bool HALVES>
+__device__ __forceinline__ Eight widen(const Raw<T> &r) {
+  if constexpr (T == AG_F32)
+    return arrange<HALVES>(make_float2(r.a.x, r.a.y), make_float2(r.a.z, r.a.w),
+                           make_float2(r.b.x, r.b.y), make_float2(r.b.z, r.b.w));
+  else
+    return arrange<HALVES>(widen2<T>(r.a.x), widen2<T>(r.a.y), widen2<T>(r.b.x), widen2<T>(r.b.y));
+}
+template <int T>
+__device__ __forceinline__ uint32_t narrow2(float2 v) {
+  if constexpr (T == AG_BF16) return pack_bf16x2(v.x, v.y);
+  const __half2 h = __floats2half2_rn(v.x, v.y);
   return *reinterpret_cast<const uint32_t *>(&h);
 }
-template <bool WIDE>
-__device__ __forceinline__ void store8(void *p, int64_t row, int a, int b, const Eight &e, bool bf16) {
-  const float *v = e.v;
-  if constexpr (WIDE) {
-    float *q = static_cast<float *>(p) + row;
-    *reinterpret_cast<float4 *>(q + a) = make_float4(v[0], v[1], v[2], v[3]);
-    *reinterpret_cast<float4 *>(q + b) = make_float4(v[4], v[5], v[6], v[7]);
+template <int T, bool HALVES>
+__device__ __forceinline__ void store8(char *p, int apart, const Eight &e) {
+  float2 o[4] = {e.v[0], e.v[1], e.v[2], e.v[3]};
+  if constexpr (!HALVES) {
+    o[0] = make_float2(e.v[0].x, e.v[2].x), o[1] = make_float2(e.v[0].y, e.v[2].y);
+    o[2] = make_float2(e.v[1].x, e.v[3].x), o[3] = make_float2(e.v[1].y, e.v[3].y);
+  }
+  if constexpr (T == AG_F32) {
+    *reinterpret_cast<float4 *>(p) = make_float4(o[0].x, o[0].y, o[1].x, o[1].y);
+    *reinterpret_cast<float4 *>(p + apart) = make_float4(o[2].x, o[2].y, o[3].x, o[3].y);
   } else {
-    uint16_t *q = static_cast<uint16_t *>(p) + row;
-    *reinterpret_cast<uint2 *>(q + a) =
-        make_uint2(narrow2(v[0], v[1], bf16), narrow2(v[2], v[3], bf16));
-    *reinterpret_cast<uint2 *>(q + b) =
-        make_uint2(narrow2(v[4], v[5], bf16), narrow2(v[6], v[7], bf16));
+    *reinterpret_cast<uint2 *>(p) = make_uint2(narrow2<T>(o[0]), narrow2<T>(o[1]));
+    *reinterpret_cast<uint2 *>(p + apart) = make_uint2(narrow2<T>(o[2]), narrow2<T>(o[3]));
   }
 }
-// Sum over the LPR lanes of a row.
+// Sum over the LPR lanes of a row, of both numbers.
 template <int LPR>
-__device__ __forceinline__ float row_sum(float v) {
+__device__ __forceinline__ float row_sum(float2 v) {
+  float s = v.x + v.y;
 #pragma unroll
-  for (int o = LPR / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+  for (int o = LPR / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return s;
 }
-__device__ __forceinline__ Eight param8(const float *p, int a, int b, float otherwise) {
-  Eight e;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) e.v[i] = p ? __ldg(p + (i < 4 ? a + i : b + i - 4)) : otherwise;
-  return e;
+__device__ __forceinline__ float2 twice(float c) { return make_float2(c, c); }
+__device__ __forceinline__ float2 negated(float2 v) { return make_float2(-v.x, -v.y); }
+__device__ __forceinline__ float2 sum4(const Eight &e) {
+  return __fadd2_rn(__fadd2_rn(e.v[0], e.v[1]), __fadd2_rn(e.v[2], e.v[3]));
 }
 
-// Where a lane's quads lie, and whether they turn.
+// Where a lane's elements lie (two quads, at a and b), and whether they turn.
 struct Lane {
   int a, b;
   bool in, turns;
 };
-template <int LPR>
-__device__ __forceinline__ Lane lane_of(int lane, int D, int R, int rope) {
+template <int LPR, bool HALVES>
+__device__ __forceinline__ Lane lane_of(int lane, int D, int R) {
   const int l = lane % LPR;
   Lane t;
   t.in = 8 * l < D;
   t.turns = 8 * l < R;
-  if (rope == AG_ROPE_HALVES && t.turns)
+  if (HALVES && t.turns)
     t.a = 4 * l, t.b = R / 2 + 4 * l;
   else
     t.a = 8 * l, t.b = 8 * l + 4;
   return t;
 }
-// The lane's four pairs turned by the position's angles; sign -1: back.
-__device__ __forceinline__ void turn_pairs(Eight &e, const float4 *cs, int rope, float sign) {
-  const float4 p = cs[0], q = cs[1];  // (cos, sin) of four angles
-  const float c[4] = {p.x, p.z, q.x, q.z};
-  const float s[4] = {sign * p.y, sign * p.w, sign * q.y, sign * q.w};
-  const bool halves = rope == AG_ROPE_HALVES;
+// The lane's part of a weight or bias, where there is one.
+template <bool HALVES>
+__device__ __forceinline__ Eight param8(const float *p, const Lane &t, float otherwise) {
+  if (!p || !t.in) {
+    const float2 c = twice(t.in ? otherwise : 0.f);
+    return {{c, c, c, c}};
+  }
+  const float4 x = __ldg(reinterpret_cast<const float4 *>(p + t.a));
+  const float4 y = __ldg(reinterpret_cast<const float4 *>(p + t.b));
+  return arrange<HALVES>(make_float2(x.x, x.y), make_float2(x.z, x.w), make_float2(y.x, y.y),
+                         make_float2(y.z, y.w));
+}
+// The lane's four pairs turned by the position's angles; BACK: the other way.
+template <bool BACK>
+__device__ __forceinline__ void turn_pairs(Eight &e, const float4 *cos4, const float4 *sin4) {
+  const float4 c = *cos4, s = *sin4;
+  const float2 cs[2] = {make_float2(c.x, c.y), make_float2(c.z, c.w)};
+  const float2 sn[2] = {make_float2(s.x, s.y), make_float2(s.z, s.w)};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float x = halves ? e.v[i] : e.v[2 * i], y = halves ? e.v[i + 4] : e.v[2 * i + 1];
-    const float u = fmaf(x, c[i], -y * s[i]), w = fmaf(y, c[i], x * s[i]);
-    if (halves) e.v[i] = u, e.v[i + 4] = w;
-    else e.v[2 * i] = u, e.v[2 * i + 1] = w;
+  for (int i = 0; i < 2; ++i) {
+    const float2 x = e.v[i], y = e.v[i + 2], p = __fmul2_rn(y, sn[i]), q = __fmul2_rn(x, sn[i]);
+    e.v[i] = __ffma2_rn(x, cs[i], BACK ? p : negated(p));
+    e.v[i + 2] = __ffma2_rn(y, cs[i], BACK ? negated(q) : q);
   }
 }
 
-// The position's angles into the warp's own shared memory.
-__device__ __forceinline__ void warp_angles(const QkArgs &a, float2 *cs, int64_t b, int64_t l,
-                                            int lane) {
+// The angles of the group's position into its own shared memory: R / 2 cosines,
+// then as many sines.
+template <int LPR>
+__device__ __forceinline__ void group_angles(const QkArgs &a, float *cs, int64_t b, int64_t l,
+                                             int lane) {
   __syncwarp();
   const long long pos = a.positions ? a.positions[b * a.pos_sb + l] : l;
-  for (int i = lane; i < a.R / 2; i += 32) cs[i] = turn(pos, a.inv_freq[i]);
+  const int half = a.R / 2;
+  for (int i = lane % LPR; i < half; i += LPR) {
+    const float2 c = turn(pos, a.inv_freq[i]);
+    cs[i] = c.x, cs[half + i] = c.y;
+  }
   __syncwarp();
 }
 
-// n = (x - mean) r in place; r.
+// n = (x - mean) r in place; r.  Lanes without elements hold zeros.
 template <int LPR>
-__device__ __forceinline__ float normalise(Eight &e, const QkArgs &a, float inv_d, bool in) {
+__device__ __forceinline__ float normalise(Eight &e, const QkArgs &a, float inv_d, bool mine) {
   if (a.norm == AG_NORM_NONE) return 1.f;
-  float mean = 0.f;
   if (a.norm == AG_NORM_LAYER) {
-    float s = 0.f;
+    const float sum = row_sum<LPR>(sum4(e));
+    const float2 mean = twice(mine ? -sum * inv_d : 0.f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s += e.v[i];
-    mean = row_sum<LPR>(s) * inv_d;
+    for (int i = 0; i < 4; ++i) e.v[i] = __fadd2_rn(e.v[i], mean);
   }
-  float q = 0.f;
+  float2 q = __fmul2_rn(e.v[0], e.v[0]);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    e.v[i] = in ? e.v[i] - mean : 0.f;
-    q = fmaf(e.v[i], e.v[i], q);
-  }
-  const float r = 1.f / sqrtf(fmaf(row_sum<LPR>(q), inv_d, a.eps));
+  for (int i = 1; i < 4; ++i) q = __ffma2_rn(e.v[i], e.v[i], q);
+  // (A group past the last position counts for nothing, also when eps is zero.)
+  float r = __frsqrt_rn(fmaf(row_sum<LPR>(q), inv_d, a.eps));
+  if (!mine) r = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) e.v[i] *= r;
+  for (int i = 0; i < 4; ++i) e.v[i] = __fmul2_rn(e.v[i], twice(r));
   return r;
 }
 
-template <int LPR, bool X32, bool O32>
-__global__ void __launch_bounds__(kThreads, 3) qk_fwd_rows_kernel(const QkArgs a) {
+template <int LPR, int XT, int OT, bool HALVES>
+__global__ void __launch_bounds__(kThreads, 4) qk_fwd_rows_kernel(const QkArgs a) {
   extern __shared__ float smem[];
-  constexpr int kAtOnce = 32 / LPR, kSteps = 4;  // rows per step; steps loaded together
+  constexpr int kGroups = 32 / LPR, kRows = 4;   // positions per warp; rows loaded together
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  float2 *cs = reinterpret_cast<float2 *>(smem) + warp * (a.R / 2);
-  const Lane t = lane_of<LPR>(lane, a.D, a.R, a.rope);
+  float *cs = smem + (warp * kGroups + lane / LPR) * a.R;
+  const float4 *cos4 = reinterpret_cast<const float4 *>(cs) + lane % LPR, *sin4 = cos4 + a.R / 8;
+  const Lane t = lane_of<LPR, HALVES>(lane, a.D, a.R);
   const float inv_d = 1.f / a.D;
-  const bool x_bf16 = a.x_dtype == AG_BF16, o_bf16 = a.o_dtype == AG_BF16;
+  const int x_apart = static_cast<int>(bytes_of<XT>(t.b - t.a)),
+            o_apart = static_cast<int>(bytes_of<OT>(t.b - t.a));
   const uint32_t L = static_cast<uint32_t>(a.L), total = static_cast<uint32_t>(a.positions_total);
-  for (uint32_t pos = blockIdx.x * kWarps + warp; pos < total; pos += gridDim.x * kWarps) {
-    const uint32_t b32 = pos / L;
-    const int64_t b = b32, l = pos - b32 * L;
-    if (a.R) warp_angles(a, cs, b, l, lane);
-    const float4 *angles = reinterpret_cast<const float4 *>(cs) + 2 * (lane % LPR);
+  const uint32_t first = (blockIdx.x * kWarps + warp) * kGroups;  // the warp's first position
+  if (first >= total) return;
+  const uint32_t pos = min(first + lane / LPR, total - 1);
+  const bool mine = t.in && first + lane / LPR < total;
+  const int64_t b = pos / L, l = pos % L;
+  bool angles_ready = a.R == 0;
 #pragma unroll 1
-    for (int which = 0; which < 2; ++which) {
-      const QkSide &s = a.side[which];
-      const int64_t from = b * s.sb + l * s.sl, to = (b * s.H * a.L + l) * a.D;
-      const Eight w = t.in ? param8(s.w, t.a, t.b, 1.f) : Eight{}, bias = t.in ? param8(s.b, t.a, t.b, 0.f) : Eight{};
+  for (int which = 0; which < 2; ++which) {
+    const QkSide &s = a.side[which];
+    const char *x_at = static_cast<const char *>(s.x) + bytes_of<XT>(b * s.sb + l * s.sl + t.a);
+    char *o_at = static_cast<char *>(s.out) + bytes_of<OT>((b * s.H * a.L + l) * a.D + t.a);
+    const int64_t x_step = bytes_of<XT>(s.sh), o_step = bytes_of<OT>(a.L * a.D);
+    const Eight w = param8<HALVES>(s.w, t, 1.f), bias = param8<HALVES>(s.b, t, 0.f);
 #pragma unroll 1
-      for (int h0 = 0; h0 < s.H; h0 += kAtOnce * kSteps) {
-        Raw<X32> raw[kSteps];
+    for (int left = s.H; left > 0; left -= kRows) {
+      Raw<XT> raw[kRows];
 #pragma unroll
-        for (int u = 0; u < kSteps; ++u) {
-          const int h = h0 + u * kAtOnce + lane / LPR;
-          raw[u] = Raw<X32>{};
-          if (t.in && h < s.H) raw[u] = load8<X32>(s.x, from + h * s.sh, t.a, t.b);
-        }
+      for (int u = 0; u < kRows; ++u) {
+        raw[u] = Raw<XT>{};
+        if (mine && u < left) raw[u] = load8<XT>(x_at, x_apart);
+        x_at += x_step;
+      }
+      if (!angles_ready) {  // while the first rows are on their way
+        group_angles<LPR>(a, cs, b, l, lane);
+        angles_ready = true;
+      }
 #pragma unroll
-        for (int u = 0; u < kSteps; ++u) {
-          if (h0 + u * kAtOnce >= s.H) break;
-          const int h = h0 + u * kAtOnce + lane / LPR;
-          Eight x = widen<X32>(raw[u], x_bf16);
-          normalise<LPR>(x, a, inv_d, t.in);
+      for (int u = 0; u < kRows; ++u) {
+        if (u >= left) break;
+        Eight x = widen<XT, HALVES>(raw[u]);
+        normalise<LPR>(x, a, inv_d, mine);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x.v[i] = fmaf(x.v[i], w.v[i], bias.v[i]);
-          if (t.turns) turn_pairs(x, angles, a.rope, 1.f);
-          if (t.in && h < s.H) store8<O32>(s.out, to + h * a.L * a.D, t.a, t.b, x, o_bf16);
-        }
+        for (int i = 0; i < 4; ++i) x.v[i] = __ffma2_rn(x.v[i], w.v[i], bias.v[i]);
+        if (t.turns) turn_pairs<false>(x, cos4, sin4);
+        if (mine) store8<OT, HALVES>(o_at, o_apart, x);
+        o_at += o_step;
       }
     }
   }
@@ -283,86 +317,96 @@ __global__ void __launch_bounds__(kThreads, 3) qk_fwd_rows_kernel(const QkArgs a
 
 // Backward.  A lane's elements are the same in every row it meets, so it sums
 // the parameter gradients of a position's heads in registers and adds them to
-// shared memory of its own, [w and b of both sides][two quads][lane]; the block
+// shared memory of its own, [w and b of both sides][A and B][lane]; the block
 // adds its lanes' and warps' at the end, in a fixed order, and writes one
 // partial.
-template <int LPR, bool X32, bool G32>
+template <int LPR, int XT, int GT, bool HALVES>
 __global__ void __launch_bounds__(kThreads, 2) qk_bwd_rows_kernel(const QkArgs a) {
   extern __shared__ float smem[];
-  constexpr int kAtOnce = 32 / LPR, kSteps = 2;
+  constexpr int kGroups = 32 / LPR, kRows = 2;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  float2 *cs = reinterpret_cast<float2 *>(smem) + warp * (a.R / 2);
-  float4 *sums = reinterpret_cast<float4 *>(smem + kWarps * a.R);  // [kWarps][8][32]
+  float *cs = smem + (warp * kGroups + lane / LPR) * a.R;
+  const float4 *cos4 = reinterpret_cast<const float4 *>(cs) + lane % LPR, *sin4 = cos4 + a.R / 8;
+  float4 *sums = reinterpret_cast<float4 *>(smem + kWarps * kGroups * a.R);  // [kWarps][8][32]
   float4 *own = sums + warp * 8 * 32 + lane;
   if (a.partial)
 #pragma unroll
     for (int q = 0; q < 8; ++q) own[q * 32] = make_float4(0.f, 0.f, 0.f, 0.f);
-  const Lane t = lane_of<LPR>(lane, a.D, a.R, a.rope);
-  const float4 *angles = reinterpret_cast<const float4 *>(cs) + 2 * (lane % LPR);
+  const Lane t = lane_of<LPR, HALVES>(lane, a.D, a.R);
   const float inv_d = 1.f / a.D;
-  const bool x_bf16 = a.x_dtype == AG_BF16, g_bf16 = a.o_dtype == AG_BF16;
+  const int x_apart = static_cast<int>(bytes_of<XT>(t.b - t.a)),
+            g_apart = static_cast<int>(bytes_of<GT>(t.b - t.a));
   const uint32_t L = static_cast<uint32_t>(a.L), total = static_cast<uint32_t>(a.positions_total);
-  for (uint32_t pos = blockIdx.x * kWarps + warp; pos < total; pos += gridDim.x * kWarps) {
-    const uint32_t b32 = pos / L;
-    const int64_t b = b32, l = pos - b32 * L;
+  const uint32_t stride = gridDim.x * kWarps * kGroups;
+  for (uint32_t first = (blockIdx.x * kWarps + warp) * kGroups; first < total; first += stride) {
+    const uint32_t pos = min(first + lane / LPR, total - 1);
+    const bool mine = t.in && first + lane / LPR < total;
+    const int64_t b = pos / L, l = pos % L;
     bool angles_ready = a.R == 0;
 #pragma unroll 1
     for (int which = 0; which < 2; ++which) {
       const QkSide &s = a.side[which];
-      if (s.H == 0) continue;
-      const int64_t x_at = b * s.sb + l * s.sl, g_at = (b * s.H * a.L + l) * a.D,
-                    dx_at = b * s.dxb + l * s.dxl;
-      const Eight w = t.in ? param8(s.w, t.a, t.b, 1.f) : Eight{};
+      const char *x_at = static_cast<const char *>(s.x) + bytes_of<XT>(b * s.sb + l * s.sl + t.a);
+      const char *g_at =
+          static_cast<const char *>(s.g) + bytes_of<GT>((b * s.H * a.L + l) * a.D + t.a);
+      char *dx_at = static_cast<char *>(s.dx) + bytes_of<XT>(b * s.dxb + l * s.dxl + t.a);
+      const int64_t x_step = bytes_of<XT>(s.sh), g_step = bytes_of<GT>(a.L * a.D),
+                    dx_step = bytes_of<XT>(s.dxh);
+      const Eight w = param8<HALVES>(s.w, t, 1.f);
       Eight dw{}, db{};
 #pragma unroll 1
-      for (int h0 = 0; h0 < s.H; h0 += kAtOnce * kSteps) {
-        Raw<X32> raw_x[kSteps];
-        Raw<G32> raw_g[kSteps];
+      for (int left = s.H; left > 0; left -= kRows) {
+        Raw<XT> raw_x[kRows];
+        Raw<GT> raw_g[kRows];
 #pragma unroll
-        for (int u = 0; u < kSteps; ++u) {
-          const int h = h0 + u * kAtOnce + lane / LPR;
-          raw_x[u] = Raw<X32>{}, raw_g[u] = Raw<G32>{};
-          if (t.in && h < s.H) {
-            raw_x[u] = load8<X32>(s.x, x_at + h * s.sh, t.a, t.b);
-            raw_g[u] = load8<G32>(s.g, g_at + h * a.L * a.D, t.a, t.b);
+        for (int u = 0; u < kRows; ++u) {
+          raw_x[u] = Raw<XT>{}, raw_g[u] = Raw<GT>{};
+          if (mine && u < left) {
+            raw_x[u] = load8<XT>(x_at, x_apart);
+            raw_g[u] = load8<GT>(g_at, g_apart);
           }
+          x_at += x_step, g_at += g_step;
         }
         if (!angles_ready) {  // while the first rows are on their way
-          warp_angles(a, cs, b, l, lane);
+          group_angles<LPR>(a, cs, b, l, lane);
           angles_ready = true;
         }
 #pragma unroll
-        for (int u = 0; u < kSteps; ++u) {
-          if (h0 + u * kAtOnce >= s.H) break;
-          const int h = h0 + u * kAtOnce + lane / LPR;
-          const bool mine = t.in && h < s.H;
-          Eight x = widen<X32>(raw_x[u], x_bf16), g = widen<G32>(raw_g[u], g_bf16);
-          const float r = normalise<LPR>(x, a, inv_d, t.in);
-          if (t.turns) turn_pairs(g, angles, a.rope, -1.f);
-          float along = 0.f, total = 0.f;
+        for (int u = 0; u < kRows; ++u) {
+          if (u >= left) break;
+          Eight x = widen<XT, HALVES>(raw_x[u]), g = widen<GT, HALVES>(raw_g[u]);
+          const float r = normalise<LPR>(x, a, inv_d, mine);
+          if (t.turns) turn_pairs<true>(g, cos4, sin4);
+          if (a.partial)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            // (A row of this step past the last head counts for nothing, also
-            // when eps is zero and its norm is not a number.)
-            if (mine) dw.v[i] = fmaf(g.v[i], x.v[i], dw.v[i]), db.v[i] += g.v[i];
-            g.v[i] *= w.v[i];
-            along = fmaf(g.v[i], x.v[i], along);
-            total += g.v[i];
+            for (int i = 0; i < 4; ++i) {
+              dw.v[i] = __ffma2_rn(g.v[i], x.v[i], dw.v[i]);
+              db.v[i] = __fadd2_rn(db.v[i], g.v[i]);
+            }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) g.v[i] = __fmul2_rn(g.v[i], w.v[i]);
+          if (a.norm != AG_NORM_NONE) {
+            float2 dot = __fmul2_rn(g.v[0], x.v[0]);
+#pragma unroll
+            for (int i = 1; i < 4; ++i) dot = __ffma2_rn(g.v[i], x.v[i], dot);
+            const float2 along = twice(-row_sum<LPR>(dot) * inv_d);
+            const float2 mean =
+                twice(a.norm == AG_NORM_LAYER ? -row_sum<LPR>(sum4(g)) * inv_d : 0.f);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              g.v[i] = __fmul2_rn(__fadd2_rn(__ffma2_rn(x.v[i], along, g.v[i]), mean), twice(r));
           }
-          along = a.norm == AG_NORM_NONE ? 0.f : row_sum<LPR>(along) * inv_d;
-          total = a.norm == AG_NORM_LAYER ? row_sum<LPR>(total) * inv_d : 0.f;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) g.v[i] = r * (fmaf(-x.v[i], along, g.v[i]) - total);
-          if (mine) store8<X32>(s.dx, dx_at + h * s.dxh, t.a, t.b, g, x_bf16);
+          if (mine) store8<XT, HALVES>(dx_at, x_apart, g);
+          dx_at += dx_step;
         }
       }
-      if (a.partial) {
+      if (a.partial && s.H > 0) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const float *v = (q < 2 ? dw.v : db.v) + 4 * (q & 1);
+          const float2 *v = (q < 2 ? dw.v : db.v) + 2 * (q & 1);
           float4 &o = own[(which * 4 + q) * 32];
           const float4 was = o;
-          o = make_float4(was.x + v[0], was.y + v[1], was.z + v[2], was.w + v[3]);
+          o = make_float4(was.x + v[0].x, was.y + v[0].y, was.z + v[1].x, was.w + v[1].y);
         }
       }
     }
@@ -370,15 +414,18 @@ __global__ void __launch_bounds__(kThreads, 2) qk_bwd_rows_kernel(const QkArgs a
   if (!a.partial) return;
   __syncthreads();
   for (int i = threadIdx.x; i < 4 * a.D; i += kThreads) {
-    // Element e of array `which` lies in quad `quad` of lane `at` (lane_of).
+    // Element e of array `which`: number `at` of A or B of lane `l` (lane_of).
     const int which = i / a.D, e = i % a.D;
-    const bool half = a.rope == AG_ROPE_HALVES && e < a.R;
-    const int quad = half ? e / (a.R / 2) : (e % 8) / 4, at = half ? e % (a.R / 2) / 4 : e / 8;
-    const float *from = reinterpret_cast<const float *>(sums + (which * 2 + quad) * 32 + at) + e % 4;
+    int l = e / 8, second = HALVES ? (e % 8) / 4 : e % 2, at = HALVES ? e % 4 : e % 8 / 2;
+    if (HALVES && e < a.R) {
+      const int pair = e % (a.R / 2);
+      l = pair / 4, at = pair % 4, second = e / (a.R / 2);
+    }
+    const float *from = reinterpret_cast<const float *>(sums + (which * 2 + second) * 32 + l) + at;
     float v = 0.f;
     for (int w = 0; w < kWarps; ++w)
 #pragma unroll
-      for (int row = 0; row < kAtOnce; ++row) v += from[(w * 8 * 32 + row * LPR) * 4];
+      for (int row = 0; row < kGroups; ++row) v += from[(w * 8 * 32 + row * LPR) * 4];
     a.partial[static_cast<int64_t>(blockIdx.x) * 4 * a.D + i] = v;
   }
 }
@@ -531,7 +578,8 @@ bool by_rows(const QkArgs &a, bool backward) {
   if (a.D % 8 || a.D > 256 || a.R % 8) return false;
   for (const QkSide &s : a.side) {
     if (s.H == 0) continue;
-    if (!quads(s.x, a.x_dtype, s.sb, s.sl, s.sh)) return false;
+    if (!quads(s.x, a.x_dtype, s.sb, s.sl, s.sh) || !aligned(s.w, 16) || !aligned(s.b, 16))
+      return false;
     if (backward ? !quads(s.g, a.o_dtype, 0, 0, 0) || !quads(s.dx, a.x_dtype, s.dxb, s.dxl, s.dxh)
                  : !quads(s.out, a.o_dtype, 0, 0, 0))
       return false;
@@ -561,33 +609,42 @@ int64_t qk_bwd_workspace(int64_t positions_total, int64_t D, int num_sms) {
 
 namespace {
 
+// Positions that a warp of the rows kernels takes.
+int groups_of(int D) { return D <= 64 ? 4 : D <= 128 ? 2 : 1; }
 using QkKernel = void (*)(QkArgs);
-template <bool X32, bool O32>
+template <int XT, int OT, bool HALVES>
 QkKernel rows_kernel(int D, bool backward) {
   if (backward)
-    return D <= 32    ? qk_bwd_rows_kernel<4, X32, O32>
-           : D <= 64  ? qk_bwd_rows_kernel<8, X32, O32>
-           : D <= 128 ? qk_bwd_rows_kernel<16, X32, O32>
-                      : qk_bwd_rows_kernel<32, X32, O32>;
-  return D <= 32    ? qk_fwd_rows_kernel<4, X32, O32>
-         : D <= 64  ? qk_fwd_rows_kernel<8, X32, O32>
-         : D <= 128 ? qk_fwd_rows_kernel<16, X32, O32>
-                    : qk_fwd_rows_kernel<32, X32, O32>;
+    return D <= 64    ? qk_bwd_rows_kernel<8, XT, OT, HALVES>
+           : D <= 128 ? qk_bwd_rows_kernel<16, XT, OT, HALVES>
+                      : qk_bwd_rows_kernel<32, XT, OT, HALVES>;
+  return D <= 64    ? qk_fwd_rows_kernel<8, XT, OT, HALVES>
+         : D <= 128 ? qk_fwd_rows_kernel<16, XT, OT, HALVES>
+                    : qk_fwd_rows_kernel<32, XT, OT, HALVES>;
+}
+template <int XT, bool HALVES>
+QkKernel rows_kernel(const QkArgs &a, bool backward) {
+  return a.o_dtype == AG_F32    ? rows_kernel<XT, AG_F32, HALVES>(a.D, backward)
+         : a.o_dtype == AG_BF16 ? rows_kernel<XT, AG_BF16, HALVES>(a.D, backward)
+                                : rows_kernel<XT, AG_F16, HALVES>(a.D, backward);
+}
+template <bool HALVES>
+QkKernel rows_kernel(const QkArgs &a, bool backward) {
+  return a.x_dtype == AG_F32    ? rows_kernel<AG_F32, HALVES>(a, backward)
+         : a.x_dtype == AG_BF16 ? rows_kernel<AG_BF16, HALVES>(a, backward)
+                                : rows_kernel<AG_F16, HALVES>(a, backward);
 }
 QkKernel rows_kernel(const QkArgs &a, bool backward) {
-  const bool o32 = a.o_dtype == AG_F32;
-  if (a.x_dtype == AG_F32)
-    return o32 ? rows_kernel<true, true>(a.D, backward) : rows_kernel<true, false>(a.D, backward);
-  return o32 ? rows_kernel<false, true>(a.D, backward) : rows_kernel<false, false>(a.D, backward);
+  return a.rope == AG_ROPE_HALVES ? rows_kernel<true>(a, backward) : rows_kernel<false>(a, backward);
 }
 
 }  // namespace
 
-cudaError_t launch_qk_fwd(const QkArgs &a, int num_sms, cudaStream_t stream) {
+cudaError_t launch_qk_fwd(const QkArgs &a, cudaStream_t stream) {
   if (by_rows(a, false)) {
-    const int64_t blocks = (a.positions_total + kWarps - 1) / kWarps;
-    rows_kernel(a, false)<<<static_cast<unsigned>(blocks < 24 * num_sms ? blocks : 24 * num_sms),
-                            kThreads, kWarps * a.R * 4, stream>>>(a);
+    const int each = kWarps * groups_of(a.D);
+    const int64_t blocks = (a.positions_total + each - 1) / each;
+    rows_kernel(a, false)<<<static_cast<unsigned>(blocks), kThreads, each * a.R * 4, stream>>>(a);
     return cudaGetLastError();
   }
   const size_t smem = (static_cast<size_t>(kPos) * a.R + kWarps * static_cast<size_t>(a.D)) * 4;
@@ -601,8 +658,9 @@ cudaError_t launch_qk_fwd(const QkArgs &a, int num_sms, cudaStream_t stream) {
 cudaError_t launch_qk_bwd(const QkArgs &a, int num_sms, cudaStream_t stream) {
   int blocks;
   if (by_rows(a, true)) {
-    blocks = bwd_blocks(a.positions_total, kWarps, 2, num_sms);
-    rows_kernel(a, true)<<<blocks, kThreads, kWarps * (a.R + 8 * 32 * 4) * 4, stream>>>(a);
+    const int each = kWarps * groups_of(a.D);
+    blocks = bwd_blocks(a.positions_total, each, 2, num_sms);
+    rows_kernel(a, true)<<<blocks, kThreads, (each * a.R + kWarps * 8 * 32 * 4) * 4, stream>>>(a);
   } else {
     const int warps = bwd_warps(a.D);
     blocks = bwd_blocks(a.positions_total, kPos, 4, num_sms);
