@@ -169,13 +169,17 @@ __device__ __forceinline__ void store8(char *p, int apart, const Eight &e) {
     *reinterpret_cast<uint2 *>(p + apart) = make_uint2(narrow2<T>(o[2]), narrow2<T>(o[3]));
   }
 }
-// Sum over the LPR lanes of a row, of both numbers.
-template <int LPR>
-__device__ __forceinline__ float row_sum(float2 v) {
-  float s = v.x + v.y;
+// Sums over the LPR lanes of a row, of both numbers, for N rows side by side
+// (one row's sum waits for each of its exchanges; several rows' cover each
+// other's).
+template <int LPR, int N>
+__device__ __forceinline__ void row_sums(const float2 (&v)[N], float (&s)[N]) {
 #pragma unroll
-  for (int o = LPR / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  return s;
+  for (int u = 0; u < N; ++u) s[u] = v[u].x + v[u].y;
+#pragma unroll
+  for (int o = LPR / 2; o > 0; o >>= 1)
+#pragma unroll
+    for (int u = 0; u < N; ++u) s[u] += __shfl_xor_sync(0xffffffffu, s[u], o);
 }
 __device__ __forceinline__ float2 twice(float c) { return make_float2(c, c); }
 __device__ __forceinline__ float2 negated(float2 v) { return make_float2(-v.x, -v.y); }
@@ -241,31 +245,86 @@ __device__ __forceinline__ void group_angles(const QkArgs &a, float *cs, int64_t
   __syncwarp();
 }
 
-// n = (x - mean) r in place; r.  Lanes without elements hold zeros.
-template <int LPR>
-__device__ __forceinline__ float normalise(Eight &e, const QkArgs &a, float inv_d, bool mine) {
-  if (a.norm == AG_NORM_NONE) return 1.f;
+// n = (x - mean) r in place, and r, for N rows.  Lanes without elements hold
+// zeros.
+template <int LPR, int N>
+__device__ __forceinline__ void normalise(Eight (&e)[N], float (&r)[N], const QkArgs &a, float inv_d,
+                                          bool mine) {
+  if (a.norm == AG_NORM_NONE) return;
+  float2 part[N];
+  float s[N];
   if (a.norm == AG_NORM_LAYER) {
-    const float sum = row_sum<LPR>(sum4(e));
-    const float2 mean = twice(mine ? -sum * inv_d : 0.f);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) e.v[i] = __fadd2_rn(e.v[i], mean);
+    for (int u = 0; u < N; ++u) part[u] = sum4(e[u]);
+    row_sums<LPR, N>(part, s);
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      const float2 mean = twice(mine ? -s[u] * inv_d : 0.f);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) e[u].v[i] = __fadd2_rn(e[u].v[i], mean);
+    }
   }
-  float2 q = __fmul2_rn(e.v[0], e.v[0]);
 #pragma unroll
-  for (int i = 1; i < 4; ++i) q = __ffma2_rn(e.v[i], e.v[i], q);
-  // (A group past the last position counts for nothing, also when eps is zero.)
-  float r = __frsqrt_rn(fmaf(row_sum<LPR>(q), inv_d, a.eps));
-  if (!mine) r = 0.f;
+  for (int u = 0; u < N; ++u) {
+    part[u] = __fmul2_rn(e[u].v[0], e[u].v[0]);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) e.v[i] = __fmul2_rn(e.v[i], twice(r));
-  return r;
+    for (int i = 1; i < 4; ++i) part[u] = __ffma2_rn(e[u].v[i], e[u].v[i], part[u]);
+  }
+  row_sums<LPR, N>(part, s);
+#pragma unroll
+  for (int u = 0; u < N; ++u) {
+    // (A group past the last position counts for nothing, also when eps is zero.)
+    r[u] = mine ? __frsqrt_rn(fmaf(s[u], inv_d, a.eps)) : 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) e[u].v[i] = __fmul2_rn(e[u].v[i], twice(r[u]));
+  }
 }
+
+// What the rows of one side share in the forward.
+template <int LPR, int XT, int OT, bool HALVES>
+struct FwdRows {
+  const QkArgs &a;
+  const Lane &t;
+  const float4 *cos4, *sin4;
+  bool mine;
+  float inv_d;
+  int x_apart, o_apart;
+  int64_t x_step, o_step;
+  const char *x_at;
+  char *o_at;
+  Eight w, bias;
+
+  // N rows from here on; `between` runs while their loads are on their way.
+  template <int N, typename F>
+  __device__ __forceinline__ void rows(F between) {
+    Raw<XT> raw[N];
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      raw[u] = Raw<XT>{};
+      if (mine) raw[u] = load8<XT>(x_at, x_apart);
+      x_at += x_step;
+    }
+    between();
+    Eight x[N];
+    float r[N];
+#pragma unroll
+    for (int u = 0; u < N; ++u) x[u] = widen<XT, HALVES>(raw[u]);
+    normalise<LPR, N>(x, r, a, inv_d, mine);
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[u].v[i] = __ffma2_rn(x[u].v[i], w.v[i], bias.v[i]);
+      if (t.turns) turn_pairs<false>(x[u], cos4, sin4);
+      if (mine) store8<OT, HALVES>(o_at, o_apart, x[u]);
+      o_at += o_step;
+    }
+  }
+};
 
 template <int LPR, int XT, int OT, bool HALVES>
 __global__ void __launch_bounds__(kThreads, 4) qk_fwd_rows_kernel(const QkArgs a) {
   extern __shared__ float smem[];
-  constexpr int kGroups = 32 / LPR, kRows = 4;   // positions per warp; rows loaded together
+  constexpr int kGroups = 32 / LPR, kRows = 2;   // positions per warp; rows loaded together
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   float *cs = smem + (warp * kGroups + lane / LPR) * a.R;
   const float4 *cos4 = reinterpret_cast<const float4 *>(cs) + lane % LPR, *sin4 = cos4 + a.R / 8;
@@ -280,40 +339,107 @@ __global__ void __launch_bounds__(kThreads, 4) qk_fwd_rows_kernel(const QkArgs a
   const bool mine = t.in && first + lane / LPR < total;
   const int64_t b = pos / L, l = pos % L;
   bool angles_ready = a.R == 0;
+  const auto angles = [&] {
+    if (!angles_ready) group_angles<LPR>(a, cs, b, l, lane);
+    angles_ready = true;
+  };
 #pragma unroll 1
   for (int which = 0; which < 2; ++which) {
     const QkSide &s = a.side[which];
-    const char *x_at = static_cast<const char *>(s.x) + bytes_of<XT>(b * s.sb + l * s.sl + t.a);
-    char *o_at = static_cast<char *>(s.out) + bytes_of<OT>((b * s.H * a.L + l) * a.D + t.a);
-    const int64_t x_step = bytes_of<XT>(s.sh), o_step = bytes_of<OT>(a.L * a.D);
-    const Eight w = param8<HALVES>(s.w, t, 1.f), bias = param8<HALVES>(s.b, t, 0.f);
+    FwdRows<LPR, XT, OT, HALVES> f{
+        a, t, cos4, sin4, mine, inv_d, x_apart, o_apart, bytes_of<XT>(s.sh), bytes_of<OT>(a.L * a.D),
+        static_cast<const char *>(s.x) + bytes_of<XT>(b * s.sb + l * s.sl + t.a),
+        static_cast<char *>(s.out) + bytes_of<OT>((b * s.H * a.L + l) * a.D + t.a),
+        param8<HALVES>(s.w, t, 1.f), param8<HALVES>(s.b, t, 0.f)};
+    int left = s.H;
 #pragma unroll 1
-    for (int left = s.H; left > 0; left -= kRows) {
-      Raw<XT> raw[kRows];
-#pragma unroll
-      for (int u = 0; u < kRows; ++u) {
-        raw[u] = Raw<XT>{};
-        if (mine && u < left) raw[u] = load8<XT>(x_at, x_apart);
-        x_at += x_step;
-      }
-      if (!angles_ready) {  // while the first rows are on their way
-        group_angles<LPR>(a, cs, b, l, lane);
-        angles_ready = true;
-      }
-#pragma unroll
-      for (int u = 0; u < kRows; ++u) {
-        if (u >= left) break;
-        Eight x = widen<XT, HALVES>(raw[u]);
-        normalise<LPR>(x, a, inv_d, mine);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x.v[i] = __ffma2_rn(x.v[i], w.v[i], bias.v[i]);
-        if (t.turns) turn_pairs<false>(x, cos4, sin4);
-        if (mine) store8<OT, HALVES>(o_at, o_apart, x);
-        o_at += o_step;
-      }
-    }
+    for (; left >= kRows; left -= kRows) f.template rows<kRows>(angles);
+#pragma unroll 1
+    for (; left > 0; --left) f.template rows<1>(angles);
   }
 }
+
+// What the rows of one side share in the backward.
+template <int LPR, int XT, int GT, bool HALVES>
+struct BwdRows {
+  const QkArgs &a;
+  const Lane &t;
+  const float4 *cos4, *sin4;
+  bool mine;
+  float inv_d;
+  int x_apart, g_apart;
+  int64_t x_step, g_step, dx_step;
+  const char *x_at, *g_at;
+  char *dx_at;
+  Eight w, dw, db;
+
+  template <int N, typename F>
+  __device__ __forceinline__ void rows(F between) {
+    Raw<XT> raw_x[N];
+    Raw<GT> raw_g[N];
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      raw_x[u] = Raw<XT>{}, raw_g[u] = Raw<GT>{};
+      if (mine) {
+        raw_x[u] = load8<XT>(x_at, x_apart);
+        raw_g[u] = load8<GT>(g_at, g_apart);
+      }
+      x_at += x_step, g_at += g_step;
+    }
+    between();
+    Eight x[N], g[N];
+    float r[N];
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      x[u] = widen<XT, HALVES>(raw_x[u]), g[u] = widen<GT, HALVES>(raw_g[u]);
+      r[u] = 1.f;
+    }
+    normalise<LPR, N>(x, r, a, inv_d, mine);
+    float2 dot[N];
+    float along[N], mean[N];
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      if (t.turns) turn_pairs<true>(g[u], cos4, sin4);
+      if (a.partial)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          dw.v[i] = __ffma2_rn(g[u].v[i], x[u].v[i], dw.v[i]);
+          db.v[i] = __fadd2_rn(db.v[i], g[u].v[i]);
+        }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) g[u].v[i] = __fmul2_rn(g[u].v[i], w.v[i]);
+    }
+    if (a.norm != AG_NORM_NONE) {
+#pragma unroll
+      for (int u = 0; u < N; ++u) {
+        dot[u] = __fmul2_rn(g[u].v[0], x[u].v[0]);
+#pragma unroll
+        for (int i = 1; i < 4; ++i) dot[u] = __ffma2_rn(g[u].v[i], x[u].v[i], dot[u]);
+      }
+      row_sums<LPR, N>(dot, along);
+      if (a.norm == AG_NORM_LAYER) {
+#pragma unroll
+        for (int u = 0; u < N; ++u) dot[u] = sum4(g[u]);
+        row_sums<LPR, N>(dot, mean);
+      } else {
+#pragma unroll
+        for (int u = 0; u < N; ++u) mean[u] = 0.f;
+      }
+#pragma unroll
+      for (int u = 0; u < N; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          g[u].v[i] = __fmul2_rn(__fadd2_rn(__ffma2_rn(x[u].v[i], twice(-along[u] * inv_d), g[u].v[i]),
+                                            twice(-mean[u] * inv_d)),
+                                 twice(r[u]));
+    }
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      if (mine) store8<XT, HALVES>(dx_at, x_apart, g[u]);
+      dx_at += dx_step;
+    }
+  }
+};
 
 // Backward.  A lane's elements are the same in every row it meets, so it sums
 // the parameter gradients of a position's heads in registers and adds them to
@@ -323,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 4) qk_fwd_rows_kernel(const QkArgs a
 template <int LPR, int XT, int GT, bool HALVES>
 __global__ void __launch_bounds__(kThreads, 2) qk_bwd_rows_kernel(const QkArgs a) {
   extern __shared__ float smem[];
-  constexpr int kGroups = 32 / LPR, kRows = 2;
+  constexpr int kGroups = 32 / LPR, kRows = 4;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   float *cs = smem + (warp * kGroups + lane / LPR) * a.R;
   const float4 *cos4 = reinterpret_cast<const float4 *>(cs) + lane % LPR, *sin4 = cos4 + a.R / 8;
@@ -343,67 +469,29 @@ __global__ void __launch_bounds__(kThreads, 2) qk_bwd_rows_kernel(const QkArgs a
     const bool mine = t.in && first + lane / LPR < total;
     const int64_t b = pos / L, l = pos % L;
     bool angles_ready = a.R == 0;
+    const auto angles = [&] {
+      if (!angles_ready) group_angles<LPR>(a, cs, b, l, lane);
+      angles_ready = true;
+    };
 #pragma unroll 1
     for (int which = 0; which < 2; ++which) {
       const QkSide &s = a.side[which];
-      const char *x_at = static_cast<const char *>(s.x) + bytes_of<XT>(b * s.sb + l * s.sl + t.a);
-      const char *g_at =
-          static_cast<const char *>(s.g) + bytes_of<GT>((b * s.H * a.L + l) * a.D + t.a);
-      char *dx_at = static_cast<char *>(s.dx) + bytes_of<XT>(b * s.dxb + l * s.dxl + t.a);
-      const int64_t x_step = bytes_of<XT>(s.sh), g_step = bytes_of<GT>(a.L * a.D),
-                    dx_step = bytes_of<XT>(s.dxh);
-      const Eight w = param8<HALVES>(s.w, t, 1.f);
-      Eight dw{}, db{};
+      BwdRows<LPR, XT, GT, HALVES> f{
+          a, t, cos4, sin4, mine, inv_d, x_apart, g_apart, bytes_of<XT>(s.sh),
+          bytes_of<GT>(a.L * a.D), bytes_of<XT>(s.dxh),
+          static_cast<const char *>(s.x) + bytes_of<XT>(b * s.sb + l * s.sl + t.a),
+          static_cast<const char *>(s.g) + bytes_of<GT>((b * s.H * a.L + l) * a.D + t.a),
+          static_cast<char *>(s.dx) + bytes_of<XT>(b * s.dxb + l * s.dxl + t.a),
+          param8<HALVES>(s.w, t, 1.f), Eight{}, Eight{}};
+      int left = s.H;
 #pragma unroll 1
-      for (int left = s.H; left > 0; left -= kRows) {
-        Raw<XT> raw_x[kRows];
-        Raw<GT> raw_g[kRows];
-#pragma unroll
-        for (int u = 0; u < kRows; ++u) {
-          raw_x[u] = Raw<XT>{}, raw_g[u] = Raw<GT>{};
-          if (mine && u < left) {
-            raw_x[u] = load8<XT>(x_at, x_apart);
-            raw_g[u] = load8<GT>(g_at, g_apart);
-          }
-          x_at += x_step, g_at += g_step;
-        }
-        if (!angles_ready) {  // while the first rows are on their way
-          group_angles<LPR>(a, cs, b, l, lane);
-          angles_ready = true;
-        }
-#pragma unroll
-        for (int u = 0; u < kRows; ++u) {
-          if (u >= left) break;
-          Eight x = widen<XT, HALVES>(raw_x[u]), g = widen<GT, HALVES>(raw_g[u]);
-          const float r = normalise<LPR>(x, a, inv_d, mine);
-          if (t.turns) turn_pairs<true>(g, cos4, sin4);
-          if (a.partial)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              dw.v[i] = __ffma2_rn(g.v[i], x.v[i], dw.v[i]);
-              db.v[i] = __fadd2_rn(db.v[i], g.v[i]);
-            }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) g.v[i] = __fmul2_rn(g.v[i], w.v[i]);
-          if (a.norm != AG_NORM_NONE) {
-            float2 dot = __fmul2_rn(g.v[0], x.v[0]);
-#pragma unroll
-            for (int i = 1; i < 4; ++i) dot = __ffma2_rn(g.v[i], x.v[i], dot);
-            const float2 along = twice(-row_sum<LPR>(dot) * inv_d);
-            const float2 mean =
-                twice(a.norm == AG_NORM_LAYER ? -row_sum<LPR>(sum4(g)) * inv_d : 0.f);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              g.v[i] = __fmul2_rn(__fadd2_rn(__ffma2_rn(x.v[i], along, g.v[i]), mean), twice(r));
-          }
-          if (mine) store8<XT, HALVES>(dx_at, x_apart, g);
-          dx_at += dx_step;
-        }
-      }
+      for (; left >= kRows; left -= kRows) f.template rows<kRows>(angles);
+#pragma unroll 1
+      for (; left > 0; --left) f.template rows<1>(angles);
       if (a.partial && s.H > 0) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const float2 *v = (q < 2 ? dw.v : db.v) + 2 * (q & 1);
+          const float2 *v = (q < 2 ? f.dw.v : f.db.v) + 2 * (q & 1);
           float4 &o = own[(which * 4 + q) * 32];
           const float4 was = o;
           o = make_float4(was.x + v[0].x, was.y + v[0].y, was.z + v[1].x, was.w + v[1].y);
@@ -552,19 +640,19 @@ __global__ void __launch_bounds__(kThreads) qk_bwd_kernel(const QkArgs a, int wa
 }
 
 // The parameter gradients: sums of the blocks' partials [blocks][4][D], 32
-// columns per block, 8 lanes over the partials, in 64 bits and a fixed order.
-__global__ void __launch_bounds__(256)
+// columns per block, 32 warps over the partials, in 64 bits and a fixed order.
+__global__ void __launch_bounds__(1024)
     qk_params_kernel(const float *partial, int blocks, int D, float *qw, float *qb, float *kw,
                      float *kb) {
-  __shared__ double part[8][32];
+  __shared__ double part[32][32];
   const int c = threadIdx.x % 32, r = threadIdx.x / 32, n = blockIdx.x * 32 + c;
   double t = 0.0;
   if (n < 4 * D)
-    for (int i = r; i < blocks; i += 8) t += partial[static_cast<int64_t>(i) * 4 * D + n];
+    for (int i = r; i < blocks; i += 32) t += partial[static_cast<int64_t>(i) * 4 * D + n];
   part[r][c] = t;
   __syncthreads();
   if (r != 0 || n >= 4 * D) return;
-  for (int i = 1; i < 8; ++i) t += part[i][c];
+  for (int i = 1; i < 32; ++i) t += part[i][c];
   float *to = n < 2 * D ? (n < D ? qw : qb) : (n < 3 * D ? kw : kb);
   if (to) to[n % D] = static_cast<float>(t);
 }
@@ -671,7 +759,7 @@ cudaError_t launch_qk_bwd(const QkArgs &a, int num_sms, cudaStream_t stream) {
   }
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !a.partial) return e;
-  qk_params_kernel<<<(4 * a.D + 31) / 32, 256, 0, stream>>>(
+  qk_params_kernel<<<(4 * a.D + 31) / 32, 1024, 0, stream>>>(
       a.partial, blocks, a.D, a.side[0].dw, a.side[0].db, a.side[1].dw, a.side[1].db);
   return cudaGetLastError();
 }
