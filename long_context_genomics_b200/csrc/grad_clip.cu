@@ -11,6 +11,7 @@
 #include <cmath>
 
 #include "ag_internal.h"
+#include "launch.cuh"
 #include "linear_epilogue.cuh"
 
 namespace ag {
@@ -78,6 +79,7 @@ __device__ __forceinline__ double block_sum(double s) {
 template <int MOST>
 __global__ void __launch_bounds__(kThreads)
     square_sum_kernel(const __grid_constant__ TensorList<MOST> list, double *partial) {
+  begin_after_previous();
   double s = 0.0;
   for (uint32_t c = blockIdx.x; c < list.first[list.n]; c += gridDim.x) {
     const Chunk k = chunk_of(list, c);
@@ -109,6 +111,7 @@ __device__ __forceinline__ double total_of(const double *partial, int slots) {
 
 __global__ void __launch_bounds__(kThreads)
     total_kernel(const double *partial, int slots, double *total) {
+  begin_after_previous();
   const double t = total_of(partial, slots);
   if (threadIdx.x == 0) *total = t;
 }
@@ -117,6 +120,7 @@ template <int MOST>
 __global__ void __launch_bounds__(kThreads)
     scale_kernel(const __grid_constant__ TensorList<MOST> list, const double *partial, int slots,
                  float max_norm, float eps, float *norm_out) {
+  begin_after_previous();
   const double norm = sqrt(total_of(partial, slots));
   if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = static_cast<float>(norm);
   if (max_norm == INFINITY) return;
@@ -190,8 +194,8 @@ cudaError_t clip(void *const *grads, const int64_t *counts, const int *dtypes, i
     if (list.n == 0) break;
     const unsigned chunks = list.first[list.n];
     const int blocks = chunks < static_cast<unsigned>(most) ? static_cast<int>(chunks) : most;
-    square_sum_kernel<<<blocks, kThreads, 0, stream>>>(list, workspace + slots);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_after_previous(square_sum_kernel<MOST>, blocks, kThreads, 0, stream,
+                                                list, workspace + slots);
     if (e != cudaSuccess) return e;
     slots += blocks;
     ++launches;
@@ -199,8 +203,8 @@ cudaError_t clip(void *const *grads, const int64_t *counts, const int *dtypes, i
   const double *sums = workspace;
   if (launches > 1) {
     double *total = workspace + slots;
-    total_kernel<<<1, kThreads, 0, stream>>>(workspace, slots, total);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e =
+        launch_after_previous(total_kernel, 1, kThreads, 0, stream, workspace, slots, total);
     if (e != cudaSuccess) return e;
     sums = total;
     slots = 1;
@@ -214,9 +218,9 @@ cudaError_t clip(void *const *grads, const int64_t *counts, const int *dtypes, i
     const unsigned chunks = list.first[list.n];
     int blocks = chunks < static_cast<unsigned>(most) ? static_cast<int>(chunks) : most;
     if (blocks == 0 || std::isinf(max_norm)) blocks = 1;
-    scale_kernel<<<blocks, kThreads, 0, stream>>>(list, sums, slots, max_norm, eps,
-                                                  first ? norm_out : nullptr);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e =
+        launch_after_previous(scale_kernel<MOST>, blocks, kThreads, 0, stream, list, sums, slots,
+                              max_norm, eps, first ? norm_out : nullptr);
     if (e != cudaSuccess) return e;
     first = false;
   } while (i < n && !std::isinf(max_norm));

@@ -7,6 +7,7 @@
 // them are the kernels that join split sums, copy operands whose rows TMA cannot
 // read, sum dy's columns, and multiply a few rows without the tensor cores.
 #include "ag_internal.h"
+#include "launch.cuh"
 #include "linear_epilogue.cuh"
 #include "linear_gemm.h"
 
@@ -42,6 +43,7 @@ template <int V>
 __global__ void __launch_bounds__(256)
     linear_join_kernel(const float *__restrict__ partial, int splits, int64_t M, int64_t N,
                        int64_t ld, const LinearEpilogue e) {
+  begin_after_previous();
   const int64_t per_row = (N + V - 1) / V;
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   if (i >= M * per_row) return;
@@ -62,6 +64,7 @@ __global__ void __launch_bounds__(256)
 __global__ void __launch_bounds__(256)
     pack_rows_kernel(const uint16_t *__restrict__ from, int64_t ld_from, uint16_t *__restrict__ to,
                      int64_t ld_to, int64_t rows, int64_t cols) {
+  begin_after_previous();
   for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
     for (int64_t c = threadIdx.x; c < cols; c += 256) to[r * ld_to + c] = from[r * ld_from + c];
 }
@@ -74,6 +77,7 @@ __global__ void __launch_bounds__(256)
     column_sum_kernel(const uint16_t *__restrict__ dy, int64_t ld, int64_t M, int64_t N, int dtype,
                       int parts, float *__restrict__ out) {
   __shared__ float part[8][32 * V];
+  begin_after_previous();
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int64_t col = (static_cast<int64_t>(blockIdx.x) * 32 + lane) * V;
   const int64_t from = M * blockIdx.y / parts, to = M * (blockIdx.y + 1) / parts;
@@ -104,6 +108,7 @@ __global__ void __launch_bounds__(256)
     column_join_kernel(const float *__restrict__ partial, int parts, int64_t N,
                        float *__restrict__ db) {
   __shared__ float sums[8][32];
+  begin_after_previous();
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int64_t n = static_cast<int64_t>(blockIdx.x) * 32 + lane;
   float s = 0.f;
@@ -134,6 +139,7 @@ __global__ void __launch_bounds__(256)
                          const uint16_t *__restrict__ W, int64_t ldw, int M, int64_t N, int64_t K,
                          int warps_k, const LinearEpilogue e) {
   __shared__ float part[8][kRowsW * MT];
+  begin_after_previous();
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int wk = warp % warps_k, group = warp / warps_k;
   const int64_t n0 = (static_cast<int64_t>(blockIdx.x) * (8 / warps_k) + group) * kRowsW;
@@ -196,10 +202,10 @@ cudaError_t launch_skinny(const LinearFwd &a) {
   const int64_t rows = static_cast<int64_t>(8 / warps_k) * kRowsW;
   const unsigned blocks = static_cast<unsigned>((a.N + rows - 1) / rows);
   auto *kernel = vec ? linear_skinny_kernel<MT, 8> : linear_skinny_kernel<MT, 1>;
-  kernel<<<blocks, 256, 0, a.stream>>>(static_cast<const uint16_t *>(a.x), a.ldx,
-                                       static_cast<const uint16_t *>(a.W), a.ldw,
-                                       static_cast<int>(a.M), a.N, a.K, warps_k, a.epi);
-  return cudaGetLastError();
+  return launch_after_previous(kernel, blocks, 256, 0, a.stream,
+                               static_cast<const uint16_t *>(a.x), a.ldx,
+                               static_cast<const uint16_t *>(a.W), a.ldw, static_cast<int>(a.M),
+                               a.N, a.K, warps_k, a.epi);
 }
 
 // --------------------------------------------------------------------------
@@ -230,10 +236,10 @@ Packed place(const void *p, int64_t rows, int64_t cols, int64_t ld, Workspace &w
 cudaError_t fill(const Packed &k, const void *p, int64_t ld, int num_sms, cudaStream_t s) {
   if (!k.copy) return cudaSuccess;
   const int64_t blocks = k.op.rows < 16 * num_sms ? k.op.rows : 16 * num_sms;
-  pack_rows_kernel<<<static_cast<unsigned>(blocks), 256, 0, s>>>(
-      static_cast<const uint16_t *>(p), ld, static_cast<uint16_t *>(const_cast<void *>(k.op.p)),
-      k.op.ld, k.op.rows, k.op.cols);
-  return cudaGetLastError();
+  return launch_after_previous(pack_rows_kernel, static_cast<unsigned>(blocks), 256, 0, s,
+                               static_cast<const uint16_t *>(p), ld,
+                               static_cast<uint16_t *>(const_cast<void *>(k.op.p)), k.op.ld,
+                               k.op.rows, k.op.cols);
 }
 
 int64_t partial_bytes(const GemmPlan &plan, int64_t M, int64_t N) {
@@ -246,13 +252,9 @@ cudaError_t run(Gemm &g) {
   const int v = g.epi.vec8 ? 8 : 1;
   const int64_t blocks = (g.M * ((g.N + v - 1) / v) + 255) / 256;
   if (blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
-  if (v == 8)
-    linear_join_kernel<8><<<static_cast<unsigned>(blocks), 256, 0, g.stream>>>(
-        g.partial, g.plan.splits, g.M, g.N, partial_ld(g.N), g.epi);
-  else
-    linear_join_kernel<1><<<static_cast<unsigned>(blocks), 256, 0, g.stream>>>(
-        g.partial, g.plan.splits, g.M, g.N, partial_ld(g.N), g.epi);
-  return cudaGetLastError();
+  return launch_after_previous(v == 8 ? linear_join_kernel<8> : linear_join_kernel<1>,
+                               static_cast<unsigned>(blocks), 256, 0, g.stream, g.partial,
+                               g.plan.splits, g.M, g.N, partial_ld(g.N), g.epi);
 }
 
 struct FwdLayout {
@@ -362,15 +364,12 @@ cudaError_t launch_linear_bwd(const LinearBwd &a) {
     const int cols = l.db_vec ? 256 : 32;
     const dim3 grid(static_cast<unsigned>((a.N + cols - 1) / cols), l.db_parts);
     float *to = l.db_parts > 1 ? l.partial : a.db;
-    auto *kernel = l.db_vec ? column_sum_kernel<8> : column_sum_kernel<1>;
-    kernel<<<grid, 256, 0, a.stream>>>(static_cast<const uint16_t *>(a.dy), a.lddy, a.M, a.N,
-                                       a.dx.dtype, l.db_parts, to);
-    e = cudaGetLastError();
-    if (e == cudaSuccess && l.db_parts > 1) {
-      column_join_kernel<<<static_cast<unsigned>((a.N + 31) / 32), 256, 0, a.stream>>>(
-          l.partial, l.db_parts, a.N, a.db);
-      e = cudaGetLastError();
-    }
+    e = launch_after_previous(l.db_vec ? column_sum_kernel<8> : column_sum_kernel<1>, grid, 256, 0,
+                              a.stream, static_cast<const uint16_t *>(a.dy), a.lddy, a.M, a.N,
+                              a.dx.dtype, l.db_parts, to);
+    if (e == cudaSuccess && l.db_parts > 1)
+      e = launch_after_previous(column_join_kernel, static_cast<unsigned>((a.N + 31) / 32), 256, 0,
+                                a.stream, l.partial, l.db_parts, a.N, a.db);
   }
   return e;
 }

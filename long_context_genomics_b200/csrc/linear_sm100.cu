@@ -35,6 +35,7 @@
 
 #include "ag_internal.h"
 #include "linear_epilogue.cuh"
+#include "launch.cuh"
 #include "linear_gemm.h"
 #include "sm100.cuh"
 
@@ -486,6 +487,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   if (threadIdx.x == 0) {
+    griddep_launch_dependents();
     for (int s = 0; s < S::kStages; ++s) {
       mbar_init(&bars->full[s], 1);
       mbar_init(&bars->empty[s], 1);
@@ -505,6 +507,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tmem_alloc2(&bars->tmem_base, S::kCols);
     tmem_relinquish2();
   }
+  griddep_wait();  // nothing before this touches what the kernel before wrote or read
   tc_fence_before();
   cluster_sync();
   tc_fence_after();
@@ -557,9 +560,8 @@ cudaError_t launch(const Gemm &g, const Params &p, const CUtensorMap &ma, const 
   });
   if (once_err[dev] != cudaSuccess) return once_err[dev];
   const int clusters = p.items < g.num_sms / 2 ? p.items : g.num_sms / 2;
-  kernel<<<static_cast<unsigned>(2 * clusters), kThreads, smem_bytes<BN>(), g.stream>>>(ma, mb, maps,
-                                                                                       p);
-  return cudaGetLastError();
+  return launch_after_previous(kernel, 2 * clusters, kThreads, smem_bytes<BN>(), g.stream, ma, mb,
+                               maps, p);
 }
 
 template <int BN, bool A_MN, bool B_MN, bool SLOPE>

@@ -21,6 +21,7 @@
 //
 // General kernels: one warp per row through shared memory, any size or stride.
 #include "ag_internal.h"
+#include "launch.cuh"
 #include "linear_epilogue.cuh"
 
 namespace ag {
@@ -324,6 +325,7 @@ struct FwdRows {
 template <int LPR, int XT, int OT, bool HALVES>
 __global__ void __launch_bounds__(kThreads, 4) qk_fwd_rows_kernel(const QkArgs a) {
   extern __shared__ float smem[];
+  begin_after_previous();
   constexpr int kGroups = 32 / LPR, kRows = 2;   // positions per warp; rows loaded together
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   float *cs = smem + (warp * kGroups + lane / LPR) * a.R;
@@ -449,6 +451,7 @@ struct BwdRows {
 template <int LPR, int XT, int GT, bool HALVES>
 __global__ void __launch_bounds__(kThreads, 2) qk_bwd_rows_kernel(const QkArgs a) {
   extern __shared__ float smem[];
+  begin_after_previous();
   constexpr int kGroups = 32 / LPR, kRows = 4;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   float *cs = smem + (warp * kGroups + lane / LPR) * a.R;
@@ -522,6 +525,7 @@ __global__ void __launch_bounds__(kThreads, 2) qk_bwd_rows_kernel(const QkArgs a
 // General kernels.  One warp per (position, head) row, any D and any strides.
 __global__ void __launch_bounds__(kThreads) qk_fwd_kernel(const QkArgs a) {
   extern __shared__ float smem[];
+  begin_after_previous();
   const int half = a.R >> 1, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   float2 *cs = reinterpret_cast<float2 *>(smem);
   float *row = smem + 2 * kPos * half + warp * a.D;
@@ -569,6 +573,7 @@ __global__ void __launch_bounds__(kThreads) qk_fwd_kernel(const QkArgs a) {
 // qk_params_kernel adds those.
 __global__ void __launch_bounds__(kThreads) qk_bwd_kernel(const QkArgs a, int warps) {
   extern __shared__ float smem[];
+  begin_after_previous();
   const int half = a.R >> 1, warp = threadIdx.x / 32, lane = threadIdx.x % 32, D = a.D;
   float2 *cs = reinterpret_cast<float2 *>(smem);
   float *row = smem + 2 * kPos * half + warp * 2 * D, *grad = row + D;
@@ -645,6 +650,7 @@ __global__ void __launch_bounds__(1024)
     qk_params_kernel(const float *partial, int blocks, int D, float *qw, float *qb, float *kw,
                      float *kb) {
   __shared__ double part[32][32];
+  begin_after_previous();
   const int c = threadIdx.x % 32, r = threadIdx.x / 32, n = blockIdx.x * 32 + c;
   double t = 0.0;
   if (n < 4 * D)
@@ -732,36 +738,37 @@ cudaError_t launch_qk_fwd(const QkArgs &a, cudaStream_t stream) {
   if (by_rows(a, false)) {
     const int each = kWarps * groups_of(a.D);
     const int64_t blocks = (a.positions_total + each - 1) / each;
-    rows_kernel(a, false)<<<static_cast<unsigned>(blocks), kThreads, each * a.R * 4, stream>>>(a);
-    return cudaGetLastError();
+    return launch_after_previous(rows_kernel(a, false), static_cast<unsigned>(blocks), kThreads,
+                                 each * a.R * 4, stream, a);
   }
   const size_t smem = (static_cast<size_t>(kPos) * a.R + kWarps * static_cast<size_t>(a.D)) * 4;
   cudaError_t e = allow_smem(reinterpret_cast<const void *>(qk_fwd_kernel), smem);
   if (e != cudaSuccess) return e;
   const int64_t blocks = (a.positions_total + kPos - 1) / kPos;
-  qk_fwd_kernel<<<static_cast<unsigned>(blocks), kThreads, smem, stream>>>(a);
-  return cudaGetLastError();
+  return launch_after_previous(qk_fwd_kernel, static_cast<unsigned>(blocks), kThreads, smem, stream,
+                               a);
 }
 
 cudaError_t launch_qk_bwd(const QkArgs &a, int num_sms, cudaStream_t stream) {
   int blocks;
+  cudaError_t e;
   if (by_rows(a, true)) {
     const int each = kWarps * groups_of(a.D);
     blocks = bwd_blocks(a.positions_total, each, 2, num_sms);
-    rows_kernel(a, true)<<<blocks, kThreads, (each * a.R + kWarps * 8 * 32 * 4) * 4, stream>>>(a);
+    e = launch_after_previous(rows_kernel(a, true), blocks, kThreads,
+                              (each * a.R + kWarps * 8 * 32 * 4) * 4, stream, a);
   } else {
     const int warps = bwd_warps(a.D);
     blocks = bwd_blocks(a.positions_total, kPos, 4, num_sms);
     const size_t smem = (static_cast<size_t>(kPos) * a.R + warps * 6 * static_cast<size_t>(a.D)) * 4;
-    const cudaError_t e = allow_smem(reinterpret_cast<const void *>(qk_bwd_kernel), smem);
+    e = allow_smem(reinterpret_cast<const void *>(qk_bwd_kernel), smem);
     if (e != cudaSuccess) return e;
-    qk_bwd_kernel<<<blocks, warps * 32, smem, stream>>>(a, warps);
+    e = launch_after_previous(qk_bwd_kernel, blocks, warps * 32, smem, stream, a, warps);
   }
-  const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !a.partial) return e;
-  qk_params_kernel<<<(4 * a.D + 31) / 32, 1024, 0, stream>>>(
-      a.partial, blocks, a.D, a.side[0].dw, a.side[0].db, a.side[1].dw, a.side[1].db);
-  return cudaGetLastError();
+  return launch_after_previous(qk_params_kernel, (4 * a.D + 31) / 32, 1024, 0, stream, a.partial,
+                               blocks, a.D, a.side[0].dw, a.side[0].db, a.side[1].dw,
+                               a.side[1].db);
 }
 
 }  // namespace ag
