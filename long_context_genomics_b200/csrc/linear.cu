@@ -16,7 +16,14 @@ namespace {
 
 // --------------------------------------------------------------------------
 // The plan of a product on `clusters` 2-SM clusters: the tile width and the
-// parts of the summed dimension with the least estimated time, in cycles.
+// parts of the summed dimension with the least estimated time, in SM cycles.
+// Fitted to measurements of 20 shapes (8 x 8 to 16384 x 4096 x 1024; splits 1
+// to 24, both widths): 64 terms of a tile take 620 cycles at width 256 and 430
+// at 128 (twice the columns per row of A that is read), a kernel 10500 or 8700
+// beside its sums, and joining splits a launch and the traffic of the partial
+// sums.  Some of both sides, us: 1024 x 1024 x 1024 width 256 11.0, 128 8.4;
+// 4096 x 4096 x 1024 28.7, 35.3; 1152 x 1024 x 8192 in 1, 3, 7 parts 43.8,
+// 24.4, 27.1; 300 x 136 x 4096 in 1, 8, 24 parts 17.5, 10.3, 11.
 GemmPlan plan_gemm(int64_t M, int64_t N, int64_t K, int clusters) {
   const int64_t k_tiles = (K + 63) / 64;
   GemmPlan best{256, 1};
@@ -26,10 +33,9 @@ GemmPlan plan_gemm(int64_t M, int64_t N, int64_t K, int clusters) {
     for (int splits = 1; splits <= 32 && splits <= k_tiles; ++splits) {
       const int64_t waves = (tiles * splits + clusters - 1) / clusters;
       const int64_t deep = (k_tiles + splits - 1) / splits;
-      double t = static_cast<double>(waves) * (deep * (bn == 256 ? 530 : 300) + 500) +
-                 (bn == 256 ? 4000 : 2500);
-      // The join: a second launch, and every partial sum written and read.
-      if (splits > 1) t += 4000 + static_cast<double>(splits) * M * partial_ld(N) * 8 / 4000;
+      double t = static_cast<double>(waves) * (deep * (bn == 256 ? 620 : 430) + 300) +
+                 (bn == 256 ? 10500 : 8700);
+      if (splits > 1) t += 6000 + static_cast<double>(splits) * M * partial_ld(N) * 8 / 4000;
       if (least == 0 || t < least) least = t, best = {bn, splits};
     }
   }
@@ -60,13 +66,21 @@ __global__ void __launch_bounds__(256)
   linear_finish<V>(e, v, bias, row, col);
 }
 
-// A copy of a 16-bit matrix with rows that TMA can read.
-__global__ void __launch_bounds__(256)
-    pack_rows_kernel(const uint16_t *__restrict__ from, int64_t ld_from, uint16_t *__restrict__ to,
-                     int64_t ld_to, int64_t rows, int64_t cols) {
+// Copies of 16-bit matrices with rows that TMA can read, all in one launch.
+struct Copies {
+  struct One {
+    const uint16_t *from;
+    uint16_t *to;
+    int64_t ld_from, ld_to, rows, cols;
+  } m[3];
+  int n;
+};
+__global__ void __launch_bounds__(256) pack_rows_kernel(const Copies c) {
   begin_after_previous();
-  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
-    for (int64_t c = threadIdx.x; c < cols; c += 256) to[r * ld_to + c] = from[r * ld_from + c];
+  const Copies::One m = c.m[blockIdx.y];
+  for (int64_t r = blockIdx.x; r < m.rows; r += gridDim.x)
+    for (int64_t k = threadIdx.x; k < m.cols; k += 256)
+      m.to[r * m.ld_to + k] = m.from[r * m.ld_from + k];
 }
 
 // db[n] = sum_m dy[m, n].  A block takes 32 V columns and a part of the rows:
@@ -233,13 +247,20 @@ Packed place(const void *p, int64_t rows, int64_t cols, int64_t ld, Workspace &w
   const int64_t ld_to = (cols + 7) / 8 * 8;
   return {{ws.take(rows * ld_to * 2), rows, cols, ld_to}, true};
 }
-cudaError_t fill(const Packed &k, const void *p, int64_t ld, int num_sms, cudaStream_t s) {
-  if (!k.copy) return cudaSuccess;
-  const int64_t blocks = k.op.rows < 16 * num_sms ? k.op.rows : 16 * num_sms;
-  return launch_after_previous(pack_rows_kernel, static_cast<unsigned>(blocks), 256, 0, s,
-                               static_cast<const uint16_t *>(p), ld,
-                               static_cast<uint16_t *>(const_cast<void *>(k.op.p)), k.op.ld,
-                               k.op.rows, k.op.cols);
+// Notes the copy that an operand needs, and makes those noted.
+void note(Copies &c, const Packed &k, const void *p, int64_t ld) {
+  if (!k.copy) return;
+  c.m[c.n++] = {static_cast<const uint16_t *>(p),
+                static_cast<uint16_t *>(const_cast<void *>(k.op.p)), ld, k.op.ld, k.op.rows,
+                k.op.cols};
+}
+cudaError_t make(const Copies &c, int num_sms, cudaStream_t s) {
+  if (c.n == 0) return cudaSuccess;
+  int64_t rows = 0;
+  for (int i = 0; i < c.n; ++i) rows = c.m[i].rows > rows ? c.m[i].rows : rows;
+  const int64_t blocks = rows < 16 * num_sms ? rows : 16 * num_sms;
+  return launch_after_previous(pack_rows_kernel, dim3(static_cast<unsigned>(blocks), c.n), 256, 0, s,
+                               c);
 }
 
 int64_t partial_bytes(const GemmPlan &plan, int64_t M, int64_t N) {
@@ -329,8 +350,10 @@ cudaError_t launch_linear_fwd(const LinearFwd &a) {
                       : launch_skinny<8>(a);
   Workspace ws{static_cast<char *>(a.workspace)};
   const FwdLayout l = fwd_layout(a, ws);
-  cudaError_t e = fill(l.x, a.x, a.ldx, a.num_sms, a.stream);
-  if (e == cudaSuccess) e = fill(l.W, a.W, a.ldw, a.num_sms, a.stream);
+  Copies copies{};
+  note(copies, l.x, a.x, a.ldx);
+  note(copies, l.W, a.W, a.ldw);
+  const cudaError_t e = make(copies, a.num_sms, a.stream);
   if (e != cudaSuccess) return e;
   Gemm g{l.x.op, l.W.op, false, false, a.M, a.N, a.K, l.plan, l.partial, a.epi,
          a.num_sms, a.err, a.encode, a.stream};
@@ -347,9 +370,11 @@ cudaError_t linear_bwd_workspace(const LinearBwd &a, int64_t *bytes) {
 cudaError_t launch_linear_bwd(const LinearBwd &a) {
   Workspace ws{static_cast<char *>(a.workspace)};
   const BwdLayout l = bwd_layout(a, ws);
-  cudaError_t e = fill(l.dy, a.dy, a.lddy, a.num_sms, a.stream);
-  if (e == cudaSuccess) e = fill(l.W, a.W, a.ldw, a.num_sms, a.stream);
-  if (e == cudaSuccess) e = fill(l.x, a.x, a.ldx, a.num_sms, a.stream);
+  Copies copies{};
+  note(copies, l.dy, a.dy, a.lddy);
+  note(copies, l.W, a.W, a.ldw);
+  note(copies, l.x, a.x, a.ldx);
+  cudaError_t e = make(copies, a.num_sms, a.stream);
   if (e == cudaSuccess && a.dx.out) {
     Gemm g{l.dy.op, l.W.op, false, true, a.M, a.K, a.N, l.dx_plan, l.partial, a.dx,
            a.num_sms, a.err, a.encode, a.stream};

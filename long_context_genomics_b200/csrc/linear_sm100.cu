@@ -288,13 +288,14 @@ struct BoxEpilogue {
   __device__ void begin(int64_t row0, int64_t col0) {
     if (reads() && !writes_pre()) start_read(row0, col0, 0);
   }
-  // Every copy this warp started ends before the CTA does.
+  // Every copy this warp started is done with the CTA's memory before the CTA
+  // ends.
   __device__ void drain() const {
     if (lane == 0) {
       const uint64_t t0 = globaltimer_ns();
       while (started != waited && !mbar_test(smem_u32(in_full), waited & 1u))
         if (globaltimer_ns() - t0 > kWaitLimitNs) break;
-      bulk_wait_all();
+      bulk_wait_read_all();  // (the grid's end waits for the writes themselves)
     }
     __syncwarp();
   }
@@ -397,8 +398,48 @@ __device__ __forceinline__ void start_sums(float2 (&sum)[COLS / 2], const float 
   }
 }
 
+// Eight rows of one column (the rows from r on of the 32 in `stage`).
+__device__ __forceinline__ void finish_column(const LinearEpilogue &e, const float *stage, int r,
+                                              int lane, int64_t row, int64_t rows, int64_t col) {
+  const int n = static_cast<int>(min(static_cast<int64_t>(8), rows - row));
+  float v[8], x[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    v[i] = stage[(r + i) * 32 + (((lane >> 2) ^ ((r + i) & 7)) << 2) + (lane & 3)];
+  const auto load = [&](const void *p, int64_t ld, int dtype) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float one[1] = {0.f};
+      if (i < n) load_values<1>(p, (row + i) * ld + col, dtype, one);
+      x[i] = one[0];
+    }
+  };
+  const auto store = [&](void *p, int64_t ld, int dtype) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float one[1] = {v[i]};
+      if (i < n) store_values<1>(p, (row + i) * ld + col, dtype, one);
+    }
+  };
+  if (e.pre_out) store(e.pre_out, e.ld_pre_out, e.dtype);
+  if (e.pre_in) {
+    load(e.pre_in, e.ld_pre_in, e.dtype);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] *= act_slope(x[i], e.act);
+  } else if (e.act != AG_ACT_NONE) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = act_value(v[i], e.act);
+  }
+  if (e.residual) {
+    load(e.residual, e.ld_res, e.out_dtype);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] += x[i];
+  }
+  store(e.out, e.ld_out, e.out_dtype);
+}
+
 // The same without boxes: 32 columns at a time through a box's memory (float4
-// q of row r in slot q ^ (r % 8)), then a lane per column, row by row.
+// q of row r in slot q ^ (r % 8)), then a lane per column, eight rows at a time.
 template <int COLS>
 __device__ __forceinline__ void plain_epilogue(const Params &p, const float2 (&sum)[COLS / 2],
                                                float *stage, int64_t row0, int64_t col0, int lane) {
@@ -414,12 +455,9 @@ __device__ __forceinline__ void plain_epilogue(const Params &p, const float2 (&s
     __syncwarp();
     const int64_t col = col0 + c + lane;
     if (col < p.N) {
-      const float bias[1] = {0.f};  // the sums started from it
 #pragma unroll 1
-      for (int r = 0; r < 32 && row0 + r < p.M; ++r) {
-        float v[1] = {stage[r * 32 + (((lane >> 2) ^ (r & 7)) << 2) + (lane & 3)]};
-        linear_finish<1>(p.epi, v, bias, row0 + r, col);
-      }
+      for (int r = 0; r < 32; r += 8)
+        if (row0 + r < p.M) finish_column(p.epi, stage, r, lane, row0 + r, p.M, col);
     }
   }
 }

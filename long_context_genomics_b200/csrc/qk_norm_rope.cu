@@ -19,7 +19,8 @@
 // forward takes four, the backward two row steps at a time): that many bytes in
 // flight is what the memory's rate asks for.
 //
-// General kernels: one warp per row through shared memory, any size or stride.
+// General kernels: one warp per row through shared memory, any size or stride.  A
+// block takes `at_once` positions a turn, enough for a row to each warp.
 #include "ag_internal.h"
 #include "launch.cuh"
 #include "linear_epilogue.cuh"
@@ -27,7 +28,6 @@
 namespace ag {
 namespace {
 
-constexpr int kPos = 4;        // positions per block and turn
 constexpr int kThreads = 256;  // 8 warps
 constexpr int kWarps = kThreads / 32;
 
@@ -523,14 +523,14 @@ __global__ void __launch_bounds__(kThreads, 2) qk_bwd_rows_kernel(const QkArgs a
 
 // --------------------------------------------------------------------------
 // General kernels.  One warp per (position, head) row, any D and any strides.
-__global__ void __launch_bounds__(kThreads) qk_fwd_kernel(const QkArgs a) {
+__global__ void __launch_bounds__(kThreads) qk_fwd_kernel(const QkArgs a, int at_once) {
   extern __shared__ float smem[];
   begin_after_previous();
   const int half = a.R >> 1, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   float2 *cs = reinterpret_cast<float2 *>(smem);
-  float *row = smem + 2 * kPos * half + warp * a.D;
-  const int64_t p0 = static_cast<int64_t>(blockIdx.x) * kPos;
-  const int np = static_cast<int>(min(static_cast<int64_t>(kPos), a.positions_total - p0));
+  float *row = smem + 2 * at_once * half + warp * a.D;
+  const int64_t p0 = static_cast<int64_t>(blockIdx.x) * at_once;
+  const int np = static_cast<int>(min(static_cast<int64_t>(at_once), a.positions_total - p0));
   for (int i = threadIdx.x; i < np * half; i += kThreads) {
     const int64_t b = (p0 + i / half) / a.L, l = (p0 + i / half) % a.L;
     cs[i] = turn(a.positions ? a.positions[b * a.pos_sb + l] : l, a.inv_freq[i % half]);
@@ -571,19 +571,19 @@ __global__ void __launch_bounds__(kThreads) qk_fwd_kernel(const QkArgs a) {
 // its own part of shared memory (element i always by lane i % 32: no atomics),
 // the block then adds its warps' in order and writes one partial per block;
 // qk_params_kernel adds those.
-__global__ void __launch_bounds__(kThreads) qk_bwd_kernel(const QkArgs a, int warps) {
+__global__ void __launch_bounds__(kThreads) qk_bwd_kernel(const QkArgs a, int warps, int at_once) {
   extern __shared__ float smem[];
   begin_after_previous();
   const int half = a.R >> 1, warp = threadIdx.x / 32, lane = threadIdx.x % 32, D = a.D;
   float2 *cs = reinterpret_cast<float2 *>(smem);
-  float *row = smem + 2 * kPos * half + warp * 2 * D, *grad = row + D;
-  float *sums = smem + 2 * kPos * half + warps * 2 * D;  // [warps][2 sides][w, b][D]
+  float *row = smem + 2 * at_once * half + warp * 2 * D, *grad = row + D;
+  float *sums = smem + 2 * at_once * half + warps * 2 * D;  // [warps][2 sides][w, b][D]
   float *own = sums + warp * 4 * D;
   for (int i = lane; i < 4 * D; i += 32) own[i] = 0.f;
   const int heads = a.side[0].H + a.side[1].H;
-  for (int64_t p0 = static_cast<int64_t>(blockIdx.x) * kPos; p0 < a.positions_total;
-       p0 += static_cast<int64_t>(gridDim.x) * kPos) {
-    const int np = static_cast<int>(min(static_cast<int64_t>(kPos), a.positions_total - p0));
+  for (int64_t p0 = static_cast<int64_t>(blockIdx.x) * at_once; p0 < a.positions_total;
+       p0 += static_cast<int64_t>(gridDim.x) * at_once) {
+    const int np = static_cast<int>(min(static_cast<int64_t>(at_once), a.positions_total - p0));
     __syncthreads();
     for (int i = threadIdx.x; i < np * half; i += blockDim.x) {
       const int64_t b = (p0 + i / half) / a.L, l = (p0 + i / half) % a.L;
@@ -682,8 +682,14 @@ bool by_rows(const QkArgs &a, bool backward) {
 }
 
 int bwd_warps(int D) { return D <= 512 ? 8 : 4; }
+// Positions a turn of the general kernels: a row to each of 8 warps.
+int positions_at_once(const QkArgs &a) {
+  const int heads = a.side[0].H + a.side[1].H;
+  return heads >= 8 ? 1 : (8 + heads - 1) / heads;
+}
 // Blocks of a backward, as many as its partial sums: the rows kernel's two to an
-// SM, the general one's four, but no more than have work.
+// SM, the general one's kGeneralPerSm, but no more than have work.
+constexpr int kGeneralPerSm = 6;
 int bwd_blocks(int64_t total, int64_t each, int per_sm, int num_sms) {
   const int64_t turns = (total + each - 1) / each;
   return static_cast<int>(turns < per_sm * num_sms ? turns : per_sm * num_sms);
@@ -698,7 +704,8 @@ cudaError_t allow_smem(const void *kernel, size_t bytes) {
 }  // namespace
 
 int64_t qk_bwd_workspace(int64_t positions_total, int64_t D, int num_sms) {
-  return static_cast<int64_t>(bwd_blocks(positions_total, kPos, 4, num_sms)) * 4 * D * 4;
+  return static_cast<int64_t>(bwd_blocks(positions_total, 1, kGeneralPerSm, num_sms)) * 4 * D *
+         4;
 }
 
 namespace {
@@ -741,12 +748,13 @@ cudaError_t launch_qk_fwd(const QkArgs &a, cudaStream_t stream) {
     return launch_after_previous(rows_kernel(a, false), static_cast<unsigned>(blocks), kThreads,
                                  each * a.R * 4, stream, a);
   }
-  const size_t smem = (static_cast<size_t>(kPos) * a.R + kWarps * static_cast<size_t>(a.D)) * 4;
+  const int at_once = positions_at_once(a);
+  const size_t smem = (static_cast<size_t>(at_once) * a.R + kWarps * static_cast<size_t>(a.D)) * 4;
   cudaError_t e = allow_smem(reinterpret_cast<const void *>(qk_fwd_kernel), smem);
   if (e != cudaSuccess) return e;
-  const int64_t blocks = (a.positions_total + kPos - 1) / kPos;
+  const int64_t blocks = (a.positions_total + at_once - 1) / at_once;
   return launch_after_previous(qk_fwd_kernel, static_cast<unsigned>(blocks), kThreads, smem, stream,
-                               a);
+                               a, at_once);
 }
 
 cudaError_t launch_qk_bwd(const QkArgs &a, int num_sms, cudaStream_t stream) {
@@ -758,12 +766,13 @@ cudaError_t launch_qk_bwd(const QkArgs &a, int num_sms, cudaStream_t stream) {
     e = launch_after_previous(rows_kernel(a, true), blocks, kThreads,
                               (each * a.R + kWarps * 8 * 32 * 4) * 4, stream, a);
   } else {
-    const int warps = bwd_warps(a.D);
-    blocks = bwd_blocks(a.positions_total, kPos, 4, num_sms);
-    const size_t smem = (static_cast<size_t>(kPos) * a.R + warps * 6 * static_cast<size_t>(a.D)) * 4;
+    const int warps = bwd_warps(a.D), at_once = positions_at_once(a);
+    blocks = bwd_blocks(a.positions_total, at_once, kGeneralPerSm, num_sms);
+    const size_t smem =
+        (static_cast<size_t>(at_once) * a.R + warps * 6 * static_cast<size_t>(a.D)) * 4;
     e = allow_smem(reinterpret_cast<const void *>(qk_bwd_kernel), smem);
     if (e != cudaSuccess) return e;
-    e = launch_after_previous(qk_bwd_kernel, blocks, warps * 32, smem, stream, a, warps);
+    e = launch_after_previous(qk_bwd_kernel, blocks, warps * 32, smem, stream, a, warps, at_once);
   }
   if (e != cudaSuccess || !a.partial) return e;
   return launch_after_previous(qk_params_kernel, (4 * a.D + 31) / 32, 1024, 0, stream, a.partial,
