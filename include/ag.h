@@ -518,8 +518,8 @@ ag_status ag_qk_norm_rope_bwd(const void *dq_out, const void *dk_out, int g_dtyp
 
 /* Bytes of workspace that ag_qk_norm_rope_bwd takes on the current device
  * (0 when none of the four weight and bias gradients is wanted). */
-ag_status ag_qk_norm_rope_bwd_workspace(int64_t B, int64_t L, int64_t D, int wants_params,
-                                        int64_t *bytes);
+ag_status ag_qk_norm_rope_bwd_workspace(int64_t B, int64_t Hq, int64_t Hk, int64_t L, int64_t D,
+                                        int wants_params, int64_t *bytes);
 
 /*
  * ag_grad_clip -- the global 2-norm of n gradient tensors, and their scaling

@@ -105,7 +105,7 @@ def _load() -> ctypes.CDLL:
                                         + [i32, vp, vp, i32, f32, vp, i64, i32, vp, i64, i64,
                                            i64, i64, i64, i64] + heads + heads
                                         + [vp, vp, vp, vp, vp, i64, vp])
-    lib.ag_qk_norm_rope_bwd_workspace.argtypes = [i64, i64, i64, i32, i64p]
+    lib.ag_qk_norm_rope_bwd_workspace.argtypes = [i64, i64, i64, i64, i64, i32, i64p]
     lib.ag_grad_clip.argtypes = [vp, vp, vp, i64, f32, f32, vp, vp, i64, vp]
     lib.ag_grad_clip_workspace.argtypes = [i64, i64p]
     for fn in (lib.ag_linear_fwd, lib.ag_linear_fwd_workspace, lib.ag_linear_bwd,
@@ -769,7 +769,7 @@ def ag_qk_norm_rope_bwd(dq_out: torch.Tensor | None, dk_out: torch.Tensor | None
         params = [None if t is None else next(rows) for t in inputs]
         p = [None if t is None else t.data_ptr() for t in params]
         ws, wsp, n = _workspace(lib.ag_qk_norm_rope_bwd_workspace, dev,
-                                "ag_qk_norm_rope_bwd_workspace", B, L, D, 1)
+                                "ag_qk_norm_rope_bwd_workspace", B, Hq, Hk, L, D, 1)
     st = lib.ag_qk_norm_rope_bwd(
         gq, gk, gt, qp, qb, ql, qh, kp, kb, kl, kh, DTYPES[T], used[0], used[1],
         _code(NORMS, norm, "norm"), eps, *_rotation(inv_freq, rope, positions, B, L, dev), B, Hq,

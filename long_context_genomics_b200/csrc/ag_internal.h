@@ -164,9 +164,9 @@ struct QkArgs {
   float eps;
   float *partial;         // backward: parameter gradients' partial sums
 };
-cudaError_t launch_qk_fwd(const QkArgs &a, cudaStream_t stream);
+cudaError_t launch_qk_fwd(const QkArgs &a, int num_sms, cudaStream_t stream);
 cudaError_t launch_qk_bwd(const QkArgs &a, int num_sms, cudaStream_t stream);
-int64_t qk_bwd_workspace(int64_t positions_total, int64_t D, int num_sms);
+int64_t qk_bwd_workspace(int64_t positions_total, int Hq, int Hk, int D, int num_sms);
 
 // Global gradient norm and clipping (grad_clip.cu).
 cudaError_t launch_grad_clip(void *const *grads, const int64_t *counts, const int *dtypes,

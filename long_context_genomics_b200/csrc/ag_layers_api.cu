@@ -401,20 +401,21 @@ ag_status ag_qk_norm_rope_fwd(const void *q, int64_t q_sb, int64_t q_sl, int64_t
   a.positions_total = B * L, a.B = B, a.L = L;
   a.D = static_cast<int>(D), a.R = static_cast<int>(R);
   a.norm = norm, a.rope = rope, a.x_dtype = x_dtype, a.o_dtype = out_dtype, a.eps = eps;
-  return ag::from_cuda(ag::launch_qk_fwd(a, static_cast<cudaStream_t>(stream)));
+  return ag::from_cuda(ag::launch_qk_fwd(a, dev->num_sms, static_cast<cudaStream_t>(stream)));
 }
 
-ag_status ag_qk_norm_rope_bwd_workspace(int64_t B, int64_t L, int64_t D, int wants_params,
-                                        int64_t *bytes) {
+ag_status ag_qk_norm_rope_bwd_workspace(int64_t B, int64_t Hq, int64_t Hk, int64_t L, int64_t D,
+                                        int wants_params, int64_t *bytes) {
   if (!bytes) return AG_ERR_NULL;
-  const ag_status st = ag::check_qk(B, 1, 0, L, D, 0, AG_NORM_NONE, 0.f, 0, AG_F32, AG_F32, 0);
+  const ag_status st = ag::check_qk(B, Hq, Hk, L, D, 0, AG_NORM_NONE, 0.f, 0, AG_F32, AG_F32, 0);
   if (st != AG_OK) return st;
   *bytes = 0;
-  if (!wants_params || B * L == 0) return AG_OK;
+  if (!wants_params || B * L == 0 || Hq + Hk == 0) return AG_OK;
   ag::DeviceInfo *dev = nullptr;
   const ag_status ds = ag::device_info(&dev);
   if (ds != AG_OK) return ds;
-  *bytes = ag::qk_bwd_workspace(B * L, D, dev->num_sms);
+  *bytes = ag::qk_bwd_workspace(B * L, static_cast<int>(Hq), static_cast<int>(Hk),
+                                static_cast<int>(D), dev->num_sms);
   return AG_OK;
 }
 
@@ -493,7 +494,7 @@ ag_status ag_qk_norm_rope_bwd(const void *dq_out, const void *dk_out, int g_dtyp
   for (int i = 0; i < 4; ++i) outs[2 + i] = {params[i], params[i] ? row : 0};
   ag::DeviceInfo *dev = nullptr;
   st = ag::device_info(&dev);
-  const int64_t need = st == AG_OK && wants ? ag::qk_bwd_workspace(B * L, D, dev->num_sms) : 0;
+  const int64_t need = st == AG_OK && wants ? ag::qk_bwd_workspace(B * L, static_cast<int>(Hq), static_cast<int>(Hk), static_cast<int>(D), dev->num_sms) : 0;
   outs[6] = {workspace, workspace ? static_cast<uint64_t>(need) : 0u};
   for (int o = 0; o < 7; ++o) {
     for (const Range &r : ins)
