@@ -29,6 +29,7 @@ import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libag.so")
+LAYERS_PATH = os.path.join(_HERE, "_layers.so")
 
 AG_OK = 0
 STATUS_NAMES = {
@@ -121,6 +122,16 @@ def _load() -> ctypes.CDLL:
 
 
 lib = _load()
+if not os.path.exists(LAYERS_PATH):
+    raise ImportError(
+        f"{LAYERS_PATH} is missing: build it with "
+        "`python long_context_genomics_b200/build.py` (or __graft_entry__.build())")
+from . import _layers  # noqa: E402  (the compiled half of the layers' binding)
+
+_layers.bind(tuple(ctypes.cast(f, ctypes.c_void_p).value for f in (
+    lib.ag_linear_fwd, lib.ag_linear_fwd_workspace, lib.ag_linear_bwd,
+    lib.ag_linear_bwd_workspace, lib.ag_qk_norm_rope_fwd, lib.ag_qk_norm_rope_bwd,
+    lib.ag_qk_norm_rope_bwd_workspace, lib.ag_grad_clip, lib.ag_grad_clip_workspace)), AgError)
 
 
 def ag_status_string(status: int) -> str:
@@ -379,36 +390,28 @@ def ag_attn_bwd_launch_count(Dv: int = 128) -> int:
 
 
 # ---------------------------------------------------------------------------
-# The layers around the attention.
+# The layers around the attention.  Their tensors are checked and their calls
+# made by _layers (csrc/layers_binding.cpp); what is here is the interface.
 
-DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 NORMS = {"none": 0, "rms": 1, "layer": 2}
 ROPES = {"halves": 0, "interleaved": 1}
-_HALF = (torch.bfloat16, torch.float16)
 
 
-def _elsewhere(dev: torch.device, stream) -> bool:
-    """Whether a call for tensors on dev has to enter _site first."""
-    return stream is not None or torch._C._cuda_getDevice() != dev.index
-
-
-def _site(dev: torch.device, stream):
+def _site(t, stream):
     """Context in which a call's memory is allocated and its kernels launched:
-    the tensors' device and the caller's stream (default: that device's
-    current stream).  Workspaces belong to that stream, so a later call on it
-    may take their memory over, and no other stream does."""
-    if stream is None:
-        return torch.cuda.device(dev)
+    the device of its first tensor and the caller's stream (a Stream or a raw
+    handle).  Without a stream a call takes the current one of that device.
+    Workspaces belong to the stream, so a later call on it may take their
+    memory over, and no other stream does."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError("the first tensor of the call must be on a CUDA device")
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=dev)
-    if stream.device != dev:
-        raise ValueError(f"stream is on {stream.device}, the tensors are on {dev}")
+        stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)),
+                                           device=t.device)
+    if stream.device != t.device:
+        raise ValueError(f"stream is on {stream.device}, the tensors are on {t.device}")
     return torch.cuda.stream(stream)
-
-
-def _current(dev: torch.device) -> int:
-    return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
 def _code(table: dict, value, name: str) -> int:
@@ -416,59 +419,6 @@ def _code(table: dict, value, name: str) -> int:
         return table[value]
     except (KeyError, TypeError):
         raise ValueError(f"{name} must be one of {', '.join(map(str, table))}, got {value}") from None
-
-
-def _on_gpu(t, name: str, dtypes) -> None:
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be on a CUDA device")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
-
-
-def _same_device(t, name: str, dev: torch.device) -> None:
-    if t.device != dev:
-        raise ValueError(f"all tensors of a call must be on {dev}; {name} is on {t.device}")
-
-
-def _matrix(t, name: str, dtype, rows: int, cols: int, dev: torch.device) -> int:
-    """Checks a row-major matrix (its rows may be apart) and returns its row
-    stride.  (The checks of the layers' calls are written for the case that
-    all is well: at a few rows they cost as much as the kernel.)"""
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == (rows, cols) \
-            and t.device == dev:
-        ld, inner = t.stride()
-        if inner == 1 or cols == 1:
-            return ld if rows > 1 or ld > cols else cols
-        raise ValueError(f"the rows of {name} must be dense")
-    _on_gpu(t, name, (dtype,))
-    _same_device(t, name, dev)
-    raise ValueError(f"{name} must be [{rows},{cols}], got {list(t.shape)}")
-
-
-def _vector(t, name: str, n: int, dev: torch.device):
-    """Checks an optional dense float32 vector of n and returns its pointer."""
-    if t is None:
-        return None
-    if isinstance(t, torch.Tensor) and t.dtype is torch.float32 and t.shape == (n,) \
-            and t.device == dev and t.is_contiguous():
-        return t.data_ptr()
-    _on_gpu(t, name, (torch.float32,))
-    _same_device(t, name, dev)
-    raise ValueError(f"{name} must be a contiguous [{n}]")
-
-
-def _workspace(query, dev: torch.device, name: str, *args):
-    """Workspace of the bytes that `query` gives for args: (tensor, pointer, bytes)."""
-    n = ctypes.c_int64(0)
-    st = query(*args, ctypes.byref(n))
-    if st != AG_OK:
-        raise AgError(name, st)
-    if n.value == 0:
-        return None, None, 0
-    t = torch.empty(n.value, dtype=torch.uint8, device=dev)
-    return t, t.data_ptr(), n.value
 
 
 def ag_linear_fwd(x: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = None,
@@ -482,43 +432,11 @@ def ag_linear_fwd(x: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = 
     act: none, relu, gelu, gelu_tanh, silu.  preact=True (or a [M,N] tensor of
     x's type to write) also returns x W^T + bias, which ag_linear_bwd of the
     next layer takes: (y, preact).  out may be the residual itself."""
-    _on_gpu(x, "x", _HALF)
-    if x.ndim != 2 or not isinstance(W, torch.Tensor) or W.ndim != 2:
-        raise ValueError("x must be [M,K] and W [N,K]")
-    dev = x.device
-    if _elsewhere(dev, stream):
-        with _site(dev, stream):
+    if stream is not None:
+        with _site(x, stream):
             return ag_linear_fwd(x, W, bias, act, residual, preact, out, out_dtype)
-    (M, K), N, T = x.shape, W.shape[0], x.dtype
-    ldx, ldw = _matrix(x, "x", T, M, K, dev), _matrix(W, "W", T, N, K, dev)
-    code = _code(ACTIVATIONS, act, "act")
-    if out_dtype is None:
-        out_dtype = T if out is None else out.dtype
-    if out_dtype is not T and out_dtype is not torch.float32:
-        raise TypeError(f"out_dtype must be {T} or torch.float32, got {out_dtype}")
-    b = _vector(bias, "bias", N, dev)
-    r, ldr, z, zp, ldz = None, 0, None, None, 0
-    if residual is not None:
-        ldr, r = _matrix(residual, "residual", out_dtype, M, N, dev), residual.data_ptr()
-    if out is None:
-        out, ldy = x.new_empty((M, N), dtype=out_dtype), N
-    else:
-        ldy = _matrix(out, "out", out_dtype, M, N, dev)
-    if preact is not False and preact is not None:
-        z = x.new_empty((M, N)) if preact is True else preact
-        ldz, zp = _matrix(z, "preact", T, M, N, dev), z.data_ptr()
-    xp, wp, yp, t, yt = x.data_ptr(), W.data_ptr(), out.data_ptr(), DTYPES[T], DTYPES[out_dtype]
-    # Most calls need no workspace; the others say so before they do anything.
-    st = lib.ag_linear_fwd(xp, ldx, wp, ldw, b, r, ldr, M, N, K, t, code, zp, ldz, yp, ldy, yt,
-                           None, 0, _current(dev))
-    if st == 9:
-        ws, wsp, n = _workspace(lib.ag_linear_fwd_workspace, dev, "ag_linear_fwd_workspace", xp,
-                                ldx, wp, ldw, M, N, K)
-        st = lib.ag_linear_fwd(xp, ldx, wp, ldw, b, r, ldr, M, N, K, t, code, zp, ldz, yp, ldy,
-                               yt, wsp, n, _current(dev))
-    if st != AG_OK:
-        raise AgError("ag_linear_fwd", st)
-    return out if z is None else (out, z)
+    return _layers.linear_fwd(x, W, bias, _code(ACTIVATIONS, act, "act"), residual, preact, out,
+                              out_dtype)
 
 
 def ag_linear_bwd(dy: torch.Tensor, x: torch.Tensor, W: torch.Tensor, act: str = "none",
@@ -533,49 +451,12 @@ def ag_linear_bwd(dy: torch.Tensor, x: torch.Tensor, W: torch.Tensor, act: str =
     the gradient of preact instead of x.  dx_dtype: x's type (default) or
     fp32; dW_dtype: fp32 (default) or x's type.  dx and dW may be given to
     write into.  The gradient of ag_linear_fwd's residual is dy itself."""
-    _on_gpu(dy, "dy", _HALF)
-    if dy.ndim != 2 or not isinstance(x, torch.Tensor) or x.ndim != 2:
-        raise ValueError("dy must be [M,N] and x [M,K]")
-    dev = dy.device
-    if _elsewhere(dev, stream):
-        with _site(dev, stream):
+    if stream is not None:
+        with _site(dy, stream):
             return ag_linear_bwd(dy, x, W, act, preact, need_dx, need_dW, need_db, dx_dtype,
                                  dW_dtype, dx, dW)
-    (M, N), K, T = dy.shape, x.shape[1], dy.dtype
-    lddy, ldx = _matrix(dy, "dy", T, M, N, dev), _matrix(x, "x", T, M, K, dev)
-    ldw = _matrix(W, "W", T, N, K, dev)
-    code = _code(ACTIVATIONS, act, "act")
-    ldz = 0 if preact is None else _matrix(preact, "preact", T, M, K, dev)
-    if code and preact is None:
-        raise ValueError(f"act {act} needs the preact of x")
-    dxp = dwp = dbp = None
-    lddx = lddw = dxt = dwt = 0
-    if need_dx:
-        dx_dtype = dx_dtype or (T if dx is None else dx.dtype)
-        if dx_dtype is not T and dx_dtype is not torch.float32:
-            raise TypeError(f"dx_dtype must be {T} or torch.float32, got {dx_dtype}")
-        if dx is None:
-            dx = dy.new_empty((M, K), dtype=dx_dtype)
-        lddx, dxp, dxt = _matrix(dx, "dx", dx_dtype, M, K, dev), dx.data_ptr(), DTYPES[dx_dtype]
-    if need_dW:
-        dW_dtype = dW_dtype if dW is None else dW.dtype
-        if dW_dtype is not T and dW_dtype is not torch.float32:
-            raise TypeError(f"dW_dtype must be {T} or torch.float32, got {dW_dtype}")
-        if dW is None:
-            dW = dy.new_empty((N, K), dtype=dW_dtype)
-        lddw, dwp, dwt = _matrix(dW, "dW", dW_dtype, N, K, dev), dW.data_ptr(), DTYPES[dW_dtype]
-    db = dy.new_empty(N, dtype=torch.float32) if need_db else None
-    if need_db:
-        dbp = db.data_ptr()
-    dyp, xp, wp = dy.data_ptr(), x.data_ptr(), W.data_ptr()
-    ws, wsp, n = _workspace(lib.ag_linear_bwd_workspace, dev, "ag_linear_bwd_workspace", dyp,
-                            lddy, xp, ldx, wp, ldw, M, N, K, dxp, dwp, dbp)
-    st = lib.ag_linear_bwd(dyp, lddy, xp, ldx, wp, ldw,
-                           None if preact is None else preact.data_ptr(), ldz, code, M, N, K,
-                           DTYPES[T], dxp, lddx, dxt, dwp, lddw, dwt, dbp, wsp, n, _current(dev))
-    if st != AG_OK:
-        raise AgError("ag_linear_bwd", st)
-    return dx if need_dx else None, dW if need_dW else None, db
+    return _layers.linear_bwd(dy, x, W, _code(ACTIVATIONS, act, "act"), preact, need_dx, need_dW,
+                              need_db, dx_dtype, dW_dtype, dx, dW)
 
 
 def ag_rope_frequencies(rotary_dim: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
@@ -583,63 +464,6 @@ def ag_rope_frequencies(rotary_dim: int, base: float = 10000.0, device="cuda") -
     usual frequencies for ag_qk_norm_rope_fwd (which takes any)."""
     p = torch.arange(0, rotary_dim, 2, dtype=torch.float64)
     return (float(base) ** (-p / rotary_dim)).to(device)
-
-
-def _heads(t, name: str, dtype, B: int, L: int, D: int, dev: torch.device):
-    """Checks a [B,L,H,D] (or [B,L,D]: one head) tensor with dense heads;
-    returns H, pointer and the strides over b, l and h."""
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == dev:
-        s = t.shape
-        if len(s) == 4 and s[0] == B and s[1] == L and s[3] == D:
-            sb, sl, sh, sd = t.stride()
-            if sd == 1 or D == 1:
-                return s[2], t.data_ptr(), sb, sl, sh
-            raise ValueError(f"the heads of {name} must be dense")
-        if s == (B, L, D):
-            sb, sl, sd = t.stride()
-            if sd == 1 or D == 1:
-                return 1, t.data_ptr(), sb, sl, 0
-            raise ValueError(f"the heads of {name} must be dense")
-    _on_gpu(t, name, (dtype,))
-    _same_device(t, name, dev)
-    raise ValueError(f"{name} must be [{B},{L},H,{D}] or [{B},{L},{D}], got {list(t.shape)}")
-
-
-def _qk_first(q, k):
-    """Type, device and sizes of a call, from the queries or else the keys."""
-    first, name = (q, "q") if q is not None else (k, "k")
-    if first is None:
-        raise ValueError("q and k are both None")
-    _on_gpu(first, name, DTYPES)
-    if first.ndim not in (3, 4):
-        raise ValueError(f"{name} must be [B,L,H,D] or [B,L,D]")
-    return first, first.dtype, first.device, first.shape[0], first.shape[1], first.shape[-1]
-
-
-def _rotation(inv_freq, rope, positions, B: int, L: int, dev: torch.device):
-    """The rotation's arguments: inv_freq, R, rope, positions, their stride over b."""
-    code, freq, R, where, pos_sb = _code(ROPES, rope, "rope"), None, 0, None, 0
-    if inv_freq is not None:
-        _on_gpu(inv_freq, "inv_freq", (torch.float64,))
-        _same_device(inv_freq, "inv_freq", dev)
-        if inv_freq.ndim != 1 or not inv_freq.is_contiguous():
-            raise ValueError("inv_freq must be a contiguous [R/2]")
-        R, freq = 2 * inv_freq.shape[0], inv_freq.data_ptr()
-    if positions is not None:
-        _on_gpu(positions, "positions", (torch.int64,))
-        _same_device(positions, "positions", dev)
-        if positions.shape != (L,) and positions.shape != (B, L):
-            raise ValueError(f"positions must be [{L}] or [{B},{L}], got {list(positions.shape)}")
-        s = positions.stride()
-        if L > 1 and s[-1] != 1:
-            raise ValueError("the rows of positions must be dense")
-        where = positions.data_ptr()
-        if len(s) == 2 and B > 1:
-            pos_sb = s[0]
-    return freq, R, code, where, pos_sb
-
-
-_NO_HEADS = (0, None, 0, 0, 0)
 
 
 def ag_qk_norm_rope_fwd(q: torch.Tensor | None, k: torch.Tensor | None,
@@ -663,51 +487,13 @@ def ag_qk_norm_rope_fwd(q: torch.Tensor | None, k: torch.Tensor | None,
     ag_rope_frequencies; None: no rotation); positions int64 [L] or [B,L]
     (default 0 .. L-1).  Returns (q_out [B,H,L,D], k_out [B,L,D] or
     [B,Hk,L,D]); q or k may be None."""
-    first, T, dev, B, L, D = _qk_first(q, k)
-    if _elsewhere(dev, stream):
-        with _site(dev, stream):
+    if stream is not None:
+        with _site(k if q is None else q, stream):
             return ag_qk_norm_rope_fwd(q, k, q_weight, k_weight, q_bias, k_bias, norm, eps,
                                        inv_freq, rope, positions, out_dtype, q_out, k_out)
-    Hq, qp, qb, ql, qh = _NO_HEADS if q is None else _heads(q, "q", T, B, L, D, dev)
-    Hk, kp, kb, kl, kh = _NO_HEADS if k is None else _heads(k, "k", T, B, L, D, dev)
-    ot = _code(DTYPES, out_dtype, "out_dtype")
-    qo = ko = None
-    if q is None:
-        q_out = None
-    else:
-        shape = (B, Hq, L, D) if q.ndim == 4 else (B, L, D)
-        if q_out is None:
-            q_out = first.new_empty(shape, dtype=out_dtype)
-            qo = q_out.data_ptr()
-        else:
-            qo = _dense(q_out, "q_out", out_dtype, shape, dev)
-    if k is None:
-        k_out = None
-    else:
-        shape = (B, Hk, L, D) if k.ndim == 4 else (B, L, D)
-        if k_out is None:
-            k_out = first.new_empty(shape, dtype=out_dtype)
-            ko = k_out.data_ptr()
-        else:
-            ko = _dense(k_out, "k_out", out_dtype, shape, dev)
-    st = lib.ag_qk_norm_rope_fwd(
-        qp, qb, ql, qh, kp, kb, kl, kh, DTYPES[T], _vector(q_weight, "q_weight", D, dev),
-        _vector(q_bias, "q_bias", D, dev), _vector(k_weight, "k_weight", D, dev),
-        _vector(k_bias, "k_bias", D, dev), _code(NORMS, norm, "norm"), eps,
-        *_rotation(inv_freq, rope, positions, B, L, dev), B, Hq, Hk, L, D, qo, ko, ot,
-        _current(dev))
-    if st != AG_OK:
-        raise AgError("ag_qk_norm_rope_fwd", st)
-    return q_out, k_out
-
-
-def _dense(t, name: str, dtype, shape: tuple, dev: torch.device) -> int:
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape \
-            and t.device == dev and t.is_contiguous():
-        return t.data_ptr()
-    _on_gpu(t, name, (dtype,))
-    _same_device(t, name, dev)
-    raise ValueError(f"{name} must be a contiguous {list(shape)}, got {list(t.shape)}")
+    return _layers.qk_fwd(q, k, q_weight, k_weight, q_bias, k_bias, _code(NORMS, norm, "norm"),
+                          eps, inv_freq, _code(ROPES, rope, "rope"), positions, out_dtype, q_out,
+                          k_out)
 
 
 def ag_qk_norm_rope_bwd(dq_out: torch.Tensor | None, dk_out: torch.Tensor | None,
@@ -727,69 +513,16 @@ def ag_qk_norm_rope_bwd(dq_out: torch.Tensor | None, dk_out: torch.Tensor | None
     written into the tensors given (which may be slices of one fused
     projection's gradient) or new ones; the others [D] fp32, None where the
     forward had none."""
-    first, T, dev, B, L, D = _qk_first(q, k)
-    if _elsewhere(dev, stream):
-        with _site(dev, stream):
+    if stream is not None:
+        with _site(k if q is None else q, stream):
             return ag_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, q_bias, k_bias,
                                        norm, eps, inv_freq, rope, positions, dq, dk)
-    Hq, qp, qb, ql, qh = _NO_HEADS if q is None else _heads(q, "q", T, B, L, D, dev)
-    Hk, kp, kb, kl, kh = _NO_HEADS if k is None else _heads(k, "k", T, B, L, D, dev)
-    g = dq_out if q is not None else dk_out
-    G = g.dtype if isinstance(g, torch.Tensor) else None
-    gt = _code(DTYPES, G, "the type of dq_out and dk_out")
-    gq = gk = None
-    (_, dqp, dqb, dql, dqh), (_, dkp, dkb, dkl, dkh) = _NO_HEADS, _NO_HEADS
-    if q is None:
-        dq = None
-    else:
-        gq = _dense(dq_out, "dq_out", G, (B, Hq, L, D) if q.ndim == 4 else (B, L, D), dev)
-        if dq is None:
-            dq = first.new_empty(q.shape)
-        elif dq.shape != q.shape:
-            raise ValueError(f"dq must be {list(q.shape)}, got {list(dq.shape)}")
-        _, dqp, dqb, dql, dqh = _heads(dq, "dq", T, B, L, D, dev)
-    if k is None:
-        dk = None
-    else:
-        gk = _dense(dk_out, "dk_out", G, (B, Hk, L, D) if k.ndim == 4 else (B, L, D), dev)
-        if dk is None:
-            dk = first.new_empty(k.shape)
-        elif dk.shape != k.shape:
-            raise ValueError(f"dk must be {list(k.shape)}, got {list(dk.shape)}")
-        _, dkp, dkb, dkl, dkh = _heads(dk, "dk", T, B, L, D, dev)
-    inputs = (q_weight, k_weight, q_bias, k_bias)
-    used = [_vector(t, n, D, dev) for t, n in zip(inputs, ("q_weight", "k_weight", "q_bias",
-                                                           "k_bias"))]
-    wanted = sum(t is not None for t in inputs)
-    params, p = [None] * 4, [None] * 4
-    ws = wsp = None
-    n = 0
-    if wanted:
-        rows = iter(torch.empty((wanted, D), dtype=torch.float32, device=dev).unbind(0))
-        params = [None if t is None else next(rows) for t in inputs]
-        p = [None if t is None else t.data_ptr() for t in params]
-        ws, wsp, n = _workspace(lib.ag_qk_norm_rope_bwd_workspace, dev,
-                                "ag_qk_norm_rope_bwd_workspace", B, Hq, Hk, L, D, 1)
-    st = lib.ag_qk_norm_rope_bwd(
-        gq, gk, gt, qp, qb, ql, qh, kp, kb, kl, kh, DTYPES[T], used[0], used[1],
-        _code(NORMS, norm, "norm"), eps, *_rotation(inv_freq, rope, positions, B, L, dev), B, Hq,
-        Hk, L, D, dqp, dqb, dql, dqh, dkp, dkb, dkl, dkh, p[0], p[2], p[1], p[3], wsp, n,
-        _current(dev))
-    if st != AG_OK:
-        raise AgError("ag_qk_norm_rope_bwd", st)
-    return dq, dk, params[0], params[1], params[2], params[3]
+    return _layers.qk_bwd(q, k, q_weight, k_weight, q_bias, k_bias, _code(NORMS, norm, "norm"),
+                          eps, inv_freq, _code(ROPES, rope, "rope"), positions, dq_out, dk_out,
+                          dq, dk)
 
 
-def _is_dense(t: torch.Tensor) -> bool:
-    """Whether the elements fill one block of memory, in any dimension order."""
-    if t.is_contiguous():
-        return True
-    want = 1
-    for stride, size in sorted((s, n) for s, n in zip(t.stride(), t.shape) if n > 1):
-        if stride != want:
-            return False
-        want *= size
-    return True
+_is_dense = _layers.is_dense
 
 
 def ag_grad_clip(grads, max_norm: float, eps: float = 1e-6,
@@ -797,46 +530,17 @@ def ag_grad_clip(grads, max_norm: float, eps: float = 1e-6,
     """The global 2-norm of the gradients and their scaling in place by
     min(1, max_norm / (norm + eps)) (libag kernels).
 
-    grads: a sequence of dense fp32, bf16 or fp16 tensors on one device, none
-    overlapping another (None entries are skipped).  max_norm = math.inf only
-    measures.  Returns the norm before scaling, an fp32 scalar tensor on the
-    device (`norm` if given); nothing waits for it."""
-    grads = [g for g in grads if g is not None]
-    if not grads:
-        raise ValueError("grads has no tensor")
-    _on_gpu(grads[0], "every gradient", DTYPES)
-    dev = grads[0].device
-    if _elsewhere(dev, stream):
-        with _site(dev, stream):
+    grads: a sequence of fp32, bf16 or fp16 tensors on one device, each dense
+    in memory in some order of its dimensions, none overlapping another (None
+    entries are skipped).  max_norm = math.inf only measures.  Returns the
+    norm before scaling, an fp32 scalar tensor on the device (`norm` if
+    given); nothing waits for it."""
+    if not isinstance(grads, (list, tuple)):
+        grads = list(grads)
+    if stream is not None:
+        with _site(next((g for g in grads if g is not None), None), stream):
             return ag_grad_clip(grads, max_norm, eps, norm)
-    n, index = len(grads), dev.index
-    try:
-        types = [DTYPES[g.dtype] for g in grads]
-        well = all([g.get_device() == index and g.is_contiguous() for g in grads])
-    except (AttributeError, KeyError, RuntimeError):
-        well = False
-    if not well:
-        for g in grads:
-            _on_gpu(g, "every gradient", DTYPES)
-            _same_device(g, "one", dev)
-            if g.layout != torch.strided or not _is_dense(g):
-                raise ValueError("every gradient must be dense")
-    ptrs = (ctypes.c_void_p * n)(*[g.data_ptr() for g in grads])
-    counts = (ctypes.c_int64 * n)(*[g.numel() for g in grads])
-    codes = (ctypes.c_int * n)(*types)
-    if norm is None:
-        norm = torch.empty((), dtype=torch.float32, device=dev)
-    else:
-        _on_gpu(norm, "norm", (torch.float32,))
-        _same_device(norm, "norm", dev)
-        if norm.numel() != 1:
-            raise ValueError("norm must have one element")
-    ws, wsp, size = _workspace(lib.ag_grad_clip_workspace, dev, "ag_grad_clip_workspace", n)
-    st = lib.ag_grad_clip(ptrs, counts, codes, n, max_norm, eps, norm.data_ptr(), wsp, size,
-                          _current(dev))
-    if st != AG_OK:
-        raise AgError("ag_grad_clip", st)
-    return norm
+    return _layers.grad_clip(grads, max_norm, eps, norm)
 
 
 def ag_device_error(device: int = 0, clear: bool = True) -> int:
