@@ -628,8 +628,9 @@ bool encode_map(const Gemm &g, CUtensorMap *m, const void *at, int size, int64_t
                 int64_t cols, int64_t ld, int box_rows, int box_cols) {
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
                               static_cast<cuuint64_t>(parts)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * size,
-                                 static_cast<cuuint64_t>(ld) * size * rows};
+  // (With one part the outer stride is never used, but has to be a valid one.)
+  const cuuint64_t row = static_cast<cuuint64_t>(ld) * size;
+  const cuuint64_t strides[2] = {row, parts > 1 ? row * rows : row};
   const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows), 1};
   const cuuint32_t step[3] = {1, 1, 1};
   return g.encode(m,

@@ -536,6 +536,42 @@ __global__ void __launch_bounds__(kThreads, 2) qk_bwd_rows_kernel(const QkArgs a
 
 // --------------------------------------------------------------------------
 // General kernels.  One warp per (position, head) row, any D and any strides.
+// Row t of a block's positions from p0 on: all heads of each position in turn.
+struct Row {
+  int which, h, p;
+  int64_t b, l;
+};
+__device__ __forceinline__ Row row_of(const QkArgs &a, int64_t p0, int t, int heads) {
+  Row w;
+  w.p = t / heads;
+  w.h = t - w.p * heads;
+  w.which = w.h >= a.side[0].H;
+  if (w.which) w.h -= a.side[0].H;
+  w.b = (p0 + w.p) / a.L;
+  w.l = (p0 + w.p) - w.b * a.L;
+  return w;
+}
+// A row into shared memory, four loads of a lane at a time on their way.
+__device__ __forceinline__ void load_row_to(float *row, const void *x, int64_t at, int D, int dtype,
+                                            int lane) {
+  for (int i = lane; i < D; i += 128) {
+    float v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) v[u] = i + 32 * u < D ? load_one(x, at + i + 32 * u, dtype) : 0.f;
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (i + 32 * u < D) row[i + 32 * u] = v[u];
+  }
+}
+// The angles of np positions, by the whole block.
+__device__ __forceinline__ void block_angles(const QkArgs &a, float2 *cs, int64_t p0, int np,
+                                             int half) {
+  for (int i = threadIdx.x; i < np * half; i += blockDim.x) {
+    const int64_t b = (p0 + i / half) / a.L, l = (p0 + i / half) % a.L;
+    cs[i] = turn(a.positions ? a.positions[b * a.pos_sb + l] : l, a.inv_freq[i % half]);
+  }
+}
+
 __global__ void __launch_bounds__(kThreads) qk_fwd_kernel(const QkArgs a, int at_once) {
   extern __shared__ float smem[];
   begin_after_previous();
@@ -544,19 +580,19 @@ __global__ void __launch_bounds__(kThreads) qk_fwd_kernel(const QkArgs a, int at
   float *row = smem + 2 * at_once * half + warp * a.D;
   const int64_t p0 = static_cast<int64_t>(blockIdx.x) * at_once;
   const int np = static_cast<int>(min(static_cast<int64_t>(at_once), a.positions_total - p0));
-  for (int i = threadIdx.x; i < np * half; i += kThreads) {
-    const int64_t b = (p0 + i / half) / a.L, l = (p0 + i / half) % a.L;
-    cs[i] = turn(a.positions ? a.positions[b * a.pos_sb + l] : l, a.inv_freq[i % half]);
-  }
+  const int heads = a.side[0].H + a.side[1].H, rows = np * heads;
+  const auto load = [&](int t) {
+    const Row w = row_of(a, p0, t, heads);
+    const QkSide &s = a.side[w.which];
+    load_row_to(row, s.x, w.b * s.sb + w.l * s.sl + w.h * s.sh, a.D, a.x_dtype, lane);
+  };
+  if (warp < rows) load(warp);  // (on its way while the angles are formed)
+  block_angles(a, cs, p0, np, half);
   __syncthreads();
-  const int heads = a.side[0].H + a.side[1].H;
-  for (int t = warp; t < np * heads; t += kWarps) {
-    const int which = t % heads >= a.side[0].H;
-    const QkSide &s = a.side[which];
-    const int h = t % heads - (which ? a.side[0].H : 0), p = t / heads;
-    const int64_t b = (p0 + p) / a.L, l = (p0 + p) % a.L;
-    const int64_t at = b * s.sb + l * s.sl + h * s.sh;
-    for (int i = lane; i < a.D; i += 32) row[i] = load_one(s.x, at + i, a.x_dtype);
+  for (int t = warp; t < rows; t += kWarps) {
+    if (t != warp) load(t);
+    const Row w = row_of(a, p0, t, heads);
+    const QkSide &s = a.side[w.which];
     float mean, r;
     row_stats(row, a.D, a.norm, a.eps, lane, mean, r);
     for (int i = lane; i < a.D; i += 32) {
@@ -566,12 +602,12 @@ __global__ void __launch_bounds__(kThreads) qk_fwd_kernel(const QkArgs a, int at
       row[i] = v;
     }
     __syncwarp();
-    const int64_t to = ((b * s.H + h) * a.L + l) * a.D;
+    const int64_t to = ((w.b * s.H + w.h) * a.L + w.l) * a.D;
     for (int i = lane; i < a.D; i += 32) {
       float v = row[i];
       if (i < a.R) {
         const Pair q = pair_of(i, a.R, a.rope);
-        const float2 c = cs[p * half + q.angle];
+        const float2 c = cs[w.p * half + q.angle];
         v = fmaf(v, c.x, q.second ? row[q.other] * c.y : -row[q.other] * c.y);
       }
       store_one(s.out, to + i, a.o_dtype, v);
@@ -597,23 +633,21 @@ __global__ void __launch_bounds__(kThreads) qk_bwd_kernel(const QkArgs a, int wa
   for (int64_t p0 = static_cast<int64_t>(blockIdx.x) * at_once; p0 < a.positions_total;
        p0 += static_cast<int64_t>(gridDim.x) * at_once) {
     const int np = static_cast<int>(min(static_cast<int64_t>(at_once), a.positions_total - p0));
+    const int rows = np * heads;
+    const auto load = [&](int t) {
+      const Row w = row_of(a, p0, t, heads);
+      const QkSide &s = a.side[w.which];
+      load_row_to(row, s.x, w.b * s.sb + w.l * s.sl + w.h * s.sh, D, a.x_dtype, lane);
+      load_row_to(grad, s.g, ((w.b * s.H + w.h) * a.L + w.l) * D, D, a.o_dtype, lane);
+    };
+    if (warp < rows) load(warp);  // (on its way while the angles are formed)
+    __syncthreads();              // the angles of the turn before are no longer read
+    block_angles(a, cs, p0, np, half);
     __syncthreads();
-    for (int i = threadIdx.x; i < np * half; i += blockDim.x) {
-      const int64_t b = (p0 + i / half) / a.L, l = (p0 + i / half) % a.L;
-      cs[i] = turn(a.positions ? a.positions[b * a.pos_sb + l] : l, a.inv_freq[i % half]);
-    }
-    __syncthreads();
-    for (int t = warp; t < np * heads; t += warps) {
-      const int which = t % heads >= a.side[0].H;
-      const QkSide &s = a.side[which];
-      const int h = t % heads - (which ? a.side[0].H : 0), p = t / heads;
-      const int64_t b = (p0 + p) / a.L, l = (p0 + p) % a.L;
-      const int64_t at = b * s.sb + l * s.sl + h * s.sh;
-      const int64_t from = ((b * s.H + h) * a.L + l) * D;
-      for (int i = lane; i < D; i += 32) {
-        row[i] = load_one(s.x, at + i, a.x_dtype);
-        grad[i] = load_one(s.g, from + i, a.o_dtype);
-      }
+    for (int t = warp; t < rows; t += warps) {
+      if (t != warp) load(t);
+      const Row w = row_of(a, p0, t, heads);
+      const QkSide &s = a.side[w.which];
       float mean, r;
       row_stats(row, D, a.norm, a.eps, lane, mean, r);
       __syncwarp();
@@ -622,24 +656,24 @@ __global__ void __launch_bounds__(kThreads) qk_bwd_kernel(const QkArgs a, int wa
         float g = grad[i];
         if (i < a.R) {
           const Pair q = pair_of(i, a.R, a.rope);
-          const float2 c = cs[p * half + q.angle];
+          const float2 c = cs[w.p * half + q.angle];
           g = fmaf(g, c.x, q.second ? -grad[q.other] * c.y : grad[q.other] * c.y);
         }
         const float n = (row[i] - mean) * r;
-        own[which * 2 * D + i] += g * n;
-        own[which * 2 * D + D + i] += g;
+        own[w.which * 2 * D + i] += g * n;
+        own[w.which * 2 * D + D + i] += g;
         const float d = s.w ? g * s.w[i] : g;
         along = fmaf(d, n, along);
         total += d;
       }
       along = a.norm == AG_NORM_NONE ? 0.f : warp_sum(along) / D;
       total = a.norm == AG_NORM_LAYER ? warp_sum(total) / D : 0.f;
-      const int64_t to = b * s.dxb + l * s.dxl + h * s.dxh;
+      const int64_t to = w.b * s.dxb + w.l * s.dxl + w.h * s.dxh;
       for (int i = lane; i < D; i += 32) {
         float g = grad[i];
         if (i < a.R) {
           const Pair q = pair_of(i, a.R, a.rope);
-          const float2 c = cs[p * half + q.angle];
+          const float2 c = cs[w.p * half + q.angle];
           g = fmaf(g, c.x, q.second ? -grad[q.other] * c.y : grad[q.other] * c.y);
         }
         const float n = (row[i] - mean) * r, d = s.w ? g * s.w[i] : g;

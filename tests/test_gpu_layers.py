@@ -159,6 +159,31 @@ def test_linear_fwd_rows_apart(ag, M, N, K, pad):
     _linear_case(ag, M, N, K, pad=pad, out=F32)
 
 
+@pytest.mark.parametrize("M,N,K", [(70001, 16, 24), (64, 24, 40000), (9, 4104, 8), (8, 3001, 17),
+                                   (6, 40, 20001)])
+def test_linear_long_sides(ag, M, N, K):
+    """Many rows, long sums (split over clusters), and few rows beside wide ones."""
+    _linear_case(ag, M, N, K, out=F32, preact=False)
+    if M > 8:
+        _linear_bwd_case(ag, M, N, K)
+
+
+def test_linear_fwd_columns_of_one_buffer(ag):
+    """x and y as column ranges of the same wider buffer; its other columns stay."""
+    for M in (3, 500):
+        g = _gen(M)
+        buf = _randn(g, M, 64 + 96 + 40, dtype=BF16)
+        keep = buf.clone()
+        W = _randn(g, 96, 64, dtype=BF16)
+        want = ag.ag_linear_fwd(buf[:, :64].contiguous(), W)
+        ag.ag_linear_fwd(buf[:, :64], W, out=buf[:, 64:160])
+        _ok(ag)
+        assert torch.equal(buf[:, 64:160], want)
+        assert torch.equal(buf[:, :64], keep[:, :64]) and torch.equal(buf[:, 160:], keep[:, 160:])
+        with pytest.raises(ag.AgError, match="ALIAS"):
+            ag.ag_linear_fwd(buf[:, :64], W, out=buf[:, 63:159])
+
+
 def test_linear_fwd_starts_off_alignment(ag):
     """Inputs and outputs that start 2 bytes past a 16-byte boundary."""
     g = _gen(5)
@@ -456,6 +481,44 @@ def test_qk_positions(ag, positions, rope):
 
 def test_qk_long(ag):
     _qk_case(ag, 2, 4111, 8, 1, 128, 128, norm="layer")
+    _qk_case(ag, 1, 5003, 1, 1, 40, 12, norm="rms", rope="interleaved")
+
+
+@pytest.mark.parametrize("Hq,Hk,D,R", [(70, 3, 128, 64), (1, 9, 64, 64), (0, 5, 128, 128),
+                                       (33, 0, 100, 10), (4, 4, 8, 8), (5, 2, 16, 0)])
+def test_qk_many_heads(ag, Hq, Hk, D, R):
+    g = _gen(Hq + D)
+    B, L = 2, 19
+    q = _randn(g, B, L, Hq, D, dtype=BF16) if Hq else None
+    k = _randn(g, B, L, Hk, D, dtype=BF16) if Hk else None
+    w = 1 + 0.3 * _randn(g, D)
+    freq = ag.ag_rope_frequencies(R) if R else None
+    pos = torch.randint(0, 1 << 20, (B, L), generator=g).cuda()
+    sides = [t for t in (q, k) if t is not None]
+    grads = [_randn(g, B, t.shape[2], L, D) if t is not None else None for t in (q, k)]
+    kw = dict(q_weight=None if q is None else w, k_weight=None if k is None else w, norm="rms",
+              inv_freq=freq, positions=pos)
+    outs = [o for o in ag.ag_qk_norm_rope_fwd(q, k, out_dtype=F32, **kw) if o is not None]
+    got = ag.ag_qk_norm_rope_bwd(*grads, q, k, **kw)
+    _ok(ag)
+    for x, o, go, dx, dw in zip(sides, outs, [t for t in grads if t is not None],
+                                [t for t in got[:2] if t is not None],
+                                [t for t in got[2:4] if t is not None]):
+        want = ref.qk(x.double(), w.double(), None, "rms", 1e-6, freq, "halves", pos)
+        scale = _row_scale(x.double(), w.double(), None, "rms", 1e-6).transpose(1, 2)
+        _close("out", o, want, 2.0 ** -17 * scale + _half_step(F32, want))
+        wdx, wdw, _ = ref.qk_grads(go.double(), x.double(), w.double(), None, "rms", 1e-6, freq,
+                                   "halves", pos)
+        n = ref.norm(x.double(), "rms", 1e-6)
+        r = 1 / torch.sqrt(x.double().square().mean(-1, keepdim=True) + 1e-6)
+        top = 2 * go.double().transpose(1, 2).abs().amax(-1, keepdim=True) * w.double().abs().max()
+        big = n.abs().amax(-1, keepdim=True)
+        _close("dx", dx, wdx, 2.0 ** -17 * r * top * (2 + big * big) * (1 + 2.0 ** -7)
+               + _half_step(BF16, wdx))
+        terms = B * L * x.shape[2]
+        turned = ref.rotate(go.double().transpose(1, 2), pos, freq, "halves", -1.0)
+        _close("dw", dw, wdw, (turned.abs() * n.abs()).sum((0, 1, 2)) * terms * 2.0 ** -24
+               + (top * big).sum((0, 1, 2)).max() * 2.0 ** -17)
 
 
 def test_qk_zero_rows_and_eps(ag):
@@ -639,6 +702,18 @@ def test_clip_of_zeros_and_nothing(ag):
     assert float(n) == 0.0 and not bool(z.any())
     e = torch.zeros(0, device="cuda")
     assert float(ag.ag_grad_clip([e], 1.0)) == 0.0
+
+
+def test_clip_of_no_tensor_through_the_c_abi(ag):
+    import ctypes
+    n, size = torch.full((1,), 5.0, device="cuda"), ctypes.c_int64(0)
+    assert ag.lib.ag_grad_clip_workspace(0, ctypes.byref(size)) == 0
+    ws = torch.zeros(size.value, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    assert ag.lib.ag_grad_clip(None, None, None, 0, 1.0, 0.0, n.data_ptr(), ws.data_ptr(),
+                               size.value, torch.cuda.current_stream().cuda_stream) == 0
+    torch.cuda.synchronize()
+    assert float(n) == 0.0
 
 
 def test_clip_refuses_overlaps(ag):
