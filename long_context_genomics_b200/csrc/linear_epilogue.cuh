@@ -81,7 +81,7 @@ __device__ __forceinline__ float2 act_slope2(float2 z) {
   if constexpr (ACT == AG_ACT_GELU_TANH) {
     const float2 p = logistic2(tanh_argument(z));
     const float2 r = __ffma2_rn(make_float2(-p.x, -p.y), p, p);  // p (1 - p)
-    const float2 k = __ffma2_rn(__fmul2_rn(both(0.21406850f), z), z, both(1.5957691f));
+    const float2 k = __ffma2_rn(__fmul2_rn(both(0.21406445f), z), z, both(1.5957691f));
     return __ffma2_rn(__fmul2_rn(z, r), k, p);
   }
   if constexpr (ACT == AG_ACT_SILU) {
@@ -91,26 +91,25 @@ __device__ __forceinline__ float2 act_slope2(float2 z) {
   }
   return both(1.f);
 }
-template <int ACT>
-__device__ __forceinline__ float act_value(float z) { return act_value2<ACT>(both(z)).x; }
-template <int ACT>
-__device__ __forceinline__ float act_slope(float z) { return act_slope2<ACT>(both(z)).x; }
-__device__ __forceinline__ float act_value(float z, int act) {
-  switch (act) {
-    case AG_ACT_RELU: return act_value<AG_ACT_RELU>(z);
-    case AG_ACT_GELU: return act_value<AG_ACT_GELU>(z);
-    case AG_ACT_GELU_TANH: return act_value<AG_ACT_GELU_TANH>(z);
-    case AG_ACT_SILU: return act_value<AG_ACT_SILU>(z);
-    default: return z;
+// V values in place; the activation looked up once for all of them.
+template <int ACT, bool SLOPE, int V>
+__device__ __forceinline__ void act_all(float (&v)[V]) {
+#pragma unroll
+  for (int i = 0; i < V; i += 2) {
+    const float2 z = make_float2(v[i], i + 1 < V ? v[i + 1] : 0.f);
+    const float2 y = SLOPE ? act_slope2<ACT>(z) : act_value2<ACT>(z);
+    v[i] = y.x;
+    if (i + 1 < V) v[i + 1] = y.y;
   }
 }
-__device__ __forceinline__ float act_slope(float z, int act) {
+template <bool SLOPE, int V>
+__device__ __forceinline__ void act_all(float (&v)[V], int act) {
   switch (act) {
-    case AG_ACT_RELU: return act_slope<AG_ACT_RELU>(z);
-    case AG_ACT_GELU: return act_slope<AG_ACT_GELU>(z);
-    case AG_ACT_GELU_TANH: return act_slope<AG_ACT_GELU_TANH>(z);
-    case AG_ACT_SILU: return act_slope<AG_ACT_SILU>(z);
-    default: return 1.f;
+    case AG_ACT_RELU: return act_all<AG_ACT_RELU, SLOPE>(v);
+    case AG_ACT_GELU: return act_all<AG_ACT_GELU, SLOPE>(v);
+    case AG_ACT_GELU_TANH: return act_all<AG_ACT_GELU_TANH, SLOPE>(v);
+    case AG_ACT_SILU: return act_all<AG_ACT_SILU, SLOPE>(v);
+    default: return act_all<AG_ACT_NONE, SLOPE>(v);
   }
 }
 
@@ -194,11 +193,11 @@ __device__ __forceinline__ void linear_finish(const LinearEpilogue &e, float (&v
   if (e.pre_in) {
     float z[V];
     load_values<V>(e.pre_in, row * e.ld_pre_in + col, e.dtype, z);
+    act_all<true>(z, e.act);
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] *= act_slope(z[i], e.act);
+    for (int i = 0; i < V; ++i) v[i] *= z[i];
   } else if (e.act != AG_ACT_NONE) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = act_value(v[i], e.act);
+    act_all<false>(v, e.act);
   }
   if (e.residual) {
     float r[V];

@@ -407,28 +407,30 @@ __device__ __forceinline__ void finish_column(const LinearEpilogue &e, const flo
   for (int i = 0; i < 8; ++i)
     v[i] = stage[(r + i) * 32 + (((lane >> 2) ^ ((r + i) & 7)) << 2) + (lane & 3)];
   const auto load = [&](const void *p, int64_t ld, int dtype) {
+    int64_t at = row * ld + col;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 8; ++i, at += ld) {
       float one[1] = {0.f};
-      if (i < n) load_values<1>(p, (row + i) * ld + col, dtype, one);
+      if (i < n) load_values<1>(p, at, dtype, one);
       x[i] = one[0];
     }
   };
   const auto store = [&](void *p, int64_t ld, int dtype) {
+    int64_t at = row * ld + col;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 8; ++i, at += ld) {
       const float one[1] = {v[i]};
-      if (i < n) store_values<1>(p, (row + i) * ld + col, dtype, one);
+      if (i < n) store_values<1>(p, at, dtype, one);
     }
   };
   if (e.pre_out) store(e.pre_out, e.ld_pre_out, e.dtype);
   if (e.pre_in) {
     load(e.pre_in, e.ld_pre_in, e.dtype);
+    act_all<true>(x, e.act);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] *= act_slope(x[i], e.act);
+    for (int i = 0; i < 8; ++i) v[i] *= x[i];
   } else if (e.act != AG_ACT_NONE) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = act_value(v[i], e.act);
+    act_all<false>(v, e.act);
   }
   if (e.residual) {
     load(e.residual, e.ld_res, e.out_dtype);

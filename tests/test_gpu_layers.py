@@ -227,6 +227,24 @@ def test_linear_fwd_non_finite_values_stay_in_their_rows_and_columns(ag):
         assert not bool(fine[M - 1].any()) and not bool(fine[:, N - 1].any())
 
 
+@pytest.mark.parametrize("act", ["relu", "gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("M", [4, 512])
+def test_activations_and_slopes_closely(ag, act, M):
+    """Identity weights and fp32 outputs leave the activation and its derivative
+    alone: values of order one, formed in a few fp32 operations each off by half
+    a unit of 2^-23 and two special-function results of one unit: 2-norms agree
+    to 2^-22."""
+    x = _randn(_gen(3), M, 128, dtype=BF16)
+    eye = torch.eye(128, device="cuda").to(BF16)
+    y = ag.ag_linear_fwd(x, eye, act=act, out_dtype=F32)
+    one = torch.ones(M, 128, dtype=BF16, device="cuda")
+    dx, _, _ = ag.ag_linear_bwd(one, x, eye, act=act, preact=x, need_dW=False, need_db=False,
+                                dx_dtype=F32)
+    _ok(ag)
+    for got, want in ((y, ref.act(x.double(), act)), (dx, ref.act_slope(x.double(), act))):
+        assert float((got.double() - want).norm()) <= 2.0 ** -22 * float(want.norm())
+
+
 def test_linear_fwd_accumulates_in_32_bits(ag):
     """A long sum of equal terms beside one large term: 16-bit partial sums, or
     a truncating accumulator over the whole length, would lose it."""
