@@ -66,7 +66,9 @@ __global__ void __launch_bounds__(256)
   linear_finish<V>(e, v, bias, row, col);
 }
 
-// Copies of 16-bit matrices with rows that TMA can read, all in one launch.
+// Copies of 16-bit matrices with rows that TMA can read, all in one launch.  A
+// thread takes 8 columns: single loads, all on their way at once, and one
+// 16-byte store (the copy's rows are padded to 8 columns, with zeros).
 struct Copies {
   struct One {
     const uint16_t *from;
@@ -78,9 +80,17 @@ struct Copies {
 __global__ void __launch_bounds__(256) pack_rows_kernel(const Copies c) {
   begin_after_previous();
   const Copies::One m = c.m[blockIdx.y];
-  for (int64_t r = blockIdx.x; r < m.rows; r += gridDim.x)
-    for (int64_t k = threadIdx.x; k < m.cols; k += 256)
-      m.to[r * m.ld_to + k] = m.from[r * m.ld_from + k];
+  const int64_t per_row = m.ld_to / 8, groups = m.rows * per_row;
+  for (int64_t g = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; g < groups;
+       g += static_cast<int64_t>(gridDim.x) * 256) {
+    const int64_t r = g / per_row, k = (g - r * per_row) * 8;
+    const uint16_t *from = m.from + r * m.ld_from + k;
+    uint32_t v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = k + i < m.cols ? from[i] : 0;
+    *reinterpret_cast<uint4 *>(m.to + r * m.ld_to + k) =
+        make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+  }
 }
 
 // db[n] = sum_m dy[m, n].  A block takes 32 V columns and a part of the rows:
@@ -259,9 +269,12 @@ void note(Copies &c, const Packed &k, const void *p, int64_t ld) {
 }
 cudaError_t make(const Copies &c, int num_sms, cudaStream_t s) {
   if (c.n == 0) return cudaSuccess;
-  int64_t rows = 0;
-  for (int i = 0; i < c.n; ++i) rows = c.m[i].rows > rows ? c.m[i].rows : rows;
-  const int64_t blocks = rows < 16 * num_sms ? rows : 16 * num_sms;
+  int64_t blocks = 0;
+  for (int i = 0; i < c.n; ++i) {
+    const int64_t b = (c.m[i].rows * (c.m[i].ld_to / 8) + 255) / 256;
+    blocks = b > blocks ? b : blocks;
+  }
+  if (blocks > 16 * num_sms) blocks = 16 * num_sms;
   return launch_after_previous(pack_rows_kernel, dim3(static_cast<unsigned>(blocks), c.n), 256, 0, s,
                                c);
 }
