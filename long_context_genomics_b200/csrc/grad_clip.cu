@@ -7,7 +7,13 @@
 // write.  The tensors are cut into chunks; a fixed grid of blocks takes them
 // in turn, so a partial sum belongs to a block and the order of every
 // addition is fixed.  Squares and sums are in 64 bits: a float32 square of a
-// large gradient overflows and of a small one vanishes.
+// large gradient overflows and of a small one vanishes; the conversions and the
+// 64-bit products keep up with memory.  Measured: 98 million float32 values in
+// 126 tensors 70 us for the norm alone (5.6 TB/s) and 223 us with the scaling
+// (5.3 TB/s over its three passes; 392 MB do not stay in L2 between them); 14
+// tensors of 98 thousand bf16 values 7.5 us, which is two launches (one cluster
+// of 8 blocks doing both in one launch took 7.4 us, and 10 us from 131 thousand
+// float32 values on, against 8.5).
 #include <cmath>
 
 #include "ag_internal.h"
@@ -20,7 +26,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kChunk = 16384;         // elements
 // Tensors per launch: the list travels as a kernel argument.  A list of 32
-// (0.7 KB) launches faster than one of 512 (10.8 KB); measured below.
+// (0.7 KB) takes the launching thread 5.9 us for the two kernels, one of 512
+// (10.8 KB) 13.9 us.
 constexpr int kFewTensors = 32, kMaxTensors = 512;
 constexpr int kBlocksPerSm = 4;
 
