@@ -473,7 +473,9 @@ typedef enum {
  * (Hq + Hk) <= 2^31 - 1, Hq and Hk <= 65536 and no dimension spanning more
  * than 2^50 elements (AG_ERR_UNSUPPORTED); B == 0 or L == 0 is a no-op.
  * Pointers aligned to their element.  Outputs may not overlap inputs or each
- * other (AG_ERR_ALIAS).  A row of zeros with eps == 0 has no norm (NaN).
+ * other (AG_ERR_ALIAS).  A row of zeros with eps == 0 has no norm (NaN), and
+ * a row whose sum of squares passes float32 (elements of about 1e18) gives
+ * zeros, as float32 arithmetic does.
  */
 ag_status ag_qk_norm_rope_fwd(const void *q, int64_t q_sb, int64_t q_sl, int64_t q_sh,
                               const void *k, int64_t k_sb, int64_t k_sl, int64_t k_sh,
@@ -539,7 +541,7 @@ ag_status ag_qk_norm_rope_bwd_workspace(int64_t B, int64_t Hq, int64_t Hk, int64
  *   most 2^42 and n at most 2^20 (AG_ERR_UNSUPPORTED); pointers aligned to
  *   their element.  No two tensors may overlap (the same tensor twice
  *   included), nor norm_out or the workspace a tensor (AG_ERR_ALIAS).
- *   n == 0 writes norm 0.
+ *   n == 0 writes norm 0.  A norm of 0 leaves the gradients as they are.
  * Bitwise reproducible.  The host arrays are not read again by a replay of a
  * captured graph, which uses the pointers of the capture.
  */

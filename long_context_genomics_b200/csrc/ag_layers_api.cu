@@ -494,7 +494,10 @@ ag_status ag_qk_norm_rope_bwd(const void *dq_out, const void *dk_out, int g_dtyp
   for (int i = 0; i < 4; ++i) outs[2 + i] = {params[i], params[i] ? row : 0};
   ag::DeviceInfo *dev = nullptr;
   st = ag::device_info(&dev);
-  const int64_t need = st == AG_OK && wants ? ag::qk_bwd_workspace(B * L, static_cast<int>(Hq), static_cast<int>(Hk), static_cast<int>(D), dev->num_sms) : 0;
+  int64_t need = 0;
+  if (st == AG_OK && wants)
+    need = ag::qk_bwd_workspace(B * L, static_cast<int>(Hq), static_cast<int>(Hk),
+                                static_cast<int>(D), dev->num_sms);
   outs[6] = {workspace, workspace ? static_cast<uint64_t>(need) : 0u};
   for (int o = 0; o < 7; ++o) {
     for (const Range &r : ins)
@@ -566,7 +569,8 @@ ag_status ag_grad_clip(void *const *grads, const int64_t *counts, const int *dty
   if (!r) return AG_ERR_SCRATCH;
   int64_t m = 0;
   r[m++] = {reinterpret_cast<uintptr_t>(norm_out), 4};
-  if (workspace && need) r[m++] = {reinterpret_cast<uintptr_t>(workspace), static_cast<uint64_t>(need)};
+  if (workspace && need)
+    r[m++] = {reinterpret_cast<uintptr_t>(workspace), static_cast<uint64_t>(need)};
   for (int64_t i = 0; i < n; ++i)
     if (counts[i])
       r[m++] = {reinterpret_cast<uintptr_t>(grads[i]),

@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(kThreads)
   begin_after_previous();
   const double norm = sqrt(total_of(partial, slots));
   if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = static_cast<float>(norm);
-  if (max_norm == INFINITY) return;
+  if (max_norm == INFINITY || norm == 0.0) return;  // (zeros stay zeros, also with eps == 0)
   const double ratio = static_cast<double>(max_norm) / (norm + static_cast<double>(eps));
   // Written so that a NaN stays a NaN.
   const float c = ratio >= 1.0 ? 1.f : static_cast<float>(ratio);
@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // Takes tensors [from, n) that are not empty into `list` up to its capacity;
-// returns the next index.  The entry point's limits (2^42 elements, 2^20
+// returns the index of the next one that is not empty.  The entry point's limits (2^42 elements, 2^20
 // tensors) keep the chunks of a launch below 2^29.
 template <int MOST>
 int64_t fill(TensorList<MOST> &list, void *const *grads, const int64_t *counts, const int *dtypes,
@@ -169,8 +169,9 @@ int64_t fill(TensorList<MOST> &list, void *const *grads, const int64_t *counts, 
   list.first[0] = 0;
   int64_t chunks = 0;
   int64_t i = from;
-  for (; i < n && list.n < MOST; ++i) {
+  for (; i < n; ++i) {
     if (counts[i] == 0) continue;
+    if (list.n == MOST) break;
     list.ptr[list.n] = grads[i];
     list.count[list.n] = counts[i];
     list.dtype[list.n] = static_cast<uint8_t>(dtypes[i]);
@@ -198,7 +199,7 @@ cudaError_t clip(void *const *grads, const int64_t *counts, const int *dtypes, i
   int slots = 0, launches = 0;
   for (int64_t i = 0; i < n;) {
     i = fill(list, grads, counts, dtypes, i, n);
-    if (list.n == 0) break;
+    if (list.n == 0) break;  // (nothing but empty tensors)
     const unsigned chunks = list.first[list.n];
     const int blocks = chunks < static_cast<unsigned>(most) ? static_cast<int>(chunks) : most;
     const cudaError_t e = launch_after_previous(square_sum_kernel<MOST>, blocks, kThreads, 0, stream,
@@ -221,7 +222,6 @@ cudaError_t clip(void *const *grads, const int64_t *counts, const int *dtypes, i
   do {
     if (launches != 1) i = fill(list, grads, counts, dtypes, i, n);
     else i = n;  // the list still holds them all
-    if (list.n == 0 && !first) break;
     const unsigned chunks = list.first[list.n];
     int blocks = chunks < static_cast<unsigned>(most) ? static_cast<int>(chunks) : most;
     if (blocks == 0 || std::isinf(max_norm)) blocks = 1;

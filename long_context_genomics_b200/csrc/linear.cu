@@ -287,8 +287,7 @@ cudaError_t run(Gemm &g) {
   cudaError_t e = launch_gemm(g);
   if (e != cudaSuccess || g.plan.splits == 1) return e;
   const int v = g.epi.vec8 ? 8 : 1;
-  const int64_t blocks = (g.M * ((g.N + v - 1) / v) + 255) / 256;
-  if (blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  const int64_t blocks = (g.M * ((g.N + v - 1) / v) + 255) / 256;  // at most 2^38 / 256
   return launch_after_previous(v == 8 ? linear_join_kernel<8> : linear_join_kernel<1>,
                                static_cast<unsigned>(blocks), 256, 0, g.stream, g.partial,
                                g.plan.splits, g.M, g.N, partial_ld(g.N), g.epi);

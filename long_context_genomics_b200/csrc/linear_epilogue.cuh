@@ -81,7 +81,11 @@ __device__ __forceinline__ float2 act_slope2(float2 z) {
   if constexpr (ACT == AG_ACT_GELU_TANH) {
     const float2 p = logistic2(tanh_argument(z));
     const float2 r = __ffma2_rn(make_float2(-p.x, -p.y), p, p);  // p (1 - p)
-    const float2 k = __ffma2_rn(__fmul2_rn(both(0.21406445f), z), z, both(1.5957691f));
+    // (z^2 stops at 2^100: beyond that r is zero, and zero times infinity is not.)
+    const float2 s = __fmul2_rn(z, z);
+    const float2 k = __ffma2_rn(both(0.21406445f),
+                                make_float2(fminf(s.x, 0x1p100f), fminf(s.y, 0x1p100f)),
+                                both(1.5957691f));
     return __ffma2_rn(__fmul2_rn(z, r), k, p);
   }
   if constexpr (ACT == AG_ACT_SILU) {

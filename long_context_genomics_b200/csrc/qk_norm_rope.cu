@@ -754,10 +754,15 @@ int64_t general_blocks(int64_t total, int heads, int num_sms) {
   return blocks_for(total, positions_at_once(heads), 6 * num_sms);
 }
 
+// The most that the general kernels take: angles of 8 positions of 1024 elements,
+// and six rows of 1024 for each of 4 warps (of 512 for 8).
+constexpr int kMostSmem = (8 * 1024 + 6 * 4 * 1024) * 4;
+// Always the same limit: a call's own would be taken back by a smaller call of
+// another thread before its launch.
 cudaError_t allow_smem(const void *kernel, size_t bytes) {
   return bytes <= 48 * 1024 ? cudaSuccess
                             : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   static_cast<int>(bytes));
+                                                   kMostSmem);
 }
 
 }  // namespace

@@ -245,6 +245,25 @@ def test_activations_and_slopes_closely(ag, act, M):
         assert float((got.double() - want).norm()) <= 2.0 ** -22 * float(want.norm())
 
 
+@pytest.mark.parametrize("act", ["relu", "gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("M,K", [(8, 8), (256, 64), (256, 61)])
+def test_activations_and_slopes_of_large_values(ag, act, M, K):
+    """Far from zero every activation is z or 0 and its slope 1 or 0, up to the
+    largest numbers, whose squares and cubes are none any more."""
+    z = torch.tensor([100.0, 1e4, 1e10, 1e13, 1e19, 1e25, 1e38, 3e38], device="cuda")
+    z = torch.cat([z, -z]).repeat((M * K + 15) // 16)[:M * K].view(M, K).to(BF16)
+    eye = torch.eye(K, device="cuda").to(BF16)
+    y = ag.ag_linear_fwd(z, eye, act=act, out_dtype=F32)
+    one = torch.ones(M, K, dtype=BF16, device="cuda")
+    dx, _, _ = ag.ag_linear_bwd(one, z, eye, act=act, preact=z, need_dW=False, need_db=False,
+                                dx_dtype=F32)
+    _ok(ag)
+    # (silu(-100) is -3.7e-42, and its slope as near to zero.)
+    zero = torch.where(z > 0, 0.0, 1e-40)
+    assert bool(((y - z.float().clamp(min=0)).abs() <= zero).all())
+    assert bool(((dx - (z > 0).float()).abs() <= zero).all())
+
+
 def test_linear_fwd_accumulates_in_32_bits(ag):
     """A long sum of equal terms beside one large term: 16-bit partial sums, or
     a truncating accumulator over the whole length, would lose it."""
@@ -682,6 +701,17 @@ def test_clip_many_tensors(ag, n):
     _clip_check(ag, [flat[i, :1 + i % 64] for i in range(n)], math.inf)
 
 
+@pytest.mark.parametrize("full", [31, 32, 33, 511, 512, 513])
+def test_clip_many_empty_tensors(ag, full):
+    """Empty tensors take no place among those of a launch, wherever they are."""
+    flat = _randn(_gen(full), full, 3)
+    empty = torch.zeros(0, device="cuda")
+    some = list(flat)
+    _clip_check(ag, some + [empty] * 600, 0.25)
+    _clip_check(ag, [empty] * 600 + some, 0.125)
+    _clip_check(ag, [t for s in some for t in (s, empty)], 0.0625)
+
+
 def test_clip_large(ag):
     g = torch.Generator(device="cuda").manual_seed(3)
     grads = [torch.randn(n, generator=g, device="cuda") for n in (30_000_001, 5, 12_345_678)]
@@ -718,6 +748,7 @@ def test_clip_of_zeros_and_nothing(ag):
     assert ag.ag_grad_clip([z, None], 1.0, norm=n) is n
     torch.cuda.synchronize()
     assert float(n) == 0.0 and not bool(z.any())
+    assert float(ag.ag_grad_clip([z], 0.0, eps=0.0)) == 0.0 and not bool(z.any())
     e = torch.zeros(0, device="cuda")
     assert float(ag.ag_grad_clip([e], 1.0)) == 0.0
 
@@ -890,6 +921,48 @@ def test_block_on_other_streams_and_in_graphs(ag):
         for out, w in zip(outs, want):
             assert all(torch.equal(x, y) for x, y in zip(out, w))
     assert ag.ag_device_error(0) == 0
+
+
+def test_calls_of_several_threads(ag):
+    """Calls with little and with much shared memory, few and many tensors and
+    several products, made by four threads at once on streams of their own."""
+    import threading
+    g = _gen(11)
+    cases = []
+    for D in (1000, 999, 331, 77):
+        q, k = _randn(g, 2, 5, 2, D), _randn(g, 2, 5, D)
+        w = _randn(g, D)
+        x, W = _randn(g, 40 + D, 72, dtype=BF16), _randn(g, D, 72, dtype=BF16)
+        cases.append((q, k, w, x, W))
+
+    def once(q, k, w, x, W):
+        kw = dict(q_weight=w, k_weight=w, norm="layer")
+        fwd = ag.ag_qk_norm_rope_fwd(q, k, out_dtype=F32, **kw)
+        bwd = ag.ag_qk_norm_rope_bwd(*fwd, q, k, **kw)
+        y = ag.ag_linear_fwd(x, W, act="gelu")
+        return [*fwd, *(t for t in bwd if t is not None), y, *ag.ag_linear_bwd(y, x, W)]
+
+    want = [once(*c) for c in cases]
+    _ok(ag)
+    failed = []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(40):
+                    got = once(*cases[i])
+                torch.cuda.current_stream().synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(got, want[i]))
+        except BaseException as e:  # noqa: BLE001  (reported by the test's own thread)
+            failed.append((i, repr(e)))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(cases))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    _ok(ag)
+    assert not failed, failed
 
 
 def test_stream_argument(ag):
