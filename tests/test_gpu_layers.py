@@ -1039,3 +1039,67 @@ def test_refusals_on_the_gpu(ag):
     assert ag.lib.ag_grad_clip(*args, n.value - 1, None) == 9
     torch.cuda.synchronize()
     assert bool((t == 1).all()) and int(need) == 0
+
+
+# ---------------------------------------------------------------------------
+# Offsets past 32 bits (8 to 26 GB on the device)
+@pytest.mark.parametrize("ld", [2 ** 28, 2 ** 28 - 1])
+def test_linear_rows_far_apart(ag, ld):
+    """Inputs, outputs and gradients in columns of one buffer whose last rows
+    start past element 2^32, with rows that TMA can and cannot address."""
+    M, N, K = 18, 40, 64
+    buf = torch.empty(17 * ld + 512, dtype=BF16, device="cuda")
+    x, y, dy, dx = (torch.as_strided(buf, (M, n), (ld, 1), at)
+                    for n, at in ((K, 0), (N, 64), (N, 128), (K, 192)))
+    g = _gen(ld % 1000)
+    x.copy_(_randn(g, M, K, dtype=BF16))
+    dy.copy_(_randn(g, M, N, dtype=BF16))
+    W = _randn(g, N, K, dtype=BF16, scale=1 / 8)
+    ag.ag_linear_fwd(x, W, out=y)
+    _, dW, db = ag.ag_linear_bwd(dy, x, W, dx=dx)
+    _ok(ag)
+    xd, Wd, dyd = x.double(), W.double(), dy.double()
+    for name, got, want, mass, n in (("y", y, xd @ Wd.T, xd.abs() @ Wd.abs().T, K),
+                                     ("dx", dx, dyd @ Wd, dyd.abs() @ Wd.abs(), N),
+                                     ("dW", dW, dyd.T @ xd, dyd.abs().T @ xd.abs(), M),
+                                     ("db", db, dyd.sum(0), dyd.abs().sum(0), M)):
+        _close(name, got, want, (n + 8) * 2.0 ** -23 * mass * 1.01 + _half_step(got.dtype, want))
+
+
+@pytest.mark.parametrize("D", [8, 7])
+def test_qk_more_elements_than_32_bits(ag, D):
+    """2^32 elements of one head, of one row at every position; the rotation
+    tells the positions apart."""
+    L = 2 ** 32 // D + 5
+    g = _gen(D)
+    row = _randn(g, D, dtype=BF16)
+    q = row.expand(1, L, 1, D)
+    freq = ag.ag_rope_frequencies(D // 2 * 2)
+    out, _ = ag.ag_qk_norm_rope_fwd(q, None, inv_freq=freq, norm="none")
+    _ok(ag)
+    n = min(1000, L)
+    last = torch.arange(L - n, L, device="cuda")
+    for at in (torch.arange(n, device="cuda"), last):
+        want = ref.qk(row.double().expand(1, n, 1, D), None, None, "none", 0.0, freq, "halves",
+                      at[None])[0, 0]
+        mass = row.double().abs().sum()
+        _close("q", out[0, 0, at], want, mass * 2.0 ** -19 + _half_step(BF16, want))
+    w = torch.ones(D, device="cuda")
+    dq, _, _, _, dbias, _ = ag.ag_qk_norm_rope_bwd(out, None, q, None, q_bias=w, inv_freq=freq,
+                                                   norm="none")
+    _ok(ag)
+    want = row.double().expand(n, D)  # turned there and back
+    _close("dq", dq[0, last, 0], want, row.double().abs().sum() * (2.0 ** -18 + 2.0 ** -7)
+           + _half_step(BF16, want))
+
+
+def test_clip_more_elements_than_32_bits(ag):
+    n = 2 ** 32 + 77
+    t = torch.full((n,), 0.5, dtype=BF16, device="cuda")
+    norm = ag.ag_grad_clip([t], 1024.0)
+    _ok(ag)
+    want = 0.5 * math.sqrt(n)
+    assert abs(float(norm) - want) <= want * 2.0 ** -23
+    scaled = torch.tensor(0.5 * 1024.0 / want).to(BF16).item()
+    for part in (t[:1000], t[n // 2:n // 2 + 1000], t[-1000:]):
+        assert bool((part == scaled).all())
