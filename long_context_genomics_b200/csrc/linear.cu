@@ -24,19 +24,62 @@ namespace {
 // sums.  Some of both sides, us: 1024 x 1024 x 1024 width 256 11.0, 128 8.4;
 // 4096 x 4096 x 1024 28.7, 35.3; 1152 x 1024 x 8192 in 1, 3, 7 parts 43.8,
 // 24.4, 27.1; 300 x 136 x 4096 in 1, 8, 24 parts 17.5, 10.3, 11.
+double item_time(int bn, int64_t deep) { return deep * (bn == 256 ? 620 : 430) + 300; }
+double join_time(int splits, int64_t M, int64_t N) {
+  return splits > 1 ? 6000 + static_cast<double>(splits) * M * partial_ld(N) * 8 / 4000 : 0;
+}
 GemmPlan plan_gemm(int64_t M, int64_t N, int64_t K, int clusters) {
   const int64_t k_tiles = (K + 63) / 64;
-  GemmPlan best{256, 1};
-  double least = 0;
+  GemmPlan best{256, 1, 0};
   for (int bn = 256; bn >= 128; bn -= 128) {
     const int64_t tiles = ((M + 255) / 256) * ((N + bn - 1) / bn);
     for (int splits = 1; splits <= 32 && splits <= k_tiles; ++splits) {
       const int64_t waves = (tiles * splits + clusters - 1) / clusters;
       const int64_t deep = (k_tiles + splits - 1) / splits;
-      double t = static_cast<double>(waves) * (deep * (bn == 256 ? 620 : 430) + 300) +
-                 (bn == 256 ? 10500 : 8700);
-      if (splits > 1) t += 6000 + static_cast<double>(splits) * M * partial_ld(N) * 8 / 4000;
-      if (least == 0 || t < least) least = t, best = {bn, splits};
+      const double t =
+          waves * item_time(bn, deep) + (bn == 256 ? 10500 : 8700) + join_time(splits, M, N);
+      if (best.time == 0 || t < best.time) best = {bn, splits, t};
+    }
+  }
+  return best;
+}
+
+// Both gradients of a layer in one launch (dW [N, K] over M rows in parts, then
+// dx [M, K] over N): the parts and turns with the least estimated time.  What is
+// idle in one product's last round then works on the other, and a launch with
+// its first loads and last stores is saved.  us in two launches and in one:
+// 8192 x 1152 x 1024 43.9, 36.0; 4096 x 1024 x 4096 with a GELU's slope 72.3, 61.1;
+// 1024 x 1024 x 1024 17.6, 10.3; 64 x 512 x 512 11.5, 6.6; 65536 x 128 x 128 29.8,
+// 28.9; 16384 x 4096 x 1024 200, 189; 1000 x 3000 x 600, whose dx could be split
+// when alone, 24.6, 26.6.
+struct PairPlan {
+  int bn, splits;
+  Turns turns;
+  double time;
+};
+PairPlan plan_pair(int64_t M, int64_t N, int64_t K, int clusters) {
+  const int64_t m_tiles = (M + 63) / 64, n_tiles = (N + 63) / 64;
+  PairPlan best{256, 1, {0, 0}, 0};
+  for (int bn = 256; bn >= 128; bn -= 128) {
+    const int64_t columns = (K + bn - 1) / bn, dx_items = (M + 255) / 256 * columns,
+                  dW_tiles = (N + 255) / 256 * columns;
+    const double dx_item = item_time(bn, n_tiles);
+    for (int splits = 1; splits <= 32 && splits <= m_tiles; ++splits) {
+      const double dW_item = item_time(bn, (m_tiles + splits - 1) / splits);
+      const int64_t rounds = dW_tiles * splits / clusters;
+      const int from = static_cast<int>(dW_tiles * splits % clusters), few = clusters - from;
+      // The clusters without an item in dW's last round can be so many rounds of
+      // dx ahead.
+      const int most = from > 0 ? static_cast<int>(dW_item / dx_item) + 1 : 0;
+      for (int extra = 0; extra <= most && extra <= 64; ++extra) {
+        const int64_t left = dx_items - static_cast<int64_t>(extra) * few;
+        const int64_t more = left > 0 ? (left + clusters - 1) / clusters : 0;
+        const double long_way = (rounds + (from > 0)) * dW_item + more * dx_item,
+                     short_way = rounds * dW_item + (extra + more) * dx_item;
+        const double t = (long_way > short_way ? long_way : short_way) +
+                         (bn == 256 ? 10500 : 8700) + join_time(splits, N, K);
+        if (best.time == 0 || t < best.time) best = {bn, splits, {from, extra}, t};
+      }
     }
   }
   return best;
@@ -283,14 +326,18 @@ int64_t partial_bytes(const GemmPlan &plan, int64_t M, int64_t N) {
   return plan.splits > 1 ? plan.splits * M * partial_ld(N) * 4 : 0;
 }
 
-cudaError_t run(Gemm &g) {
-  cudaError_t e = launch_gemm(g);
-  if (e != cudaSuccess || g.plan.splits == 1) return e;
+// The joining of a product's parts.
+cudaError_t join(const Gemm &g) {
+  if (g.plan.splits == 1) return cudaSuccess;
   const int v = g.epi.vec8 ? 8 : 1;
   const int64_t blocks = (g.M * ((g.N + v - 1) / v) + 255) / 256;  // at most 2^38 / 256
   return launch_after_previous(v == 8 ? linear_join_kernel<8> : linear_join_kernel<1>,
                                static_cast<unsigned>(blocks), 256, 0, g.stream, g.partial,
                                g.plan.splits, g.M, g.N, partial_ld(g.N), g.epi);
+}
+cudaError_t run(const Gemm &g) {
+  const cudaError_t e = launch_gemm(g);
+  return e == cudaSuccess ? join(g) : e;
 }
 
 struct FwdLayout {
@@ -319,6 +366,8 @@ int column_parts(int64_t M, int64_t N, bool vec, int num_sms) {
 struct BwdLayout {
   Packed dy, x, W;
   GemmPlan dx_plan, dW_plan;
+  PairPlan pair;
+  bool paired;
   float *partial;  // of dx, then of dW, then of db
   int db_parts;
   bool db_vec;
@@ -336,6 +385,13 @@ BwdLayout bwd_layout(const LinearBwd &a, Workspace &ws) {
     l.dW_plan = plan_gemm(a.N, a.K, a.M, a.num_sms / 2);
     l.x = place(a.x, a.M, a.K, a.ldx, ws);
     const int64_t b = partial_bytes(l.dW_plan, a.N, a.K);
+    partial = b > partial ? b : partial;
+  }
+  // In one launch where that is estimated to be faster (plan_pair).
+  if (a.dx.out && a.dW.out) {
+    l.pair = plan_pair(a.M, a.N, a.K, a.num_sms / 2);
+    l.paired = l.pair.time < l.dx_plan.time + l.dW_plan.time;
+    const int64_t b = l.paired ? partial_bytes({l.pair.bn, l.pair.splits, 0}, a.N, a.K) : 0;
     partial = b > partial ? b : partial;
   }
   if (a.db) {
@@ -390,16 +446,19 @@ cudaError_t launch_linear_bwd(const LinearBwd &a) {
   note(copies, l.W, a.W, a.ldw);
   note(copies, l.x, a.x, a.ldx);
   cudaError_t e = make(copies, a.num_sms, a.stream);
-  if (e == cudaSuccess && a.dx.out) {
-    Gemm g{l.dy.op, l.W.op, false, true, a.M, a.K, a.N, l.dx_plan, l.partial, a.dx,
-           a.num_sms, a.err, a.encode, a.stream};
-    e = run(g);
+  Gemm dx{l.dy.op, l.W.op, false, true, a.M, a.K, a.N, l.dx_plan, l.partial, a.dx,
+          a.num_sms, a.err, a.encode, a.stream};
+  Gemm dW{l.dy.op, l.x.op, true, true, a.N, a.K, a.M, l.dW_plan, l.partial, a.dW,
+          a.num_sms, a.err, a.encode, a.stream};
+  bool done = false;
+  if (e == cudaSuccess && l.paired) {
+    Gemm one = dx, two = dW;
+    one.plan = {l.pair.bn, 1, 0}, two.plan = {l.pair.bn, l.pair.splits, 0};
+    e = launch_gemm_pair(two, one, l.pair.turns, &done);
+    if (e == cudaSuccess && done) e = join(two);
   }
-  if (e == cudaSuccess && a.dW.out) {
-    Gemm g{l.dy.op, l.x.op, true, true, a.N, a.K, a.M, l.dW_plan, l.partial, a.dW,
-           a.num_sms, a.err, a.encode, a.stream};
-    e = run(g);
-  }
+  if (e == cudaSuccess && a.dx.out && !done) e = run(dx);
+  if (e == cudaSuccess && a.dW.out && !done) e = run(dW);
   if (e == cudaSuccess && a.db) {
     const int cols = l.db_vec ? 256 : 32;
     const dim3 grid(static_cast<unsigned>((a.N + cols - 1) / cols), l.db_parts);

@@ -14,8 +14,17 @@ struct Operand {
 };
 
 struct GemmPlan {
-  int bn;      // columns of a tile: 256 or 128
-  int splits;  // parts of the summed dimension
+  int bn;       // columns of a tile: 256 or 128
+  int splits;   // parts of the summed dimension
+  double time;  // estimated, in SM cycles
+};
+
+// Which items (tiles x parts) of a product a cluster takes, one a round: in the
+// first `extra` rounds only the clusters from `from` on take one each, in later
+// rounds all of them.  So the second of two products in one launch goes first to
+// the clusters that have one item fewer of the first.
+struct Turns {
+  int from, extra;
 };
 
 // C[m, n] = sum_k A(m, k) B(n, k), m < M, n < N, k < K.  A lies as [M][K], or
@@ -35,5 +44,10 @@ struct Gemm {
 };
 inline int64_t partial_ld(int64_t N) { return (N + 7) / 8 * 8; }
 cudaError_t launch_gemm(const Gemm &g);
+// The gradients of a linear layer in one launch: dW (a_mn, b_mn; its items go
+// first), then dx (b_mn, one part) by `turns`; both with tiles of one width.
+// `done` is false, and nothing is launched, where TMA cannot address dW's or
+// dx's arrays.
+cudaError_t launch_gemm_pair(const Gemm &dW, const Gemm &dx, Turns turns, bool *done);
 
 }  // namespace ag

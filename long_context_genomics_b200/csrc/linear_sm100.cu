@@ -38,6 +38,10 @@
 // residual: 128 tiles over 74 pairs are two rounds, the second 73 % full, and the
 // first loads and last stores are not hidden.
 //
+// Both gradients of a layer run in one launch (linear_gemm_pair_kernel): the
+// roles go from dW's tiles to dx's without a pause, and the clusters that have a
+// tile of dW less take more of dx (Turns).
+//
 // A small C does not fill the GPU: the summed dimension is then split between
 // clusters, each writing float32 partial sums that a second kernel
 // (linear_join_kernel) adds in order and finishes.
@@ -96,6 +100,7 @@ struct Params {
   int64_t M, N;               // rows and columns of C
   int items;                  // tiles x splits (below 2^31: see check_linear_sizes)
   int tiles_m, tiles_n, k_tiles, splits;
+  Turns turns;
   int boxes;                  // every array of the epilogue is TMA's to read or write
   int wide;                   // the output is float32
   uint32_t idesc;
@@ -123,6 +128,23 @@ __device__ __forceinline__ Item item_at(const Params &p, int i) {
   return t;
 }
 
+// This cluster's item of round r (by the product's turns, or with one product in
+// the launch all clusters in every round); past the last one at or after p.items.
+template <bool TURNS>
+__device__ __forceinline__ int item_of(const Params &p, int r) {
+  const int c = blockIdx.x / 2, all = gridDim.x / 2;
+  if constexpr (!TURNS) return c;
+  const int few = all - p.turns.from;
+  if (c < p.turns.from) return p.turns.extra * few + r * all + c;
+  return r < p.turns.extra ? r * few + c - p.turns.from
+                           : p.turns.extra * few + (r - p.turns.extra) * all + c;
+}
+
+template <bool TURNS>
+__device__ __forceinline__ int next_item(const Params &p, int i, int &r) {
+  return TURNS ? item_of<true>(p, ++r) : i + static_cast<int>(gridDim.x / 2);
+}
+
 // One 64-deep tile of `rows` rows of an operand: K-major, one box of 64 terms
 // x rows; MN-major, boxes of 64 rows x 64 terms.
 template <bool MN, int ROWS>
@@ -137,15 +159,16 @@ __device__ __forceinline__ void load_tile(uint8_t *dst, const CUtensorMap *map, 
   }
 }
 
-template <int BN, bool A_MN, bool B_MN>
-__device__ __forceinline__ void load_role(const CUtensorMap *ma, const CUtensorMap *mb,
-                                          uint8_t *ring, Barriers *bars, const Params &p,
-                                          uint32_t rank, volatile int *abort) {
+// The roles' loops over a product's items.  n counts k tiles and acc accumulators,
+// through both products where a launch has two.
+template <int BN, bool A_MN, bool B_MN, bool TURNS>
+__device__ __forceinline__ bool load_items(const CUtensorMap *ma, const CUtensorMap *mb,
+                                           uint8_t *ring, Barriers *bars, const Params &p,
+                                           uint32_t rank, volatile int *abort, uint32_t &n) {
   using S = Shape<BN>;
   const uint32_t full0 = cluster_addr(&bars->full[0], 0);
-  uint32_t n = 0;
   bool ok = true;
-  for (int i = blockIdx.x / 2; ok && i < p.items; i += gridDim.x / 2) {
+  for (int r = 0, i = item_of<TURNS>(p, 0); ok && i < p.items; i = next_item<TURNS>(p, i, r)) {
     const Item t = item_at(p, i);
     const int row_a = t.tm * 256 + static_cast<int>(rank) * 128;
     const int row_b = t.tn * BN + static_cast<int>(rank) * (BN / 2);
@@ -163,9 +186,13 @@ __device__ __forceinline__ void load_role(const CUtensorMap *ma, const CUtensorM
       ++n;
     }
   }
-  // Every copy of the pair lands before its CTAs exit: the products wait for
-  // all of them, so only after a failure may some be on their way.
-  if (ok) return;
+  return ok;
+}
+// Every copy of the pair lands before its CTAs exit: the products wait for
+// all of them, so only after a failure may some be on their way.
+template <int BN>
+__device__ __forceinline__ void load_drain(Barriers *bars, uint32_t rank, uint32_t n) {
+  using S = Shape<BN>;
   if (rank == 0) {
     for (uint32_t i = n > S::kStages ? n - S::kStages : 0; i < n; ++i) {
       const uint32_t a = smem_u32(&bars->full[i % S::kStages]);
@@ -180,18 +207,18 @@ __device__ __forceinline__ void load_role(const CUtensorMap *ma, const CUtensorM
 }
 
 // The whole warp of the even CTA; one elected lane issues.
-template <int BN, bool A_MN, bool B_MN>
-__device__ __forceinline__ void issue_role(uint8_t *ring, Barriers *bars, uint32_t tmem,
-                                           const Params &p, volatile int *abort) {
+template <int BN, bool A_MN, bool B_MN, bool TURNS>
+__device__ __forceinline__ bool issue_items(uint8_t *ring, Barriers *bars, uint32_t tmem,
+                                            const Params &p, volatile int *abort, uint32_t &n,
+                                            uint32_t &acc) {
   using S = Shape<BN>;
   constexpr uint32_t kHi = desc_sw128_hi(1024);  // 8-row groups 1 KB apart, either major
   constexpr uint32_t kAtom = 64 * kStepBytes;    // MN-major: the next 64 rows
   // 16 terms further: 32 bytes along a K-major row, 16 rows of an MN-major tile.
   constexpr uint32_t kAStep = (A_MN ? 16 * kStepBytes : 32) >> 4;
   constexpr uint32_t kBStep = (B_MN ? 16 * kStepBytes : 32) >> 4;
-  uint32_t n = 0, acc = 0;
   bool ok = true;
-  for (int i = blockIdx.x / 2; ok && i < p.items; i += gridDim.x / 2) {
+  for (int r = 0, i = item_of<TURNS>(p, 0); ok && i < p.items; i = next_item<TURNS>(p, i, r)) {
     const Item t = item_at(p, i);
     for (int k0 = t.kb; ok && k0 < t.ke; k0 += kPromote, ++acc) {
       const uint32_t b = acc & 1u, use = acc >> 1;
@@ -218,7 +245,10 @@ __device__ __forceinline__ void issue_role(uint8_t *ring, Barriers *bars, uint32
       if (ok) umma2_commit_both_w(&bars->acc_full[b]);
     }
   }
-  // Everything this warp issued completes before tensor memory is freed.
+  return ok;
+}
+// Everything this warp issued completes before tensor memory is freed.
+__device__ __forceinline__ void issue_drain(Barriers *bars) {
   umma2_commit_self_w(&bars->drain);
   const uint32_t a = smem_u32(&bars->drain);
   const uint64_t t0 = globaltimer_ns();
@@ -474,10 +504,11 @@ __device__ __forceinline__ void plain_epilogue(const Params &p, const float2 (&s
   }
 }
 
-template <int BN, int ACT, bool SLOPE, bool WIDE, bool BOXES>
-__device__ __forceinline__ void epilogue_role(uint8_t *stage, Barriers *bars, uint32_t tmem,
-                                              const Params &p, const EpiMaps *maps, uint32_t rank,
-                                              int warp, int lane, volatile int *abort) {
+template <int BN, int ACT, bool SLOPE, bool WIDE, bool BOXES, bool TURNS>
+__device__ __forceinline__ bool finish_items_as(uint8_t *stage, Barriers *bars, uint32_t tmem,
+                                             const Params &p, const EpiMaps *maps, uint32_t rank,
+                                             int warp, int lane, volatile int *abort,
+                                             uint32_t &acc) {
   constexpr int kCols = BN / 4;                  // columns per warp
   const int quarter = warp % 4, part = (warp - kFirstEpiWarp) / 4;
   const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
@@ -485,9 +516,8 @@ __device__ __forceinline__ void epilogue_role(uint8_t *stage, Barriers *bars, ui
   uint8_t *own = stage + (warp - kFirstEpiWarp) * kBoxBytes;
   BoxEpilogue<kCols, ACT, SLOPE, WIDE> boxes{
       p, maps, own, &bars->in_full[warp - kFirstEpiWarp], abort, lane};
-  uint32_t acc = 0;
   bool ok = true;
-  for (int i = blockIdx.x / 2; ok && i < p.items; i += gridDim.x / 2) {
+  for (int r = 0, i = item_of<TURNS>(p, 0); ok && i < p.items; i = next_item<TURNS>(p, i, r)) {
     const Item t = item_at(p, i);
     const int64_t row0 = static_cast<int64_t>(t.tm) * 256 + rank * 128 + quarter * 32;
     const int64_t col0 = static_cast<int64_t>(t.tn) * BN + kCols * part;
@@ -522,13 +552,31 @@ __device__ __forceinline__ void epilogue_role(uint8_t *stage, Barriers *bars, ui
     }
   }
   if constexpr (BOXES) boxes.drain();
+  return ok;
+}
+template <int BN, int ACT, bool SLOPE, bool BOXES, bool TURNS>
+__device__ __forceinline__ bool finish_items(uint8_t *stage, Barriers *bars, uint32_t tmem,
+                                             const Params &p, const EpiMaps *maps, uint32_t rank,
+                                             int warp, int lane, volatile int *abort,
+                                             uint32_t &acc) {
+  if (BOXES && p.wide)
+    return finish_items_as<BN, ACT, SLOPE, true, BOXES, TURNS>(stage, bars, tmem, p, maps, rank,
+                                                               warp, lane, abort, acc);
+  return finish_items_as<BN, ACT, SLOPE, false, BOXES, TURNS>(stage, bars, tmem, p, maps, rank,
+                                                              warp, lane, abort, acc);
 }
 
-template <int BN, bool A_MN, bool B_MN, int ACT, bool SLOPE, bool BOXES>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    linear_gemm_kernel(const __grid_constant__ CUtensorMap ma,
-                       const __grid_constant__ CUtensorMap mb,
-                       const __grid_constant__ EpiMaps maps, const __grid_constant__ Params p) {
+// A product as a kernel's argument.
+struct Product {
+  CUtensorMap ma, mb;
+  EpiMaps maps;
+  Params p;
+};
+
+// A CTA's setup, its roles (each returns whether all its waits ended) and its end.
+template <int BN, typename Load, typename Issue, typename Finish>
+__device__ __forceinline__ void run_roles(const CUtensorMap *ma, const CUtensorMap *mb, Load load,
+                                          Issue issue, Finish finish) {
   using S = Shape<BN>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -550,8 +598,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mbar_init(&bars->drain, 1);
     bars->abort = 0;
     fence_mbar_init();
-    prefetch_tensormap(&ma);
-    prefetch_tensormap(&mb);
+    prefetch_tensormap(ma);
+    prefetch_tensormap(mb);
   }
   if (warp == 1) {
     tmem_alloc2(&bars->tmem_base, S::kCols);
@@ -566,18 +614,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp < kFirstEpiWarp) {
     regs_dec<kRegsLow>();
     if (warp == 1 && rank == 0) {
-      issue_role<BN, A_MN, B_MN>(ring, bars, tmem, p, abort);
+      uint32_t n = 0, acc = 0;
+      issue(ring, bars, tmem, abort, n, acc);
+      issue_drain(bars);
     } else if (warp == 0 && lane == 0) {
-      load_role<BN, A_MN, B_MN>(&ma, &mb, ring, bars, p, rank, abort);
+      uint32_t n = 0;
+      if (!load(ring, bars, rank, abort, n)) load_drain<BN>(bars, rank, n);
     }
   } else {
     regs_inc<kRegsHigh>();
-    if (BOXES && p.wide)
-      epilogue_role<BN, ACT, SLOPE, true, BOXES>(stage, bars, tmem, p, &maps, rank, warp, lane,
-                                                 abort);
-    else
-      epilogue_role<BN, ACT, SLOPE, false, BOXES>(stage, bars, tmem, p, &maps, rank, warp, lane,
-                                                  abort);
+    uint32_t acc = 0;
+    finish(stage, bars, tmem, rank, warp, lane, abort, acc);
   }
   __syncwarp();
   // Neither CTA leaves while the other may use its shared or tensor memory.
@@ -590,47 +637,109 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 template <int BN, bool A_MN, bool B_MN, int ACT, bool SLOPE, bool BOXES>
-cudaError_t launch(const Gemm &g, const Params &p, const CUtensorMap &ma, const CUtensorMap &mb,
-                   const EpiMaps &maps) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    linear_gemm_kernel(const __grid_constant__ Product a) {
+  run_roles<BN>(
+      &a.ma, &a.mb,
+      [&](uint8_t *ring, Barriers *bars, uint32_t rank, volatile int *abort, uint32_t &n) {
+        return load_items<BN, A_MN, B_MN, false>(&a.ma, &a.mb, ring, bars, a.p, rank, abort, n);
+      },
+      [&](uint8_t *ring, Barriers *bars, uint32_t tmem, volatile int *abort, uint32_t &n,
+          uint32_t &acc) { issue_items<BN, A_MN, B_MN, false>(ring, bars, tmem, a.p, abort, n, acc); },
+      [&](uint8_t *stage, Barriers *bars, uint32_t tmem, uint32_t rank, int warp, int lane,
+          volatile int *abort, uint32_t &acc) {
+        finish_items<BN, ACT, SLOPE, BOXES, false>(stage, bars, tmem, a.p, &a.maps, rank, warp, lane,
+                                            abort, acc);
+      });
+}
+
+// Two products one after the other, without a pause between them: dW = dy^T x,
+// then dx = (dy W) times the activation's derivative.
+template <int BN, int ACT, bool SLOPE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    linear_gemm_pair_kernel(const __grid_constant__ Product a, const __grid_constant__ Product b) {
+  run_roles<BN>(
+      &a.ma, &a.mb,
+      [&](uint8_t *ring, Barriers *bars, uint32_t rank, volatile int *abort, uint32_t &n) {
+        return load_items<BN, true, true, false>(&a.ma, &a.mb, ring, bars, a.p, rank, abort, n) &&
+               load_items<BN, false, true, true>(&b.ma, &b.mb, ring, bars, b.p, rank, abort, n);
+      },
+      [&](uint8_t *ring, Barriers *bars, uint32_t tmem, volatile int *abort, uint32_t &n,
+          uint32_t &acc) {
+        if (issue_items<BN, true, true, false>(ring, bars, tmem, a.p, abort, n, acc))
+          issue_items<BN, false, true, true>(ring, bars, tmem, b.p, abort, n, acc);
+      },
+      [&](uint8_t *stage, Barriers *bars, uint32_t tmem, uint32_t rank, int warp, int lane,
+          volatile int *abort, uint32_t &acc) {
+        if (finish_items<BN, AG_ACT_NONE, false, true, false>(stage, bars, tmem, a.p, &a.maps, rank, warp,
+                                                       lane, abort, acc))
+          finish_items<BN, ACT, SLOPE, true, true>(stage, bars, tmem, b.p, &b.maps, rank, warp, lane,
+                                             abort, acc);
+      });
+}
+
+// kKernel(products...) on so many clusters.
+template <int BN, auto kKernel, typename... P>
+cudaError_t launch_clusters(int clusters, cudaStream_t stream, const P &...products) {
   static std::once_flag once[64];
   static cudaError_t once_err[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  auto *kernel = linear_gemm_kernel<BN, A_MN, B_MN, ACT, SLOPE, BOXES>;
   std::call_once(once[dev], [&] {
-    once_err[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    once_err[dev] = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(smem_bytes<BN>()));
     // The register split waits for ever on a launch with fewer registers.
     cudaFuncAttributes fa;
-    if (once_err[dev] == cudaSuccess) once_err[dev] = cudaFuncGetAttributes(&fa, kernel);
+    if (once_err[dev] == cudaSuccess) once_err[dev] = cudaFuncGetAttributes(&fa, kKernel);
     if (once_err[dev] == cudaSuccess && static_cast<uint32_t>(fa.numRegs) < kRegsLaunch)
       once_err[dev] = cudaErrorInvalidConfiguration;
   });
   if (once_err[dev] != cudaSuccess) return once_err[dev];
-  const int clusters = p.items < g.num_sms / 2 ? p.items : g.num_sms / 2;
-  return launch_after_previous(kernel, 2 * clusters, kThreads, smem_bytes<BN>(), g.stream, ma, mb,
-                               maps, p);
+  return launch_after_previous(kKernel, 2 * clusters, kThreads, smem_bytes<BN>(), stream,
+                               products...);
 }
 
 template <int BN, bool A_MN, bool B_MN, bool SLOPE>
-cudaError_t launch_act(const Gemm &g, const Params &p, const CUtensorMap &ma, const CUtensorMap &mb,
-                       const EpiMaps &maps) {
+cudaError_t launch_act(const Gemm &g, const Product &a) {
   // The activation is compiled into the box epilogue; the plain one looks it up.
   // Partial sums have none yet.
-  if (!p.boxes) return launch<BN, A_MN, B_MN, AG_ACT_NONE, false, false>(g, p, ma, mb, maps);
-  if constexpr (A_MN) {
-    return launch<BN, A_MN, B_MN, AG_ACT_NONE, false, true>(g, p, ma, mb, maps);
-  } else {
-    switch (p.epi.act) {
-      case AG_ACT_RELU: return launch<BN, A_MN, B_MN, AG_ACT_RELU, SLOPE, true>(g, p, ma, mb, maps);
-      case AG_ACT_GELU: return launch<BN, A_MN, B_MN, AG_ACT_GELU, SLOPE, true>(g, p, ma, mb, maps);
+  const int n = min(a.p.items, g.num_sms / 2);
+  const cudaStream_t s = g.stream;
+  if (!a.p.boxes)
+    return launch_clusters<BN, linear_gemm_kernel<BN, A_MN, B_MN, AG_ACT_NONE, false, false>>(n, s, a);
+  if constexpr (!A_MN) {
+    switch (a.p.epi.act) {
+      case AG_ACT_RELU:
+        return launch_clusters<BN, linear_gemm_kernel<BN, A_MN, B_MN, AG_ACT_RELU, SLOPE, true>>(n, s, a);
+      case AG_ACT_GELU:
+        return launch_clusters<BN, linear_gemm_kernel<BN, A_MN, B_MN, AG_ACT_GELU, SLOPE, true>>(n, s, a);
       case AG_ACT_GELU_TANH:
-        return launch<BN, A_MN, B_MN, AG_ACT_GELU_TANH, SLOPE, true>(g, p, ma, mb, maps);
-      case AG_ACT_SILU: return launch<BN, A_MN, B_MN, AG_ACT_SILU, SLOPE, true>(g, p, ma, mb, maps);
-      default: return launch<BN, A_MN, B_MN, AG_ACT_NONE, false, true>(g, p, ma, mb, maps);
+        return launch_clusters<BN, linear_gemm_kernel<BN, A_MN, B_MN, AG_ACT_GELU_TANH, SLOPE, true>>(n, s, a);
+      case AG_ACT_SILU:
+        return launch_clusters<BN, linear_gemm_kernel<BN, A_MN, B_MN, AG_ACT_SILU, SLOPE, true>>(n, s, a);
+      default: break;
     }
+  }
+  return launch_clusters<BN, linear_gemm_kernel<BN, A_MN, B_MN, AG_ACT_NONE, false, true>>(n, s, a);
+}
+
+template <int BN>
+cudaError_t launch_pair(const Gemm &g, const Product &a, const Product &b) {
+  const int n = g.num_sms / 2;
+  const cudaStream_t s = g.stream;
+  switch (b.p.epi.act) {
+    case AG_ACT_RELU:
+      return launch_clusters<BN, linear_gemm_pair_kernel<BN, AG_ACT_RELU, true>>(n, s, a, b);
+    case AG_ACT_GELU:
+      return launch_clusters<BN, linear_gemm_pair_kernel<BN, AG_ACT_GELU, true>>(n, s, a, b);
+    case AG_ACT_GELU_TANH:
+      return launch_clusters<BN, linear_gemm_pair_kernel<BN, AG_ACT_GELU_TANH, true>>(n, s, a, b);
+    case AG_ACT_SILU:
+      return launch_clusters<BN, linear_gemm_pair_kernel<BN, AG_ACT_SILU, true>>(n, s, a, b);
+    default:
+      return launch_clusters<BN, linear_gemm_pair_kernel<BN, AG_ACT_NONE, false>>(n, s, a, b);
   }
 }
 
@@ -660,15 +769,19 @@ bool boxable(const void *p, int64_t ld, int size) {
 
 }  // namespace gemm
 
-cudaError_t launch_gemm(const Gemm &g) {
-  using namespace gemm;
-  Params p{};
+namespace gemm {
+namespace {
+// The kernel's argument for a product; false if a tensor map cannot be made.
+bool prepare(const Gemm &g, Turns turns, Product *a) {
+  Params &p = a->p;
+  p = Params{};
   p.M = g.M, p.N = g.N;
   p.tiles_m = static_cast<int>((g.M + 255) / 256);
   p.tiles_n = static_cast<int>((g.N + g.plan.bn - 1) / g.plan.bn);
   p.k_tiles = static_cast<int>((g.K + 63) / 64);
   p.splits = g.plan.splits;
   p.items = p.tiles_m * p.tiles_n * p.splits;
+  p.turns = turns;
   p.idesc = idesc_half_f32(256, g.plan.bn, g.epi.dtype == AG_BF16, g.a_mn, g.b_mn);
   p.err = g.err;
   p.epi = g.epi;
@@ -682,12 +795,12 @@ cudaError_t launch_gemm(const Gemm &g) {
   p.wide = e.out_dtype == AG_F32;
   p.boxes = boxable(e.out, e.ld_out, out_size) && boxable(e.residual, e.ld_res, out_size) &&
             boxable(e.pre_in, e.ld_pre_in, 2) && boxable(e.pre_out, e.ld_pre_out, 2);
-  CUtensorMap ma, mb;
-  EpiMaps maps{};
+  a->maps = EpiMaps{};
   const Operand &A = g.A, &B = g.B;
-  bool ok = encode_map(g, &ma, A.p, 2, 0, A.rows, A.cols, A.ld, g.a_mn ? 64 : 128, 64) &&
-            encode_map(g, &mb, B.p, 2, 0, B.rows, B.cols, B.ld, g.b_mn ? 64 : g.plan.bn / 2, 64);
+  bool ok = encode_map(g, &a->ma, A.p, 2, 0, A.rows, A.cols, A.ld, g.a_mn ? 64 : 128, 64) &&
+            encode_map(g, &a->mb, B.p, 2, 0, B.rows, B.cols, B.ld, g.b_mn ? 64 : g.plan.bn / 2, 64);
   if (p.boxes) {
+    EpiMaps &maps = a->maps;
     const int width = p.wide ? 32 : g.plan.bn / 4;
     ok = ok && encode_map(g, &maps.out, e.out, out_size, p.splits, g.M, g.N, e.ld_out, 32, width);
     if (e.residual)
@@ -697,15 +810,33 @@ cudaError_t launch_gemm(const Gemm &g) {
     if (e.pre_out)
       ok = ok && encode_map(g, &maps.pre, e.pre_out, 2, 1, g.M, g.N, e.ld_pre_out, 32, width);
   }
-  if (!ok) return cudaErrorInvalidValue;
+  return ok;
+}
+}  // namespace
+}  // namespace gemm
+
+cudaError_t launch_gemm(const Gemm &g) {
+  using namespace gemm;
+  Product a;
+  if (!prepare(g, Turns{0, 0}, &a)) return cudaErrorInvalidValue;
   if (g.plan.bn == 256) {
-    if (g.a_mn) return launch_act<256, true, true, false>(g, p, ma, mb, maps);
-    return g.b_mn ? launch_act<256, false, true, true>(g, p, ma, mb, maps)
-                  : launch_act<256, false, false, false>(g, p, ma, mb, maps);
+    if (g.a_mn) return launch_act<256, true, true, false>(g, a);
+    return g.b_mn ? launch_act<256, false, true, true>(g, a)
+                  : launch_act<256, false, false, false>(g, a);
   }
-  if (g.a_mn) return launch_act<128, true, true, false>(g, p, ma, mb, maps);
-  return g.b_mn ? launch_act<128, false, true, true>(g, p, ma, mb, maps)
-                : launch_act<128, false, false, false>(g, p, ma, mb, maps);
+  if (g.a_mn) return launch_act<128, true, true, false>(g, a);
+  return g.b_mn ? launch_act<128, false, true, true>(g, a)
+                : launch_act<128, false, false, false>(g, a);
+}
+
+cudaError_t launch_gemm_pair(const Gemm &dW, const Gemm &dx, Turns turns, bool *done) {
+  using namespace gemm;
+  Product a, b;
+  *done = false;
+  if (!prepare(dW, Turns{0, 0}, &a) || !prepare(dx, turns, &b)) return cudaErrorInvalidValue;
+  if (!a.p.boxes || !b.p.boxes) return cudaSuccess;
+  *done = true;
+  return dx.plan.bn == 256 ? launch_pair<256>(dx, a, b) : launch_pair<128>(dx, a, b);
 }
 
 }  // namespace ag

@@ -354,6 +354,38 @@ def test_linear_bwd_rows_apart(ag, M, N, K, pad):
     _linear_bwd_case(ag, M, N, K, pad=pad, act="gelu")
 
 
+@pytest.mark.parametrize("act", ["none", "gelu"])
+@pytest.mark.parametrize("M,N,K", [(9, 40, 72), (257, 264, 136), (300, 61, 37), (1000, 1504, 600),
+                                   (2048, 64, 40), (5000, 136, 128), (4096, 1024, 1024)])
+def test_linear_bwd_of_one_gradient(ag, M, N, K, act):
+    """Each gradient by itself is a launch of its own, with its own plan."""
+    g = _gen(M + N + K)
+    dy, x = _randn(g, M, N, dtype=BF16), _randn(g, M, K, dtype=BF16)
+    W = _randn(g, N, K, dtype=BF16, scale=1 / math.sqrt(N))
+    z = _randn(g, M, K, dtype=BF16) if act != "none" else None
+    dx, none, _ = ag.ag_linear_bwd(dy, x, W, act=act, preact=z, need_dW=False, need_db=False)
+    none2, dW, _ = ag.ag_linear_bwd(dy, x, W, act=act, preact=z, need_dx=False, need_db=False)
+    _ok(ag)
+    assert none is None and none2 is None
+    dyd, xd, Wd = dy.double(), x.double(), W.double()
+    want, tol = dyd @ Wd, (N + 8) * 2.0 ** -23 * (dyd.abs() @ Wd.abs())
+    if z is not None:
+        tol = tol * 1.13 + want.abs() * 2.0 ** -20 * (1 + z.double().abs())
+        want = want * ref.act_slope(z.double(), act)
+    _close("dx", dx, want, tol * (1 + 2.0 ** -7) + _half_step(BF16, want))
+    want = dyd.T @ xd
+    _close("dW", dW, want, (M + 8) * 2.0 ** -23 * (dyd.abs().T @ xd.abs()) * (1 + 2.0 ** -22)
+           + _half_step(F32, want))
+
+
+@pytest.mark.parametrize("M,N,K,act", [(8192, 1152, 1024, "none"), (4096, 1024, 4096, "gelu"),
+                                       (19000, 256, 256, "silu"), (40000, 128, 128, "none"),
+                                       (1000, 3008, 600, "relu"), (300, 200, 5000, "gelu_tanh")])
+def test_linear_bwd_of_many_tiles(ag, M, N, K, act):
+    """More tiles of either gradient than clusters, in uneven rounds."""
+    _linear_bwd_case(ag, M, N, K, act=act)
+
+
 def test_linear_bwd_only_what_is_needed(ag):
     g = _gen(3)
     dy, x, W = (_randn(g, *s, dtype=BF16) for s in ((70, 48), (70, 96), (48, 96)))
