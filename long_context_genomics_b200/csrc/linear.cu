@@ -50,8 +50,8 @@ GemmPlan plan_gemm(int64_t M, int64_t N, int64_t K, int clusters) {
 // its first loads and last stores is saved.  us in two launches and in one:
 // 8192 x 1152 x 1024 43.9, 36.0; 4096 x 1024 x 4096 with a GELU's slope 72.3, 61.1;
 // 1024 x 1024 x 1024 17.6, 10.3; 64 x 512 x 512 11.5, 6.6; 65536 x 128 x 128 29.8,
-// 28.9; 16384 x 4096 x 1024 200, 189; 1000 x 3000 x 600, whose dx could be split
-// when alone, 24.6, 26.6.
+// 28.9; 16384 x 4096 x 1024 200, 189; 777 x 501 x 1003 (plain epilogues) 21.7, 13.4;
+// 1000 x 3000 x 600, whose dx could be split when alone, 24.6, 26.6.
 struct PairPlan {
   int bn, splits;
   Turns turns;

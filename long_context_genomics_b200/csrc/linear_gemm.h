@@ -46,8 +46,8 @@ inline int64_t partial_ld(int64_t N) { return (N + 7) / 8 * 8; }
 cudaError_t launch_gemm(const Gemm &g);
 // The gradients of a linear layer in one launch: dW (a_mn, b_mn; its items go
 // first), then dx (b_mn, one part) by `turns`; both with tiles of one width.
-// `done` is false, and nothing is launched, where TMA cannot address dW's or
-// dx's arrays.
+// `done` is false, and nothing is launched, where TMA can address dx's arrays but
+// not dW's (which is rare enough to take two launches).
 cudaError_t launch_gemm_pair(const Gemm &dW, const Gemm &dx, Turns turns, bool *done);
 
 }  // namespace ag

@@ -655,7 +655,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 // Two products one after the other, without a pause between them: dW = dy^T x,
 // then dx = (dy W) times the activation's derivative.
-template <int BN, int ACT, bool SLOPE>
+template <int BN, int ACT, bool SLOPE, bool W_BOXES, bool X_BOXES>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     linear_gemm_pair_kernel(const __grid_constant__ Product a, const __grid_constant__ Product b) {
   run_roles<BN>(
@@ -671,9 +671,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       },
       [&](uint8_t *stage, Barriers *bars, uint32_t tmem, uint32_t rank, int warp, int lane,
           volatile int *abort, uint32_t &acc) {
-        if (finish_items<BN, AG_ACT_NONE, false, true, false>(stage, bars, tmem, a.p, &a.maps, rank, warp,
+        if (finish_items<BN, AG_ACT_NONE, false, W_BOXES, false>(stage, bars, tmem, a.p, &a.maps, rank, warp,
                                                        lane, abort, acc))
-          finish_items<BN, ACT, SLOPE, true, true>(stage, bars, tmem, b.p, &b.maps, rank, warp, lane,
+          finish_items<BN, ACT, SLOPE, X_BOXES, true>(stage, bars, tmem, b.p, &b.maps, rank, warp, lane,
                                              abort, acc);
       });
 }
@@ -729,17 +729,22 @@ template <int BN>
 cudaError_t launch_pair(const Gemm &g, const Product &a, const Product &b) {
   const int n = g.num_sms / 2;
   const cudaStream_t s = g.stream;
+  constexpr int kNone = AG_ACT_NONE;
+  if (!b.p.boxes)
+    return a.p.boxes
+               ? launch_clusters<BN, linear_gemm_pair_kernel<BN, kNone, false, true, false>>(n, s, a, b)
+               : launch_clusters<BN, linear_gemm_pair_kernel<BN, kNone, false, false, false>>(n, s, a, b);
   switch (b.p.epi.act) {
     case AG_ACT_RELU:
-      return launch_clusters<BN, linear_gemm_pair_kernel<BN, AG_ACT_RELU, true>>(n, s, a, b);
+      return launch_clusters<BN, linear_gemm_pair_kernel<BN, AG_ACT_RELU, true, true, true>>(n, s, a, b);
     case AG_ACT_GELU:
-      return launch_clusters<BN, linear_gemm_pair_kernel<BN, AG_ACT_GELU, true>>(n, s, a, b);
+      return launch_clusters<BN, linear_gemm_pair_kernel<BN, AG_ACT_GELU, true, true, true>>(n, s, a, b);
     case AG_ACT_GELU_TANH:
-      return launch_clusters<BN, linear_gemm_pair_kernel<BN, AG_ACT_GELU_TANH, true>>(n, s, a, b);
+      return launch_clusters<BN, linear_gemm_pair_kernel<BN, AG_ACT_GELU_TANH, true, true, true>>(n, s, a, b);
     case AG_ACT_SILU:
-      return launch_clusters<BN, linear_gemm_pair_kernel<BN, AG_ACT_SILU, true>>(n, s, a, b);
+      return launch_clusters<BN, linear_gemm_pair_kernel<BN, AG_ACT_SILU, true, true, true>>(n, s, a, b);
     default:
-      return launch_clusters<BN, linear_gemm_pair_kernel<BN, AG_ACT_NONE, false>>(n, s, a, b);
+      return launch_clusters<BN, linear_gemm_pair_kernel<BN, kNone, false, true, true>>(n, s, a, b);
   }
 }
 
@@ -834,7 +839,7 @@ cudaError_t launch_gemm_pair(const Gemm &dW, const Gemm &dx, Turns turns, bool *
   Product a, b;
   *done = false;
   if (!prepare(dW, Turns{0, 0}, &a) || !prepare(dx, turns, &b)) return cudaErrorInvalidValue;
-  if (!a.p.boxes || !b.p.boxes) return cudaSuccess;
+  if (!a.p.boxes && b.p.boxes) return cudaSuccess;
   *done = true;
   return dx.plan.bn == 256 ? launch_pair<256>(dx, a, b) : launch_pair<128>(dx, a, b);
 }

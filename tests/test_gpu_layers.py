@@ -380,6 +380,7 @@ def test_linear_bwd_of_one_gradient(ag, M, N, K, act):
 
 @pytest.mark.parametrize("M,N,K,act", [(8192, 1152, 1024, "none"), (4096, 1024, 4096, "gelu"),
                                        (19000, 256, 256, "silu"), (40000, 128, 128, "none"),
+                                       (9000, 301, 701, "gelu"), (3000, 1500, 999, "none"),
                                        (1000, 3008, 600, "relu"), (300, 200, 5000, "gelu_tanh")])
 def test_linear_bwd_of_many_tiles(ag, M, N, K, act):
     """More tiles of either gradient than clusters, in uneven rounds."""
