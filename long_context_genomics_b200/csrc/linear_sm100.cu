@@ -446,15 +446,6 @@ __device__ __forceinline__ void finish_column(const LinearEpilogue &e, const flo
 #pragma unroll
   for (int i = 0; i < 8; ++i)
     v[i] = stage[(r + i) * 32 + (((lane >> 2) ^ ((r + i) & 7)) << 2) + (lane & 3)];
-  const auto load = [&](const void *p, int64_t ld, int dtype) {
-    int64_t at = row * ld + col;
-#pragma unroll
-    for (int i = 0; i < 8; ++i, at += ld) {
-      float one[1] = {0.f};
-      if (i < n) load_values<1>(p, at, dtype, one);
-      x[i] = one[0];
-    }
-  };
   const auto store = [&](void *p, int64_t ld, int dtype) {
     int64_t at = row * ld + col;
 #pragma unroll
@@ -465,7 +456,7 @@ __device__ __forceinline__ void finish_column(const LinearEpilogue &e, const flo
   };
   if (e.pre_out) store(e.pre_out, e.ld_pre_out, e.dtype);
   if (e.pre_in) {
-    load(e.pre_in, e.ld_pre_in, e.dtype);
+    load_apart<8>(e.pre_in, row * e.ld_pre_in + col, e.ld_pre_in, n, e.dtype, x);
     act_all<true>(x, e.act);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] *= x[i];
@@ -473,7 +464,7 @@ __device__ __forceinline__ void finish_column(const LinearEpilogue &e, const flo
     act_all<false>(v, e.act);
   }
   if (e.residual) {
-    load(e.residual, e.ld_res, e.out_dtype);
+    load_apart<8>(e.residual, row * e.ld_res + col, e.ld_res, n, e.out_dtype, x);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] += x[i];
   }
