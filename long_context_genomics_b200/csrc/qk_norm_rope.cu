@@ -26,7 +26,10 @@
 // positions 23.6 us.  Gradients of half of that (76 MB): 25 us.
 //
 // General kernels: one warp per row through shared memory, any size or stride.  A
-// block takes `at_once` positions a turn, enough for a row to each warp.
+// block takes `at_once` positions a turn, enough for a row to each warp.  Bound by
+// the instructions around each element: 8192 positions of 8 + 1 heads of 100 in
+// bf16 57 us, the gradients 87 us; with the types looked up per element, divisions
+// of 64 bits and the gradient turned back a second time 77 and 112 us.
 #include "ag_internal.h"
 #include "launch.cuh"
 #include "linear_epilogue.cuh"
@@ -58,14 +61,16 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-__device__ __forceinline__ float load_one(const void *p, int64_t at, int dtype) {
+template <int T>
+__device__ __forceinline__ float load_one(const void *p, int64_t at) {
   float v[1];
-  load_values<1>(p, at, dtype, v);
+  load_values<1>(p, at, T, v);
   return v[0];
 }
-__device__ __forceinline__ void store_one(void *p, int64_t at, int dtype, float x) {
+template <int T>
+__device__ __forceinline__ void store_one(void *p, int64_t at, float x) {
   const float v[1] = {x};
-  store_values<1>(p, at, dtype, v);
+  store_values<1>(p, at, T, v);
 }
 
 // The pair member of element i and whether i is the second of its pair.
@@ -541,57 +546,66 @@ struct Row {
   int which, h, p;
   int64_t b, l;
 };
-__device__ __forceinline__ Row row_of(const QkArgs &a, int64_t p0, int t, int heads) {
+// (Positions and rows are below 2^31: the divisions are of 32 bits.)
+__device__ __forceinline__ Row row_of(const QkArgs &a, uint32_t p0, int t, int heads) {
   Row w;
-  w.p = t / heads;
+  w.p = static_cast<uint32_t>(t) / static_cast<uint32_t>(heads);
   w.h = t - w.p * heads;
   w.which = w.h >= a.side[0].H;
   if (w.which) w.h -= a.side[0].H;
-  w.b = (p0 + w.p) / a.L;
-  w.l = (p0 + w.p) - w.b * a.L;
+  const uint32_t pos = p0 + w.p, L = static_cast<uint32_t>(a.L);
+  w.b = pos / L;
+  w.l = pos % L;
   return w;
 }
+// Blocks to an SM.
+constexpr int kGeneralBlocks = 6;
+
 // A row into shared memory, four loads of a lane at a time on their way.
-__device__ __forceinline__ void load_row_to(float *row, const void *x, int64_t at, int D, int dtype,
+template <int T>
+__device__ __forceinline__ void load_row_to(float *row, const void *x, int64_t at, int D,
                                             int lane) {
   for (int i = lane; i < D; i += 128) {
     float v[4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) v[u] = i + 32 * u < D ? load_one(x, at + i + 32 * u, dtype) : 0.f;
+    for (int u = 0; u < 4; ++u) v[u] = i + 32 * u < D ? load_one<T>(x, at + i + 32 * u) : 0.f;
 #pragma unroll
     for (int u = 0; u < 4; ++u)
       if (i + 32 * u < D) row[i + 32 * u] = v[u];
   }
 }
 // The angles of np positions, by the whole block.
-__device__ __forceinline__ void block_angles(const QkArgs &a, float2 *cs, int64_t p0, int np,
+__device__ __forceinline__ void block_angles(const QkArgs &a, float2 *cs, uint32_t p0, int np,
                                              int half) {
+  const uint32_t L = static_cast<uint32_t>(a.L);
   for (int i = threadIdx.x; i < np * half; i += blockDim.x) {
-    const int64_t b = (p0 + i / half) / a.L, l = (p0 + i / half) % a.L;
-    cs[i] = turn(a.positions ? a.positions[b * a.pos_sb + l] : l, a.inv_freq[i % half]);
+    const uint32_t p = static_cast<uint32_t>(i) / static_cast<uint32_t>(half), pos = p0 + p;
+    const int64_t b = pos / L, l = pos % L;
+    cs[i] = turn(a.positions ? a.positions[b * a.pos_sb + l] : l, a.inv_freq[i - p * half]);
   }
 }
 
-__global__ void __launch_bounds__(kThreads) qk_fwd_kernel(const QkArgs a, int at_once) {
+template <int XT, int OT>
+__global__ void __launch_bounds__(kThreads, kGeneralBlocks) qk_fwd_kernel(const QkArgs a, int at_once) {
   extern __shared__ float smem[];
   begin_after_previous();
   const int half = a.R >> 1, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   float2 *cs = reinterpret_cast<float2 *>(smem);
   float *row = smem + 2 * at_once * half + warp * a.D;
-  const int64_t p0 = static_cast<int64_t>(blockIdx.x) * at_once;
+  const uint32_t p0 = blockIdx.x * at_once;
   const int np = static_cast<int>(min(static_cast<int64_t>(at_once), a.positions_total - p0));
   const int heads = a.side[0].H + a.side[1].H, rows = np * heads;
+  Row w;
   const auto load = [&](int t) {
-    const Row w = row_of(a, p0, t, heads);
+    w = row_of(a, p0, t, heads);
     const QkSide &s = a.side[w.which];
-    load_row_to(row, s.x, w.b * s.sb + w.l * s.sl + w.h * s.sh, a.D, a.x_dtype, lane);
+    load_row_to<XT>(row, s.x, w.b * s.sb + w.l * s.sl + w.h * s.sh, a.D, lane);
   };
   if (warp < rows) load(warp);  // (on its way while the angles are formed)
   block_angles(a, cs, p0, np, half);
   __syncthreads();
   for (int t = warp; t < rows; t += kWarps) {
     if (t != warp) load(t);
-    const Row w = row_of(a, p0, t, heads);
     const QkSide &s = a.side[w.which];
     float mean, r;
     row_stats(row, a.D, a.norm, a.eps, lane, mean, r);
@@ -610,7 +624,7 @@ __global__ void __launch_bounds__(kThreads) qk_fwd_kernel(const QkArgs a, int at
         const float2 c = cs[w.p * half + q.angle];
         v = fmaf(v, c.x, q.second ? row[q.other] * c.y : -row[q.other] * c.y);
       }
-      store_one(s.out, to + i, a.o_dtype, v);
+      store_one<OT>(s.out, to + i, v);
     }
     __syncwarp();
   }
@@ -620,25 +634,27 @@ __global__ void __launch_bounds__(kThreads) qk_fwd_kernel(const QkArgs a, int at
 // its own part of shared memory (element i always by lane i % 32: no atomics),
 // the block then adds its warps' in order and writes one partial per block;
 // qk_params_kernel adds those.
-__global__ void __launch_bounds__(kThreads) qk_bwd_kernel(const QkArgs a, int warps, int at_once) {
+template <int XT, int GT>
+__global__ void __launch_bounds__(kThreads, kGeneralBlocks) qk_bwd_kernel(const QkArgs a, int warps, int at_once) {
   extern __shared__ float smem[];
   begin_after_previous();
   const int half = a.R >> 1, warp = threadIdx.x / 32, lane = threadIdx.x % 32, D = a.D;
   float2 *cs = reinterpret_cast<float2 *>(smem);
-  float *row = smem + 2 * at_once * half + warp * 2 * D, *grad = row + D;
-  float *sums = smem + 2 * at_once * half + warps * 2 * D;  // [warps][2 sides][w, b][D]
+  float *row = smem + 2 * at_once * half + warp * 3 * D, *grad = row + D, *back = grad + D;
+  float *sums = smem + 2 * at_once * half + warps * 3 * D;  // [warps][2 sides][w, b][D]
   float *own = sums + warp * 4 * D;
   for (int i = lane; i < 4 * D; i += 32) own[i] = 0.f;
   const int heads = a.side[0].H + a.side[1].H;
-  for (int64_t p0 = static_cast<int64_t>(blockIdx.x) * at_once; p0 < a.positions_total;
-       p0 += static_cast<int64_t>(gridDim.x) * at_once) {
+  // (positions_total < 2^31 and a grid's turn is below 2^16: p0 stays in 32 bits)
+  for (uint32_t p0 = blockIdx.x * at_once; p0 < a.positions_total; p0 += gridDim.x * at_once) {
     const int np = static_cast<int>(min(static_cast<int64_t>(at_once), a.positions_total - p0));
     const int rows = np * heads;
+    Row w;
     const auto load = [&](int t) {
-      const Row w = row_of(a, p0, t, heads);
+      w = row_of(a, p0, t, heads);
       const QkSide &s = a.side[w.which];
-      load_row_to(row, s.x, w.b * s.sb + w.l * s.sl + w.h * s.sh, D, a.x_dtype, lane);
-      load_row_to(grad, s.g, ((w.b * s.H + w.h) * a.L + w.l) * D, D, a.o_dtype, lane);
+      load_row_to<XT>(row, s.x, w.b * s.sb + w.l * s.sl + w.h * s.sh, D, lane);
+      load_row_to<GT>(grad, s.g, ((w.b * s.H + w.h) * a.L + w.l) * D, D, lane);
     };
     if (warp < rows) load(warp);  // (on its way while the angles are formed)
     __syncthreads();              // the angles of the turn before are no longer read
@@ -646,7 +662,6 @@ __global__ void __launch_bounds__(kThreads) qk_bwd_kernel(const QkArgs a, int wa
     __syncthreads();
     for (int t = warp; t < rows; t += warps) {
       if (t != warp) load(t);
-      const Row w = row_of(a, p0, t, heads);
       const QkSide &s = a.side[w.which];
       float mean, r;
       row_stats(row, D, a.norm, a.eps, lane, mean, r);
@@ -660,25 +675,17 @@ __global__ void __launch_bounds__(kThreads) qk_bwd_kernel(const QkArgs a, int wa
           g = fmaf(g, c.x, q.second ? -grad[q.other] * c.y : grad[q.other] * c.y);
         }
         const float n = (row[i] - mean) * r;
-        own[w.which * 2 * D + i] += g * n;
-        own[w.which * 2 * D + D + i] += g;
+        if (a.partial) own[w.which * 2 * D + i] += g * n, own[w.which * 2 * D + D + i] += g;
         const float d = s.w ? g * s.w[i] : g;
+        row[i] = n, back[i] = d;  // (an element stays with its lane)
         along = fmaf(d, n, along);
         total += d;
       }
       along = a.norm == AG_NORM_NONE ? 0.f : warp_sum(along) / D;
       total = a.norm == AG_NORM_LAYER ? warp_sum(total) / D : 0.f;
       const int64_t to = w.b * s.dxb + w.l * s.dxl + w.h * s.dxh;
-      for (int i = lane; i < D; i += 32) {
-        float g = grad[i];
-        if (i < a.R) {
-          const Pair q = pair_of(i, a.R, a.rope);
-          const float2 c = cs[w.p * half + q.angle];
-          g = fmaf(g, c.x, q.second ? -grad[q.other] * c.y : grad[q.other] * c.y);
-        }
-        const float n = (row[i] - mean) * r, d = s.w ? g * s.w[i] : g;
-        store_one(s.dx, to + i, a.x_dtype, r * (d - n * along - total));
-      }
+      for (int i = lane; i < D; i += 32)
+        store_one<XT>(s.dx, to + i, r * (back[i] - row[i] * along - total));
       __syncwarp();
     }
   }
@@ -751,12 +758,12 @@ int64_t rows_blocks(int64_t total, int D, int chunks, int num_sms) {
   return blocks_for(total, kWarps * (D <= 64 ? 4 : D <= 128 ? 2 : 1), 2 * num_sms / chunks);
 }
 int64_t general_blocks(int64_t total, int heads, int num_sms) {
-  return blocks_for(total, positions_at_once(heads), 6 * num_sms);
+  return blocks_for(total, positions_at_once(heads), kGeneralBlocks * num_sms);
 }
 
 // The most that the general kernels take: angles of 8 positions of 1024 elements,
-// and six rows of 1024 for each of 4 warps (of 512 for 8).
-constexpr int kMostSmem = (8 * 1024 + 6 * 4 * 1024) * 4;
+// and seven rows of 1024 for each of 4 warps (of 512 for 8).
+constexpr int kMostSmem = (8 * 1024 + 7 * 4 * 1024) * 4;
 // Always the same limit: a call's own would be taken back by a smaller call of
 // another thread before its launch.
 cudaError_t allow_smem(const void *kernel, size_t bytes) {
@@ -807,6 +814,20 @@ QkKernel rows_kernel(const QkArgs &a, bool backward) {
   return a.rope == AG_ROPE_HALVES ? rows_kernel<true>(a, backward) : rows_kernel<false>(a, backward);
 }
 
+// The general kernels by type.
+template <int XT>
+void (*general_fwd(const QkArgs &a))(QkArgs, int) {
+  return a.o_dtype == AG_F32    ? qk_fwd_kernel<XT, AG_F32>
+         : a.o_dtype == AG_BF16 ? qk_fwd_kernel<XT, AG_BF16>
+                                : qk_fwd_kernel<XT, AG_F16>;
+}
+template <int XT>
+void (*general_bwd(const QkArgs &a))(QkArgs, int, int) {
+  return a.o_dtype == AG_F32    ? qk_bwd_kernel<XT, AG_F32>
+         : a.o_dtype == AG_BF16 ? qk_bwd_kernel<XT, AG_BF16>
+                                : qk_bwd_kernel<XT, AG_F16>;
+}
+
 }  // namespace
 
 cudaError_t launch_qk_fwd(const QkArgs &a, int num_sms, cudaStream_t stream) {
@@ -822,10 +843,13 @@ cudaError_t launch_qk_fwd(const QkArgs &a, int num_sms, cudaStream_t stream) {
   }
   const int at_once = positions_at_once(a.side[0].H + a.side[1].H);
   const size_t smem = (static_cast<size_t>(at_once) * a.R + kWarps * static_cast<size_t>(a.D)) * 4;
-  cudaError_t e = allow_smem(reinterpret_cast<const void *>(qk_fwd_kernel), smem);
+  const auto kernel = a.x_dtype == AG_F32    ? general_fwd<AG_F32>(a)
+                      : a.x_dtype == AG_BF16 ? general_fwd<AG_BF16>(a)
+                                             : general_fwd<AG_F16>(a);
+  cudaError_t e = allow_smem(reinterpret_cast<const void *>(kernel), smem);
   if (e != cudaSuccess) return e;
   const int64_t blocks = (a.positions_total + at_once - 1) / at_once;
-  return launch_after_previous(qk_fwd_kernel, static_cast<unsigned>(blocks), kThreads, smem, stream,
+  return launch_after_previous(kernel, static_cast<unsigned>(blocks), kThreads, smem, stream,
                                a, at_once);
 }
 
@@ -846,10 +870,13 @@ cudaError_t launch_qk_bwd(const QkArgs &a, int num_sms, cudaStream_t stream) {
     const int warps = bwd_warps(a.D), at_once = positions_at_once(heads);
     const int blocks = static_cast<int>(general_blocks(a.positions_total, heads, num_sms));
     const size_t smem =
-        (static_cast<size_t>(at_once) * a.R + warps * 6 * static_cast<size_t>(a.D)) * 4;
-    e = allow_smem(reinterpret_cast<const void *>(qk_bwd_kernel), smem);
+        (static_cast<size_t>(at_once) * a.R + warps * 7 * static_cast<size_t>(a.D)) * 4;
+    const auto kernel = a.x_dtype == AG_F32    ? general_bwd<AG_F32>(a)
+                        : a.x_dtype == AG_BF16 ? general_bwd<AG_BF16>(a)
+                                               : general_bwd<AG_F16>(a);
+    e = allow_smem(reinterpret_cast<const void *>(kernel), smem);
     if (e != cudaSuccess) return e;
-    e = launch_after_previous(qk_bwd_kernel, blocks, warps * 32, smem, stream, a, warps, at_once);
+    e = launch_after_previous(kernel, blocks, warps * 32, smem, stream, a, warps, at_once);
     p.first[0] = 0, p.first[1] = 2 * a.D;
     p.count[0] = p.count[1] = blocks;
     p.step = 4 * a.D;
