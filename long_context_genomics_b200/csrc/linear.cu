@@ -70,7 +70,8 @@ PairPlan plan_pair(int64_t M, int64_t N, int64_t K, int clusters) {
       const int from = static_cast<int>(dW_tiles * splits % clusters), few = clusters - from;
       // The clusters without an item in dW's last round can be so many rounds of
       // dx ahead.
-      const int most = from > 0 ? static_cast<int>(dW_item / dx_item) + 1 : 0;
+      const int64_t ahead = from > 0 ? static_cast<int64_t>(dW_item / dx_item) + 1 : 0,
+                    all_dx = (dx_items + few - 1) / few, most = ahead < all_dx ? ahead : all_dx;
       for (int extra = 0; extra <= most && extra <= 64; ++extra) {
         const int64_t left = dx_items - static_cast<int64_t>(extra) * few;
         const int64_t more = left > 0 ? (left + clusters - 1) / clusters : 0;
