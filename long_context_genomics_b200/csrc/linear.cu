@@ -87,13 +87,43 @@ PairPlan plan_pair(int64_t M, int64_t N, int64_t K, int clusters) {
 }
 
 // --------------------------------------------------------------------------
+// db from the partial sums of dy's columns [parts][N] (column_sum_kernel): 32
+// columns a block, its warps over the parts, all in a fixed order.
+struct ColumnParts {
+  const float *partial;
+  int parts;
+  int64_t N;
+  float *db;
+  __host__ unsigned blocks() const { return db ? static_cast<unsigned>((N + 31) / 32) : 0; }
+};
+__device__ __forceinline__ void join_columns(const ColumnParts &c, unsigned block) {
+  __shared__ float sums[8][32];
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int64_t n = static_cast<int64_t>(block) * 32 + lane;
+  float s = 0.f;
+  if (n < c.N)
+    for (int i = warp; i < c.parts; i += 8) s += c.partial[i * c.N + n];
+  sums[warp][lane] = s;
+  __syncthreads();
+  if (warp == 0 && n < c.N) {
+#pragma unroll
+    for (int w = 1; w < 8; ++w) s += sums[w][lane];
+    c.db[n] = s;
+  }
+}
+
 // C from its partial sums: V columns of a row per thread, the parts added in
-// order.
+// order.  The blocks behind the first `blocks` join db's parts, where there are
+// some (one launch less: 2 us of a layer's gradients).
 template <int V>
 __global__ void __launch_bounds__(256)
     linear_join_kernel(const float *__restrict__ partial, int splits, int64_t M, int64_t N,
-                       int64_t ld, const LinearEpilogue e) {
+                       int64_t ld, const LinearEpilogue e, unsigned blocks, const ColumnParts c) {
   begin_after_previous();
+  if (blockIdx.x >= blocks) {
+    join_columns(c, blockIdx.x - blocks);
+    return;
+  }
   const int64_t per_row = (N + V - 1) / V;
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   if (i >= M * per_row) return;
@@ -172,23 +202,9 @@ __global__ void __launch_bounds__(256)
     if (n < N) out[blockIdx.y * N + n] = t;
   }
 }
-__global__ void __launch_bounds__(256)
-    column_join_kernel(const float *__restrict__ partial, int parts, int64_t N,
-                       float *__restrict__ db) {
-  __shared__ float sums[8][32];
+__global__ void __launch_bounds__(256) column_join_kernel(const ColumnParts c) {
   begin_after_previous();
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const int64_t n = static_cast<int64_t>(blockIdx.x) * 32 + lane;
-  float s = 0.f;
-  if (n < N)
-    for (int i = warp; i < parts; i += 8) s += partial[i * N + n];
-  sums[warp][lane] = s;
-  __syncthreads();
-  if (warp == 0 && n < N) {
-#pragma unroll
-    for (int w = 1; w < 8; ++w) s += sums[w][lane];
-    db[n] = s;
-  }
+  join_columns(c, blockIdx.x);
 }
 
 // --------------------------------------------------------------------------
@@ -327,18 +343,15 @@ int64_t partial_bytes(const GemmPlan &plan, int64_t M, int64_t N) {
   return plan.splits > 1 ? plan.splits * M * partial_ld(N) * 4 : 0;
 }
 
-// The joining of a product's parts.
-cudaError_t join(const Gemm &g) {
+// The joining of a product's parts, and of db's.
+cudaError_t join(const Gemm &g, const ColumnParts &c) {
   if (g.plan.splits == 1) return cudaSuccess;
   const int v = g.epi.vec8 ? 8 : 1;
-  const int64_t blocks = (g.M * ((g.N + v - 1) / v) + 255) / 256;  // at most 2^38 / 256
+  const unsigned blocks =  // at most 2^38 / 256
+      static_cast<unsigned>((g.M * ((g.N + v - 1) / v) + 255) / 256);
   return launch_after_previous(v == 8 ? linear_join_kernel<8> : linear_join_kernel<1>,
-                               static_cast<unsigned>(blocks), 256, 0, g.stream, g.partial,
-                               g.plan.splits, g.M, g.N, partial_ld(g.N), g.epi);
-}
-cudaError_t run(const Gemm &g) {
-  const cudaError_t e = launch_gemm(g);
-  return e == cudaSuccess ? join(g) : e;
+                               blocks + c.blocks(), 256, 0, g.stream, g.partial, g.plan.splits, g.M,
+                               g.N, partial_ld(g.N), g.epi, blocks, c);
 }
 
 struct FwdLayout {
@@ -369,7 +382,8 @@ struct BwdLayout {
   GemmPlan dx_plan, dW_plan;
   PairPlan pair;
   bool paired;
-  float *partial;  // of dx, then of dW, then of db
+  float *partial;     // of dx, then of dW
+  float *db_partial;
   int db_parts;
   bool db_vec;
 };
@@ -398,8 +412,7 @@ BwdLayout bwd_layout(const LinearBwd &a, Workspace &ws) {
   if (a.db) {
     l.db_vec = a.N % 8 == 0 && tma_readable(a.dy, a.lddy);
     l.db_parts = column_parts(a.M, a.N, l.db_vec, a.num_sms);
-    const int64_t b = l.db_parts > 1 ? l.db_parts * a.N * 4 : 0;
-    partial = b > partial ? b : partial;
+    l.db_partial = static_cast<float *>(ws.take(l.db_parts > 1 ? l.db_parts * a.N * 4 : 0));
   }
   l.partial = static_cast<float *>(ws.take(partial));
   return l;
@@ -425,11 +438,12 @@ cudaError_t launch_linear_fwd(const LinearFwd &a) {
   Copies copies{};
   note(copies, l.x, a.x, a.ldx);
   note(copies, l.W, a.W, a.ldw);
-  const cudaError_t e = make(copies, a.num_sms, a.stream);
+  cudaError_t e = make(copies, a.num_sms, a.stream);
   if (e != cudaSuccess) return e;
-  Gemm g{l.x.op, l.W.op, false, false, a.M, a.N, a.K, l.plan, l.partial, a.epi,
+  const Gemm g{l.x.op, l.W.op, false, false, a.M, a.N, a.K, l.plan, l.partial, a.epi,
          a.num_sms, a.err, a.encode, a.stream};
-  return run(g);
+  e = launch_gemm(g);
+  return e == cudaSuccess ? join(g, ColumnParts{}) : e;
 }
 
 cudaError_t linear_bwd_workspace(const LinearBwd &a, int64_t *bytes) {
@@ -456,22 +470,27 @@ cudaError_t launch_linear_bwd(const LinearBwd &a) {
     Gemm one = dx, two = dW;
     one.plan = {l.pair.bn, 1, 0}, two.plan = {l.pair.bn, l.pair.splits, 0};
     e = launch_gemm_pair(two, one, l.pair.turns, &done);
-    if (e == cudaSuccess && done) e = join(two);
+    if (done) dW.plan = two.plan;
   }
-  if (e == cudaSuccess && a.dx.out && !done) e = run(dx);
-  if (e == cudaSuccess && a.dW.out && !done) e = run(dW);
+  if (e == cudaSuccess && a.dx.out && !done) {
+    e = launch_gemm(dx);
+    if (e == cudaSuccess) e = join(dx, ColumnParts{});
+  }
+  if (e == cudaSuccess && a.dW.out && !done) e = launch_gemm(dW);
+  // db's parts behind the products, which leave dy in L2 (in front of them 0.6 to
+  // 1.6 us slower with cold operands), and joined in one launch with dW's.
+  ColumnParts c{};
   if (e == cudaSuccess && a.db) {
     const int cols = l.db_vec ? 256 : 32;
     const dim3 grid(static_cast<unsigned>((a.N + cols - 1) / cols), l.db_parts);
-    float *to = l.db_parts > 1 ? l.partial : a.db;
     e = launch_after_previous(l.db_vec ? column_sum_kernel<8> : column_sum_kernel<1>, grid, 256, 0,
                               a.stream, static_cast<const uint16_t *>(a.dy), a.lddy, a.M, a.N,
-                              a.dx.dtype, l.db_parts, to);
-    if (e == cudaSuccess && l.db_parts > 1)
-      e = launch_after_previous(column_join_kernel, static_cast<unsigned>((a.N + 31) / 32), 256, 0,
-                                a.stream, l.partial, l.db_parts, a.N, a.db);
+                              a.dx.dtype, l.db_parts, l.db_parts > 1 ? l.db_partial : a.db);
+    if (l.db_parts > 1) c = {l.db_partial, l.db_parts, a.N, a.db};
   }
-  return e;
+  if (e != cudaSuccess) return e;
+  if (a.dW.out && dW.plan.splits > 1) return join(dW, c);
+  return c.db ? launch_after_previous(column_join_kernel, c.blocks(), 256, 0, a.stream, c) : e;
 }
 
 }  // namespace ag
