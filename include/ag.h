@@ -498,9 +498,12 @@ ag_status ag_qk_norm_rope_fwd(const void *q, int64_t q_sb, int64_t q_sl, int64_t
  *   q ... D as ag_qk_norm_rope_fwd (the biases have no part in the gradients)
  *   dq [B, L, Hq, D] x_dtype with element strides dq_sb, dq_sl, dq_sh and dk
  *      likewise (written).  No two elements of dq (of dk) may share an
- *      address (AG_ERR_SHAPE).  dq and dk may lie side by side in the same
- *      rows (a fused projection's gradient); otherwise no output may overlap
- *      an input or another output (AG_ERR_ALIAS).
+ *      address (AG_ERR_SHAPE).  dq and dk may lie in one buffer, side by side
+ *      or each between the other's heads (a fused projection's gradient), as
+ *      long as they share no element; otherwise no output may overlap an
+ *      input or another output (AG_ERR_ALIAS).  Where they interleave with
+ *      strides so unlike that more than 4096 pairs of their slices would
+ *      have to be compared, they count as sharing one.
  *   dq_weight, dq_bias, dk_weight, dk_bias [D] float32 (written), each NULL:
  *      not wanted.  With B == 0 or L == 0, or for a side without heads, they
  *      are written as zeros.

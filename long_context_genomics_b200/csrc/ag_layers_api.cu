@@ -303,24 +303,61 @@ bool heads_overlap(const Heads &a, const Heads &b) {
   return overlap(a.p, a.bytes(), b.p, b.bytes());
 }
 
-// Two outputs that may lie side by side in the rows of one buffer: the same
-// strides over b and l, each position's heads of one in front of the other's,
-// and both within the position's stride.
+// Dimensions of more than one index, from the largest stride down.
+struct Dims {
+  int n = 0;
+  int64_t count[3], stride[3];
+  explicit Dims(const Heads &h) {
+    for (int i = 0; i < 3; ++i) {
+      if (h.n[i] == 1) continue;
+      int at = n++;
+      for (; at > 0 && stride[at - 1] < h.s[i]; --at)
+        count[at] = count[at - 1], stride[at] = stride[at - 1];
+      count[at] = h.n[i], stride[at] = h.s[i];
+    }
+  }
+  // Elements from the first to the last that the dimensions from `from` on span.
+  int64_t extent(int from, int64_t D) const {
+    int64_t e = D;
+    for (int i = from; i < n; ++i) e += (count[i] - 1) * stride[i];
+    return e;
+  }
+};
+
+// The most pairs of slices of two outputs that are compared.
+constexpr int kMostPairs = 4096;
+
+// Whether the runs of D elements of a (dimensions from ia on, starting at 0) and
+// of b (from ib on, starting at `gap`) share no element.  Both step over what lies
+// inside a dimension (distinct), so of two dimensions with one stride only
+// neighbouring slices can meet.  Unequal strides where more than `left` pairs of
+// slices might meet count as sharing one.
+bool apart(const Dims &a, int ia, const Dims &b, int ib, int64_t gap, int64_t D, int &left) {
+  if (left-- <= 0) return false;
+  if (gap >= a.extent(ia, D) || gap + b.extent(ib, D) <= 0) return true;
+  const bool in_a = ia < a.n, in_b = ib < b.n;
+  if (!in_a && !in_b) return false;
+  const bool both = in_a && in_b && a.stride[ia] == b.stride[ib];
+  const bool step_a = both || (in_a && (!in_b || a.stride[ia] > b.stride[ib]));
+  const int na = ia + (step_a ? 1 : 0), nb = ib + (both || !step_a ? 1 : 0);
+  const int64_t s = step_a ? a.stride[ia] : b.stride[ib];
+  // b's slice j against a's slice i lies k = j - i strides further.
+  const int64_t first = step_a ? 1 - a.count[ia] : 0, last = nb > ib ? b.count[ib] - 1 : 0;
+  int64_t from = (-b.extent(nb, D) - gap) / s, to = (a.extent(na, D) - gap) / s;
+  from = from - 1 > first ? from - 1 : first, to = to + 1 < last ? to + 1 : last;
+  for (int64_t k = from; k <= to; ++k)
+    if (!apart(a, na, b, nb, gap + k * s, D, left)) return false;
+  return true;
+}
+
+// Two outputs may lie between each other's heads or rows in one buffer, as the
+// slices of a fused projection's gradient do, but not share an element.
 bool outputs_overlap(const Heads &a, const Heads &b) {
   if (!heads_overlap(a, b)) return false;
-  if (a.s[0] != b.s[0] || a.s[1] != b.s[1] || a.size != b.size) return true;
-  const Heads &lo = a.p <= b.p ? a : b, &hi = a.p <= b.p ? b : a;
-  const int64_t gap_bytes = static_cast<int64_t>(reinterpret_cast<uintptr_t>(hi.p) -
-                                                 reinterpret_cast<uintptr_t>(lo.p));
-  if (gap_bytes % a.size) return true;
-  const int64_t gap = gap_bytes / a.size;
-  const int64_t of_lo = (lo.n[2] - 1) * lo.s[2] + lo.D, of_hi = (hi.n[2] - 1) * hi.s[2] + hi.D;
-  if (gap < of_lo) return true;
-  const int64_t end = gap + of_hi;  // of both, from the position's first element
-  const bool l_steps_over = lo.n[1] == 1 || lo.s[1] >= end;
-  const int64_t row = lo.n[1] == 1 ? end : (lo.n[1] - 1) * lo.s[1] + end;
-  const bool b_steps_over = lo.n[0] == 1 || lo.s[0] >= row;
-  return !(l_steps_over && b_steps_over);
+  const int64_t gap = reinterpret_cast<intptr_t>(b.p) - reinterpret_cast<intptr_t>(a.p);
+  if (gap % a.size) return true;
+  int left = kMostPairs;
+  return !apart(Dims(a), 0, Dims(b), 0, gap / a.size, a.D, left);
 }
 
 // Size and value checks shared by the two directions.

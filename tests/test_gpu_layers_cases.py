@@ -1,0 +1,47 @@
+"""More cases of the layers around the attention on a B200: layouts, sizes and
+sums that test_gpu_layers.py does not reach.  Tolerances as derived there, or
+beside the test."""
+import math
+
+import pytest
+import torch
+
+import layers_reference as ref
+from test_gpu_layers import (BF16, F16, F32, _close, _gen, _half_step, _ok, _randn,  # noqa: F401
+                             ag)
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------------------
+# Queries and keys: gradients into every layout of one buffer
+def _fused(layout, B, L, D, fill):
+    """A buffer and its query and key slices [B, L, H, D]."""
+    t = lambda *s: torch.full(s, fill, dtype=BF16, device="cuda")  # noqa: E731
+    if layout == "side by side":
+        buf = t(B, L, 9 * D + 64)
+        return buf, buf[..., :8 * D].view(B, L, 8, D), buf[..., 8 * D:9 * D].view(B, L, 1, D)
+    if layout == "interleaved":  # each head's query, key and value together
+        buf = t(B, L, 4, 3, D)
+        return buf, buf[:, :, :, 0], buf[:, :, :, 1]
+    buf = t(B, 10, L, D)         # the attention's own order
+    return buf, buf[:, :8].transpose(1, 2), buf[:, 8:9].transpose(1, 2)
+
+
+@pytest.mark.parametrize("layout", ["side by side", "interleaved", "heads first"])
+@pytest.mark.parametrize("D", [128, 100])
+@pytest.mark.parametrize("B,L", [(2, 1), (1, 1), (1, 9), (2, 13)])
+def test_qk_bwd_into_one_buffer_of_any_layout(ag, B, L, D, layout):
+    """The same values as into tensors of their own; what lies beside stays."""
+    g = _gen(B + 7 * L + D)
+    src, q, k = _fused(layout, B, L, D, 0.0)
+    src.copy_(_randn(g, *src.shape, dtype=BF16))
+    gq, gk = (_randn(g, B, t.shape[2], L, D) for t in (q, k))
+    kw = dict(inv_freq=ag.ag_rope_frequencies(D))
+    want = ag.ag_qk_norm_rope_bwd(gq, gk, q, k, **kw)
+    buf, dq, dk = _fused(layout, B, L, D, 7.0)
+    ag.ag_qk_norm_rope_bwd(gq, gk, q, k, dq=dq, dk=dk, **kw)
+    _ok(ag)
+    assert torch.equal(dq, want[0]) and torch.equal(dk, want[1])
+    dq.fill_(7.0), dk.fill_(7.0)
+    assert bool((buf == 7.0).all()), "wrote beside the gradients"

@@ -245,3 +245,73 @@ def test_binding_refusals(ag):
     f = ag.ag_rope_frequencies(8, base=100.0, device="cpu")
     assert f.dtype == torch.float64
     assert torch.allclose(f, torch.tensor([1.0, 100 ** -0.25, 0.1, 100 ** -0.75]).double())
+
+
+def _elements(at, n, s, D):
+    i = torch.arange(D) + at
+    for count, stride in zip(n, s):
+        i = (i[None] + torch.arange(count)[:, None] * stride).flatten()
+    return set(i.tolist())
+
+
+SIDE_BY_SIDE = {
+    # One position in each of two sequences: the slices' views give the length of
+    # one another strides (a view of a dimension of one element may have any).
+    "one position": dict(L=1, dq_sb=1152, dq_sl=1024, dk_sb=1152, dk_sl=1152),
+    "one sequence": dict(B=1, dq_sb=1024, dk_sb=9 * 128 * 7),
+    "one of both": dict(B=1, L=1, dq_sb=1024, dq_sl=1024, dk_sb=128, dk_sl=128),
+    # [B, L, H, 3, D]: each head's query, key and value together.
+    "interleaved heads": dict(Hk=8, dq_sb=7 * 3072, dq_sl=3072, dq_sh=384, dk_sb=7 * 3072,
+                              dk_sl=3072, dk_sh=384, dk=_p(5) + 256),
+    # [B, 9, L, D]: the attention's own order, the keys behind the queries.
+    "heads before positions": dict(dq_sb=9 * 7 * 128, dq_sl=128, dq_sh=7 * 128, dk_sb=9 * 7 * 128,
+                                   dk_sl=128, dk_sh=7 * 128, dk=_p(5) + 8 * 7 * 256),
+    # [B, L, Hk, 1 + 1, D] with the keys first.
+    "keys first": dict(Hq=4, Hk=4, dk=_p(5), dq=_p(5) + 256, dq_sb=7 * 1024, dq_sl=1024, dq_sh=256,
+                       dk_sb=7 * 1024, dk_sl=1024, dk_sh=256),
+}
+
+
+@pytest.mark.parametrize("layout", SIDE_BY_SIDE)
+def test_qk_bwd_takes_gradients_of_any_fused_layout(ag, layout):
+    kw = SIDE_BY_SIDE[layout]
+    if torch.cuda.is_available():
+        pytest.skip("would launch")
+    assert _qk_bwd(ag, **kw) in (UNSUPPORTED, CUDA)
+
+
+def test_qk_bwd_refuses_shared_elements_exactly(ag):
+    """Small layouts of every order against the sets of their elements."""
+    if torch.cuda.is_available():
+        pytest.skip("would launch")
+    import itertools
+    import random
+
+    rng = random.Random(5)
+    B, L, D, seen = 2, 3, 4, [0, 0]
+    for _ in range(3000):
+        heads = [rng.choice([1, 2]), rng.choice([1, 2])]
+        strides = []
+        for H in heads:
+            n, s, inner = (B, L, H), [0, 0, 0], D
+            for i in rng.choice(list(itertools.permutations(range(3)))):
+                s[i] = inner + rng.choice([0, 0, 4, 4, 8, 24])
+                inner = s[i] * (n[i] - 1) + inner if rng.random() < 0.5 else s[i] * n[i]
+            strides.append(s)
+        if rng.random() < 0.6:
+            strides[1] = strides[0]
+        at = rng.randrange(0, 200, 4) - 100
+        a = _elements(0, (B, L, heads[0]), strides[0], D)
+        b = _elements(at, (B, L, heads[1]), strides[1], D)
+        if len(a) != B * L * heads[0] * D or len(b) != B * L * heads[1] * D:
+            continue
+        q, k = strides
+        st = _qk_bwd(ag, B=B, L=L, Hq=heads[0], Hk=heads[1], D=D, R=4, pos_sb=L, dq=_p(5),
+                     dq_sb=q[0], dq_sl=q[1], dq_sh=q[2], dk=_p(5) + 2 * at, dk_sb=k[0], dk_sl=k[1],
+                     dk_sh=k[2])
+        if st == SHAPE:  # (distinct, but not by steps over what lies inside)
+            continue
+        shared = bool(a & b)
+        assert st == ALIAS if shared else st in (UNSUPPORTED, CUDA), (q, k, at, heads)
+        seen[shared] += 1
+    assert min(seen) > 200
