@@ -380,8 +380,8 @@ typedef enum {
  * truncates rather than rounds (see linear_sm100.cu).
  * M >= 0 (M == 0 is a no-op), N, K >= 1 (AG_ERR_SHAPE), and a row stride not
  * below its row (AG_ERR_SHAPE); M <= 2^26, N, K <= 2^20, M N, M K and N K <=
- * 2^38, every stride <= 2^28 (AG_ERR_UNSUPPORTED); an unknown dtype, y_dtype or
- * act is AG_ERR_VALUE.
+ * 2^38, every stride of more than one row <= 2^28 (AG_ERR_UNSUPPORTED); an
+ * unknown dtype, y_dtype or act is AG_ERR_VALUE.
  * Pointers aligned to their element; rows whose start is not 16-byte aligned
  * (odd sizes, strides or offsets) cost a copy of that matrix into the
  * workspace.  The outputs may not overlap an input or each other

@@ -38,9 +38,12 @@ bool mats_overlap(const Mat &a, const Mat &b) {
   return !(d >= a.row_bytes() && d + b.row_bytes() <= ld);
 }
 
-// Row strides: at least the row, at most kMaxStride.
-ag_status check_ld(int64_t ld, int64_t cols) {
+// Row strides: at least the row, at most kMaxStride.  Of one row the stride is
+// never used, so any will do (the last position of a long sequence, say): a
+// longer one becomes a plain one.
+ag_status check_ld(int64_t &ld, int64_t rows, int64_t cols) {
   if (ld < cols) return AG_ERR_SHAPE;
+  if (ld > kMaxStride && rows <= 1) ld = (cols + 7) / 8 * 8;
   return ld > kMaxStride ? AG_ERR_UNSUPPORTED : AG_OK;
 }
 
@@ -81,8 +84,8 @@ ag_status ag_linear_fwd_workspace(const void *x, int64_t ldx, const void *W, int
                                   int64_t M, int64_t N, int64_t K, int64_t *bytes) {
   if (!bytes) return AG_ERR_NULL;
   ag_status st = ag::check_linear_sizes(M, N, K);
-  if (st == AG_OK) st = ag::check_ld(ldx, K);
-  if (st == AG_OK) st = ag::check_ld(ldw, K);
+  if (st == AG_OK) st = ag::check_ld(ldx, M, K);
+  if (st == AG_OK) st = ag::check_ld(ldw, N, K);
   if (st != AG_OK) return st;
   *bytes = 0;
   if (M == 0) return AG_OK;
@@ -101,11 +104,11 @@ ag_status ag_linear_fwd(const void *x, int64_t ldx, const void *W, int64_t ldw,
                         void *y, int64_t ldy, int y_dtype, void *workspace,
                         int64_t workspace_bytes, void *stream) {
   ag_status st = ag::check_linear_sizes(M, N, K);
-  if (st == AG_OK) st = ag::check_ld(ldx, K);
-  if (st == AG_OK) st = ag::check_ld(ldw, K);
-  if (st == AG_OK) st = ag::check_ld(ldy, N);
-  if (st == AG_OK && residual) st = ag::check_ld(ldr, N);
-  if (st == AG_OK && preact) st = ag::check_ld(ldz, N);
+  if (st == AG_OK) st = ag::check_ld(ldx, M, K);
+  if (st == AG_OK) st = ag::check_ld(ldw, N, K);
+  if (st == AG_OK) st = ag::check_ld(ldy, M, N);
+  if (st == AG_OK && residual) st = ag::check_ld(ldr, M, N);
+  if (st == AG_OK && preact) st = ag::check_ld(ldz, M, N);
   if (st != AG_OK) return st;
   if (!ag::is_half(dtype) || (y_dtype != dtype && y_dtype != AG_F32) || act < AG_ACT_NONE ||
       act > AG_ACT_SILU)
@@ -156,9 +159,9 @@ ag_status ag_linear_bwd_workspace(const void *dy, int64_t lddy, const void *x, i
                                   int64_t *bytes) {
   if (!bytes) return AG_ERR_NULL;
   ag_status st = ag::check_linear_sizes(M, N, K);
-  if (st == AG_OK) st = ag::check_ld(lddy, N);
-  if (st == AG_OK && dW) st = ag::check_ld(ldx, K);
-  if (st == AG_OK && dx) st = ag::check_ld(ldw, K);
+  if (st == AG_OK) st = ag::check_ld(lddy, M, N);
+  if (st == AG_OK && dW) st = ag::check_ld(ldx, M, K);
+  if (st == AG_OK && dx) st = ag::check_ld(ldw, N, K);
   if (st != AG_OK) return st;
   *bytes = 0;
   if (M == 0) return AG_OK;
@@ -180,12 +183,12 @@ ag_status ag_linear_bwd(const void *dy, int64_t lddy, const void *x, int64_t ldx
                         int dx_dtype, void *dW, int64_t lddw, int dW_dtype, float *db,
                         void *workspace, int64_t workspace_bytes, void *stream) {
   ag_status st = ag::check_linear_sizes(M, N, K);
-  if (st == AG_OK) st = ag::check_ld(lddy, N);
-  if (st == AG_OK && dW) st = ag::check_ld(ldx, K);
-  if (st == AG_OK && dW) st = ag::check_ld(lddw, K);
-  if (st == AG_OK && dx) st = ag::check_ld(ldw, K);
-  if (st == AG_OK && dx) st = ag::check_ld(lddx, K);
-  if (st == AG_OK && dx && preact) st = ag::check_ld(ldz, K);
+  if (st == AG_OK) st = ag::check_ld(lddy, M, N);
+  if (st == AG_OK && dW) st = ag::check_ld(ldx, M, K);
+  if (st == AG_OK && dW) st = ag::check_ld(lddw, N, K);
+  if (st == AG_OK && dx) st = ag::check_ld(ldw, N, K);
+  if (st == AG_OK && dx) st = ag::check_ld(lddx, M, K);
+  if (st == AG_OK && dx && preact) st = ag::check_ld(ldz, M, K);
   if (st != AG_OK) return st;
   if (!ag::is_half(dtype) || act < AG_ACT_NONE || act > AG_ACT_SILU ||
       (dx && dx_dtype != dtype && dx_dtype != AG_F32) ||

@@ -45,3 +45,27 @@ def test_qk_bwd_into_one_buffer_of_any_layout(ag, B, L, D, layout):
     assert torch.equal(dq, want[0]) and torch.equal(dk, want[1])
     dq.fill_(7.0), dk.fill_(7.0)
     assert bool((buf == 7.0).all()), "wrote beside the gradients"
+
+
+# ---------------------------------------------------------------------------
+# Linear layers
+@pytest.mark.parametrize("K", [64, 37])
+@pytest.mark.parametrize("far", [1 << 29, (1 << 40) + 1])
+def test_linear_one_row_of_any_stride(ag, far, K):
+    """The last position of a long sequence: one row, whose stride is never used."""
+    g, N = _gen(K), 40
+    one = lambda n: torch.as_strided(torch.zeros(n, dtype=BF16, device="cuda"), (1, n), (far, 1))  # noqa: E731
+    x, r, y, z, dy, dx = (one(n) for n in (K, N, N, N, N, K))
+    for t in (x, r, dy):
+        t.copy_(_randn(g, *t.shape, dtype=BF16))
+    W = _randn(g, N, K, dtype=BF16)
+    plain = [t.clone(memory_format=torch.contiguous_format) for t in (x, r, dy)]
+    want = ag.ag_linear_fwd(plain[0], W, act="silu", residual=plain[1], preact=True)
+    ag.ag_linear_fwd(x, W, act="silu", residual=r, preact=z, out=y)
+    wdx, wdW, wdb = ag.ag_linear_bwd(plain[2], plain[0], W)
+    _, dW, db = ag.ag_linear_bwd(dy, x, W, dx=dx)
+    _ok(ag)
+    for a, b in ((y, want[0]), (z, want[1]), (dx, wdx), (dW, wdW), (db, wdb)):
+        assert torch.equal(a, b)
+    w = torch.as_strided(W, (1, K), (far, 1))
+    assert torch.equal(ag.ag_linear_fwd(plain[0], w), ag.ag_linear_fwd(plain[0], W[:1].clone()))

@@ -315,3 +315,24 @@ def test_qk_bwd_refuses_shared_elements_exactly(ag):
         assert st == ALIAS if shared else st in (UNSUPPORTED, CUDA), (q, k, at, heads)
         seen[shared] += 1
     assert min(seen) > 200
+
+
+def test_linear_stride_of_one_row_is_free(ag):
+    """Nothing uses it: the last position of a long sequence is one row whose
+    stride is the sequence's."""
+    if torch.cuda.is_available():
+        pytest.skip("would launch")
+    end, far = (UNSUPPORTED, CUDA), 1 << 40
+    n = ctypes.c_int64(0)
+    f = ag.lib.ag_linear_fwd_workspace
+    no_device = f(_p(0), 64, _p(1), 64, 1, 32, 64, ctypes.byref(n))
+    assert no_device in end
+    if no_device == CUDA:
+        end = (CUDA,)  # so that a refusal of the stride shows
+    assert _fwd(ag, M=1, ldx=far, ldr=far + 1, ldz=far + 3, ldy=far) in end
+    assert _fwd(ag, N=1, ldw=far + 1) in end
+    assert f(_p(0), far, _p(1), far, 1, 1, 64, ctypes.byref(n)) in end
+    assert _bwd(ag, M=1, lddy=far, ldx=far, lddx=far, ldz=far) in end
+    assert _bwd(ag, N=1, ldw=far, lddw=far) in end
+    assert _bwd(ag, M=1, lddy=31) == SHAPE
+    assert _fwd(ag, M=2, ldx=far) == UNSUPPORTED
