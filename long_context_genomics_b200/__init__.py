@@ -461,7 +461,10 @@ def ag_linear_bwd(dy: torch.Tensor, x: torch.Tensor, W: torch.Tensor, act: str =
 
 def ag_rope_frequencies(rotary_dim: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
     """inv_freq[p] = base^(-2p / rotary_dim), p < rotary_dim / 2, in fp64: the
-    usual frequencies for ag_qk_norm_rope_fwd (which takes any)."""
+    usual frequencies for ag_qk_norm_rope_fwd (which takes any).
+    rotary_dim, the number of elements that turn, is even."""
+    if rotary_dim < 0 or rotary_dim % 2:
+        raise ValueError(f"rotary_dim must be even and not negative, got {rotary_dim}")
     p = torch.arange(0, rotary_dim, 2, dtype=torch.float64)
     return (float(base) ** (-p / rotary_dim)).to(device)
 

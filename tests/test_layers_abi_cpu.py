@@ -336,3 +336,11 @@ def test_linear_stride_of_one_row_is_free(ag):
     assert _bwd(ag, N=1, ldw=far, lddw=far) in end
     assert _bwd(ag, M=1, lddy=31) == SHAPE
     assert _fwd(ag, M=2, ldx=far) == UNSUPPORTED
+
+
+def test_rope_frequencies_of_an_odd_dimension_are_refused(ag):
+    """(3 frequencies turn 6 elements, so 5 cannot be what was meant.)"""
+    for n in (5, 1, -2):
+        with pytest.raises(ValueError, match="even"):
+            ag.ag_rope_frequencies(n, device="cpu")
+    assert ag.ag_rope_frequencies(0, device="cpu").numel() == 0
