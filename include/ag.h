@@ -538,7 +538,9 @@ ag_status ag_qk_norm_rope_bwd_workspace(int64_t B, int64_t Hq, int64_t Hk, int64
  * +INFINITY only measures.  A gradient that is not finite makes norm
  * infinite or NaN: an infinite norm scales by 0 (so that the infinite
  * elements become NaN), a NaN one makes every element NaN.
- *   norm_out  float32, 4-byte aligned (written); the sum is kept in 64 bits
+ *   norm_out  float32, 4-byte aligned (written); the sum is kept in 64 bits,
+ *             and c is formed from it (so finite gradients whose norm passes
+ *             float32, written as infinite, are still scaled to max_norm)
  *   max_norm >= 0, eps >= 0 and not NaN (AG_ERR_VALUE); an unknown dtype
  *   likewise.  n >= 0, every count in [0, 2^40] (AG_ERR_SHAPE), their sum at
  *   most 2^42 and n at most 2^20 (AG_ERR_UNSUPPORTED); pointers aligned to

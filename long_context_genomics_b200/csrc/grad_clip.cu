@@ -135,6 +135,10 @@ __global__ void __launch_bounds__(kThreads)
   // Written so that a NaN stays a NaN.
   const float c = ratio >= 1.0 ? 1.f : static_cast<float>(ratio);
   if (c == 1.f) return;
+  // A factor below the normal numbers of 32 bits (gradients near their largest)
+  // would keep only some of its digits: it is applied in two steps.
+  const bool tiny = ratio < 0x1p-126;
+  const float once = tiny ? static_cast<float>(ratio * 0x1p120) : c, again = tiny ? 0x1p-120f : 1.f;
   // From the end: what the first pass read last is still in L2.
   const uint32_t chunks = list.first[list.n];
   for (uint32_t q = blockIdx.x; q < chunks; q += gridDim.x) {
@@ -145,7 +149,7 @@ __global__ void __launch_bounds__(kThreads)
       const int64_t at = k.at + head + 8 * static_cast<int64_t>(i);
       load_values<8>(k.base, at, k.dtype, v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] *= c;
+      for (int j = 0; j < 8; ++j) v[j] = v[j] * once * again;
       store_values<8>(k.base, at, k.dtype, v);
     }
     const int rest = k.len - 8 * body;
@@ -153,7 +157,7 @@ __global__ void __launch_bounds__(kThreads)
       const int i = static_cast<int>(threadIdx.x) < head ? threadIdx.x : threadIdx.x + 8 * body;
       float v[1];
       load_values<1>(k.base, k.at + i, k.dtype, v);
-      v[0] *= c;
+      v[0] = v[0] * once * again;
       store_values<1>(k.base, k.at + i, k.dtype, v);
     }
   }

@@ -69,3 +69,24 @@ def test_linear_one_row_of_any_stride(ag, far, K):
         assert torch.equal(a, b)
     w = torch.as_strided(W, (1, K), (far, 1))
     assert torch.equal(ag.ag_linear_fwd(plain[0], w), ag.ag_linear_fwd(plain[0], W[:1].clone()))
+
+
+# ---------------------------------------------------------------------------
+# Clipping
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("n,max_norm", [(8, 1e-2), (8, 1e-6), (1000, 1.0), (19, 1e-30)])
+def test_clip_by_a_factor_below_the_normal_numbers(ag, dtype, n, max_norm):
+    """Gradients near the largest number: the factor, formed in 64 bits, is a
+    subnormal number of 32 bits, which would leave few or none of its digits.
+    Two roundings to fp32 (the factor and the product) keep 2^-22."""
+    g = (torch.rand(n, generator=_gen(n)) * 1e38 + 1e38).to(dtype).cuda()
+    before = g.double()
+    norm = ag.ag_grad_clip([g], max_norm)
+    _ok(ag)
+    size = float(before.square().sum().sqrt())
+    want_norm = torch.tensor(size, dtype=torch.float64).float()
+    assert float(norm) == math.inf if math.isinf(float(want_norm)) else (
+        abs(float(norm) - size) <= size * 2.0 ** -23)
+    want = before * (max_norm / size)
+    _close("gradient", g, want, want.abs() * 2.0 ** -22 + _half_step(dtype, want) * 1.01
+           + 2.0 ** -149)
