@@ -455,8 +455,9 @@ typedef enum {
  *   a = position[b, l] * inv_freq[p] for the p-th pair (i, j) of the first R
  *   elements; the elements from R on are v.
  * Angles are formed and reduced in 64 bits, so positions far apart (alignment
- * columns, base pairs) keep their phase; everything else is float32, rounded
- * once.
+ * columns, base pairs) keep their phase (up to angles of 2^50); everything else
+ * is float32, rounded once.  For 16-bit outputs (in the gradients: 16-bit q and
+ * k) the sines and cosines are within 2^-21, for 32-bit ones within 2^-23.
  *
  *   q  [B, L, Hq, D] x_dtype, element strides q_sb, q_sl, q_sh over b, l, h
  *      (>= 0; D is dense), e.g. a slice of a fused projection's rows

@@ -40,19 +40,43 @@ namespace {
 constexpr int kThreads = 256;  // 8 warps
 constexpr int kWarps = kThreads / 32;
 
-// cos and sin of position * frequency.  The product and its reduction to
-// [-pi, pi] are in 64 bits (two-part 2 pi), so the phase of a far position is as
-// exact as the frequency; there the special-function unit's sine and cosine are
-// within 2^-21 (CUDA's bound for the fast functions), which a rotated float32
-// value of the row shares.
+// cos and sin of position * frequency.  The product and its reduction are in 64
+// bits (by a two-part 2 pi or pi / 2), so the phase of a far position is as exact
+// as the frequency, up to angles of 2^50.
+//
+// Where the results are of 16 bits, the special-function unit's sine and cosine
+// on [-pi, pi], within 2^-21 (CUDA's bound for the fast functions), are far
+// below their rounding.  EXACT, for 32-bit results: the Taylor sums to r^9 and
+// r^10 on [-pi / 4, pi / 4], where the next terms are below
+// 2^-28; within 1.3 units of 2^-24.
+template <bool EXACT>
 __device__ __forceinline__ float2 turn(long long pos, double freq) {
-  const double a = static_cast<double>(pos) * freq;
-  const double n = rint(a * 0.15915494309189535);
-  double r = fma(n, -6.283185307179586, a);
-  r = fma(n, -2.4492935982947064e-16, r);
-  float s, c;
-  __sincosf(static_cast<float>(r), &s, &c);
-  return make_float2(c, s);
+  double a = static_cast<double>(pos) * freq;
+  if constexpr (!EXACT) {
+    const double n = rint(a * 0.15915494309189535);
+    double r = fma(n, -6.283185307179586, a);
+    r = fma(n, -2.4492935982947064e-16, r);
+    float s, c;
+    __sincosf(static_cast<float>(r), &s, &c);
+    return make_float2(c, s);
+  }
+  // Angles of 2^51 and more have no quarter turn left that could be told: 0 (or NaN).
+  if ((__double2hiint(a) & 0x7FFFFFFF) >= 0x43200000) a -= a;
+  // Rounded by adding 1.5 * 2^52: the sum's lower word ends in the quarter turns.
+  const double t = fma(a, 0.6366197723675814, 0x1.8p52), n = t - 0x1.8p52;
+  const int turns = __double2loint(t);
+  const float r = static_cast<float>(
+      fma(n, -6.123233995736766e-17, fma(n, -1.5707963267948966, a)));
+  const float q = r * r;
+  float s = fmaf(q, 1.f / 362880, -1.f / 5040), c = fmaf(q, -1.f / 3628800, 1.f / 40320);
+  s = fmaf(fmaf(s, q, 1.f / 120), q, -1.f / 6);
+  c = fmaf(fmaf(fmaf(c, q, -1.f / 720), q, 1.f / 24), q, -0.5f);
+  s = fmaf(s * q, r, r), c = fmaf(c, q, 1.f);
+  const float cos = turns & 1 ? s : c, sin = turns & 1 ? c : s;
+  const uint32_t top = 0x80000000u;
+  return make_float2(
+      __uint_as_float(__float_as_uint(cos) ^ ((static_cast<uint32_t>(turns) + 1) << 30 & top)),
+      __uint_as_float(__float_as_uint(sin) ^ (static_cast<uint32_t>(turns) << 30 & top)));
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -244,15 +268,24 @@ __device__ __forceinline__ void turn_pairs(Eight &e, const float4 *cos4, const f
 
 // The angles of the group's position into its own shared memory: R / 2 cosines,
 // then as many sines.
-template <int LPR>
+template <int LPR, bool EXACT>
 __device__ __forceinline__ void group_angles(const QkArgs &a, float *cs, int64_t b, int64_t l,
                                              int lane) {
   __syncwarp();
   const long long pos = a.positions ? a.positions[b * a.pos_sb + l] : l;
   const int half = a.R / 2;
-  for (int i = lane % LPR; i < half; i += LPR) {
-    const float2 c = turn(pos, a.inv_freq[i]);
+  const auto one = [&](int i) {
+    const float2 c = turn<EXACT>(pos, a.inv_freq[i]);
     cs[i] = c.x, cs[half + i] = c.y;
+  };
+  if constexpr (EXACT) {
+    // (Four side by side, or their chains of products add up: 16384 positions of 9
+    // heads of 128 from bf16 to fp32 27.3 us, so 26.6; with the fast sine and
+    // cosine 26.3.)
+#pragma unroll 4
+    for (int i = lane % LPR; i < half; i += LPR) one(i);
+  } else {
+    for (int i = lane % LPR; i < half; i += LPR) one(i);
   }
   __syncwarp();
 }
@@ -368,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 4) qk_fwd_rows_kernel(const QkArgs a
   const Heads part = heads_of(a);
   bool ready = a.R == 0;
   const auto angles = [&] {  // while the first rows are on their way
-    if (!ready) group_angles<LPR>(a, cs, b, l, lane);
+    if (!ready) group_angles<LPR, OT == AG_F32>(a, cs, b, l, lane);
     ready = true;
   };
 #pragma unroll
@@ -504,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 2) qk_bwd_rows_kernel(const QkArgs a
     f.dx_at = static_cast<char *>(s.dx) +
               bytes_of<XT>(b * s.dxb + l * s.dxl + h.first * s.dxh + t.a);
     const auto angles = [&] {
-      if (a.R) group_angles<LPR>(a, cs, b, l, lane);
+      if (a.R) group_angles<LPR, XT == AG_F32>(a, cs, b, l, lane);
     };
     if (h.count == kChunk) {
       f.template rows<kChunk>(angles);
@@ -575,13 +608,14 @@ __device__ __forceinline__ void load_row_to(float *row, const void *x, int64_t a
   }
 }
 // The angles of np positions, by the whole block.
+template <bool EXACT>
 __device__ __forceinline__ void block_angles(const QkArgs &a, float2 *cs, uint32_t p0, int np,
                                              int half) {
   const uint32_t L = static_cast<uint32_t>(a.L);
   for (int i = threadIdx.x; i < np * half; i += blockDim.x) {
     const uint32_t p = static_cast<uint32_t>(i) / static_cast<uint32_t>(half), pos = p0 + p;
     const int64_t b = pos / L, l = pos % L;
-    cs[i] = turn(a.positions ? a.positions[b * a.pos_sb + l] : l, a.inv_freq[i - p * half]);
+    cs[i] = turn<EXACT>(a.positions ? a.positions[b * a.pos_sb + l] : l, a.inv_freq[i - p * half]);
   }
 }
 
@@ -602,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, kGeneralBlocks) qk_fwd_kernel(const 
     load_row_to<XT>(row, s.x, w.b * s.sb + w.l * s.sl + w.h * s.sh, a.D, lane);
   };
   if (warp < rows) load(warp);  // (on its way while the angles are formed)
-  block_angles(a, cs, p0, np, half);
+  block_angles<OT == AG_F32>(a, cs, p0, np, half);
   __syncthreads();
   for (int t = warp; t < rows; t += kWarps) {
     if (t != warp) load(t);
@@ -658,7 +692,7 @@ __global__ void __launch_bounds__(kThreads, kGeneralBlocks) qk_bwd_kernel(const 
     };
     if (warp < rows) load(warp);  // (on its way while the angles are formed)
     __syncthreads();              // the angles of the turn before are no longer read
-    block_angles(a, cs, p0, np, half);
+    block_angles<XT == AG_F32>(a, cs, p0, np, half);
     __syncthreads();
     for (int t = warp; t < rows; t += warps) {
       if (t != warp) load(t);

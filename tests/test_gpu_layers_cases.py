@@ -90,3 +90,55 @@ def test_clip_by_a_factor_below_the_normal_numbers(ag, dtype, n, max_norm):
     want = before * (max_norm / size)
     _close("gradient", g, want, want.abs() * 2.0 ** -22 + _half_step(dtype, want) * 1.01
            + 2.0 ** -149)
+
+
+# ---------------------------------------------------------------------------
+# Queries and keys: the angles of 32-bit results
+@pytest.mark.parametrize("rope", ["halves", "interleaved"])
+@pytest.mark.parametrize("D", [32, 64, 128, 256, 100, 6])
+@pytest.mark.parametrize("T", [BF16, F32])
+def test_qk_angles_of_32_bit_results(ag, T, D, rope):
+    """Rows without a norm: a rotated element is x cos - y sin, each sine and
+    cosine within 2^-23 (their own, see the kernel: 1.3 units of 2^-24), the
+    product and the sum each within half a unit: (2^-23 + 2 * 2^-24) (|x| + |y|),
+    a quarter of what the special-function unit's 2^-21 would need.  The same
+    for the gradient of 32-bit queries, which turns back."""
+    g, B, L, H = _gen(D), 2, 60, 3
+    q = _randn(g, B, L, H, D, dtype=T)
+    pos = torch.cat([torch.arange(0, 20), torch.randint(0, 1 << 20, (20,), generator=g),
+                     torch.randint(-(1 << 40), 1 << 40, (20,), generator=g)]).cuda()
+    freq = ag.ag_rope_frequencies(D)
+    kw = dict(norm="none", inv_freq=freq, rope=rope, positions=pos)
+    out, _ = ag.ag_qk_norm_rope_fwd(q, None, out_dtype=F32, **kw)
+    go = _randn(g, B, H, L, D)
+    dq = ag.ag_qk_norm_rope_bwd(go, None, q, None, **kw)[0]
+    _ok(ag)
+    where = pos.expand(B, L)
+
+    def mass(x):  # |x| + |y| of each element's pair
+        m = x.abs()
+        i = torch.arange(D, device="cuda")
+        return m + m[..., (i + D // 2) % D if rope == "halves" else i ^ 1]
+
+    unit = 2.0 ** -23 + 2 * 2.0 ** -24
+    want = ref.rotate(q.double(), where, freq, rope).transpose(1, 2)
+    _close("out", out, want, mass(q.double()).transpose(1, 2) * unit)
+    if T == F32:
+        gt = go.double().transpose(1, 2)
+        want = ref.rotate(gt, where, freq, rope, -1.0)
+        _close("dq", dq, want, mass(gt) * unit)
+
+
+@pytest.mark.parametrize("D", [64, 36])
+@pytest.mark.parametrize("out", [BF16, F32])
+def test_qk_positions_without_a_phase(ag, D, out):
+    """Beyond angles of 2^50 the phase is that of rounding, but a row keeps its
+    length: a rotation's sine and cosine stay those of some angle."""
+    q = _randn(_gen(1), 1, 6, 2, D)
+    pos = torch.tensor([1 << 52, -(1 << 55), 1 << 58, 1 << 62, -(1 << 63), (1 << 63) - 1]).cuda()
+    o, _ = ag.ag_qk_norm_rope_fwd(q, None, norm="none", inv_freq=ag.ag_rope_frequencies(D),
+                                  positions=pos, out_dtype=out)
+    _ok(ag)
+    size = lambda t: t.double().square().view(*t.shape[:-1], 2, D // 2).sum(-2).sqrt()  # noqa: E731
+    want = size(q).transpose(1, 2)
+    assert float((size(o) / want - 1).abs().max()) <= 2.0 ** -7
