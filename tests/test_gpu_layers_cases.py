@@ -142,3 +142,36 @@ def test_qk_positions_without_a_phase(ag, D, out):
     size = lambda t: t.double().square().view(*t.shape[:-1], 2, D // 2).sum(-2).sqrt()  # noqa: E731
     want = size(q).transpose(1, 2)
     assert float((size(o) / want - 1).abs().max()) <= 2.0 ** -7
+
+
+# ---------------------------------------------------------------------------
+# Activations element by element
+@pytest.mark.parametrize("M", [8, 512])
+def test_gelu_and_slope_of_every_size(ag, M):
+    """Identity weights and fp32 outputs.  The kernels form z Phi(z) as max(z, 0)
+    - |z| t with the tail t = Phi(-|z|) = R exp(-z^2 / 2), R a polynomial in
+    u = 1 / (1 + p |z|).  Relative errors, in units of 2^-24: the exponential
+    3 z^2 / 2 (three roundings of its argument) + 4 (the function unit); u 3,
+    which R, of slope 2.3 at most, makes 7; R's last sums 3, and the products
+    2: 16 + 3 z^2 / 2, on top of the polynomial's own fit, 9.2e-8 times
+    min(30, 1 / (2 t max(|z|, 1))).  phi(z) in the slope has the exponential's
+    and three roundings.  What is below the normal numbers is lost."""
+    z = torch.linspace(-14, 14, M * 128).view(M, 128).to(BF16).cuda()
+    eye = torch.eye(128, device="cuda").to(BF16)
+    y = ag.ag_linear_fwd(z, eye, act="gelu", out_dtype=F32)
+    one = torch.ones(M, 128, dtype=BF16, device="cuda")
+    dx, _, _ = ag.ag_linear_bwd(one, z, eye, act="gelu", preact=z, need_dW=False, need_db=False,
+                                dx_dtype=F32)
+    _ok(ag)
+    z = z.double()
+    x = z.abs()
+    phi = torch.exp(-z.square() / 2) / math.sqrt(2 * math.pi)
+    tail = 0.5 * torch.erfc(x / math.sqrt(2))
+    fit = 9.2e-8 * torch.clamp(1 / (2 * tail * x.clamp(min=1)), max=30)
+    of_tail = ((16 + 1.5 * z.square()) * 2.0 ** -24 + fit) * tail
+    lost = 14 * 2.0 ** -126
+    want = ref.act(z, "gelu")
+    _close("y", y, want, x * of_tail + 2.0 ** -24 * want.abs() + lost)
+    want = ref.act_slope(z, "gelu")
+    of_phi = (7 + 1.5 * z.square()) * 2.0 ** -24 * x * phi
+    _close("slope", dx, want, of_tail + of_phi + 2.0 ** -24 * (want.abs() + (z > 0)) + lost)
