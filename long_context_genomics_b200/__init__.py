@@ -4,7 +4,9 @@ layers around it.
 Argument marshalling only.  Every step of the computation runs in the CUDA
 kernels of libag.so (see include/ag.h for the C ABI); there is no CPU or
 PyTorch fallback, and importing this package raises if the library is
-missing.  PyTorch supplies device memory and the current stream.
+missing.  The layers' calls go through _layers.so: without it they raise
+ImportError, and the attention works.  PyTorch supplies device memory and the
+current stream.
 
     ag_pair_bias_project(pair[P,P,Cp] f32, W[Cp,H] f32) -> bias[H,P,P] f32
     ag_attn_fwd(q[B,H,L,D] bf16, k[B,L,D] bf16, v[B,L,D] bf16,
@@ -122,16 +124,36 @@ def _load() -> ctypes.CDLL:
 
 
 lib = _load()
-if not os.path.exists(LAYERS_PATH):
-    raise ImportError(
-        f"{LAYERS_PATH} is missing: build it with "
-        "`python long_context_genomics_b200/build.py` (or __graft_entry__.build())")
-from . import _layers  # noqa: E402  (the compiled half of the layers' binding)
 
-_layers.bind(tuple(ctypes.cast(f, ctypes.c_void_p).value for f in (
-    lib.ag_linear_fwd, lib.ag_linear_fwd_workspace, lib.ag_linear_bwd,
-    lib.ag_linear_bwd_workspace, lib.ag_qk_norm_rope_fwd, lib.ag_qk_norm_rope_bwd,
-    lib.ag_qk_norm_rope_bwd_workspace, lib.ag_grad_clip, lib.ag_grad_clip_workspace)), AgError)
+
+class _NoLayers:
+    """Stands for the layers' compiled binding where that cannot be used."""
+
+    def __init__(self, why: str):
+        self._why = why
+
+    def __getattr__(self, name):
+        raise ImportError(f"{LAYERS_PATH} {self._why}: build it with "
+                          "`python long_context_genomics_b200/build.py` "
+                          "(or __graft_entry__.build())")
+
+
+def _load_layers():
+    """The compiled half of the layers' binding, bound to this library."""
+    if not os.path.exists(LAYERS_PATH):
+        return _NoLayers("is missing")
+    try:
+        from . import _layers
+    except ImportError as e:  # e.g. symbols that this torch does not have
+        return _NoLayers(f"does not load ({e})")
+    _layers.bind(tuple(ctypes.cast(f, ctypes.c_void_p).value for f in (
+        lib.ag_linear_fwd, lib.ag_linear_fwd_workspace, lib.ag_linear_bwd,
+        lib.ag_linear_bwd_workspace, lib.ag_qk_norm_rope_fwd, lib.ag_qk_norm_rope_bwd,
+        lib.ag_qk_norm_rope_bwd_workspace, lib.ag_grad_clip, lib.ag_grad_clip_workspace)), AgError)
+    return _layers
+
+
+_layers = _load_layers()
 
 
 def ag_status_string(status: int) -> str:
@@ -525,7 +547,10 @@ def ag_qk_norm_rope_bwd(dq_out: torch.Tensor | None, dk_out: torch.Tensor | None
                           dq, dk)
 
 
-_is_dense = _layers.is_dense
+def _is_dense(t: torch.Tensor) -> bool:
+    """Whether the elements fill one block of memory, in any order of the
+    dimensions (what ag_grad_clip takes)."""
+    return _layers.is_dense(t)
 
 
 def ag_grad_clip(grads, max_norm: float, eps: float = 1e-6,

@@ -6,7 +6,7 @@ _layers.so (the compiled half of the layers' Python binding).
 The library links the CUDA runtime statically and reaches the driver's
 tensor-map encoder through cudaGetDriverEntryPoint, so it needs no CUDA
 driver library at link time and cross-compiles on a machine without a GPU.
-_layers.so is compiled by g++ against the headers of the installed torch.
+_layers.so is compiled by g++ against the headers of the installed torch.  Without torch the library is built alone (the C ABI needs nothing else).
 """
 from __future__ import annotations
 
@@ -16,6 +16,7 @@ import os
 import subprocess
 import sys
 import sysconfig
+import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -45,13 +46,22 @@ def _stale(target: str, inputs) -> bool:
     return any(os.path.getmtime(p) > t for p in inputs)
 
 
+def torch_dir():
+    """Where torch is installed, or None (torch itself is not imported)."""
+    spec = importlib.util.find_spec("torch")
+    return os.path.dirname(spec.origin) if spec and spec.origin else None
+
+
+def _layers_stale() -> bool:
+    return torch_dir() is not None and _stale(
+        LAYERS, [LAYERS_SOURCE, os.path.join(ROOT, "include", "ag.h")])
+
+
 def needs_build() -> bool:
-    return (_stale(LIB, _inputs())
-            or _stale(LAYERS, [LAYERS_SOURCE, os.path.join(ROOT, "include", "ag.h")]))
+    return _stale(LIB, _inputs()) or _layers_stale()
 
 
-def _layers_command():
-    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+def _layers_command(torch: str):
     cmd = [CXX, "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden"]
     for d in (os.path.join(torch, "include"),
               os.path.join(torch, "include", "torch", "csrc", "api", "include"),
@@ -61,7 +71,17 @@ def _layers_command():
                   "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch", "-ltorch_python"]
 
 
+def _build_layers(torch: str, verbose: bool) -> None:
+    cmd = _layers_command(torch)
+    if verbose:
+        print(" ".join(cmd))
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError("_layers build failed:\n" + res.stdout + res.stderr)
+
+
 def build(verbose: bool = False, ptxas_v: bool = False) -> str:
+    """Builds both; a failure of _layers.so is raised when libag.so is done."""
     cmd = [
         NVCC, "-gencode", "arch=compute_100a,code=sm_100a", "-O3",
         "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-shared",
@@ -70,19 +90,29 @@ def build(verbose: bool = False, ptxas_v: bool = False) -> str:
     ] + [os.path.join(CSRC, s) for s in SOURCES]
     if ptxas_v:
         cmd[1:1] = ["-Xptxas", "-v"]
-    layers = _layers_command()
     if verbose:
         print(" ".join(cmd))
-        print(" ".join(layers))
-    other = subprocess.Popen(layers, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    other_out, _ = other.communicate()
-    if res.returncode != 0:
-        raise RuntimeError("libag build failed:\n" + res.stdout + res.stderr)
-    if other.returncode != 0:
-        raise RuntimeError("_layers build failed:\n" + other_out)
+    # (nvcc's output goes to a file, so that it never waits for a reader.)
+    with tempfile.TemporaryFile("w+") as log:
+        lib = subprocess.Popen(cmd, stdout=log, stderr=subprocess.STDOUT)
+        torch, failed = torch_dir(), None
+        try:
+            if torch is None:
+                print("torch is not installed: _layers.so (the layers' Python binding) is not built")
+            else:
+                _build_layers(torch, verbose)
+        except (RuntimeError, OSError) as e:
+            failed = e
+        finally:
+            lib.wait()
+        log.seek(0)
+        out = log.read()
+    if lib.returncode != 0:
+        raise RuntimeError("libag build failed:\n" + out)
     if verbose or ptxas_v:
-        sys.stdout.write(res.stdout + res.stderr)
+        sys.stdout.write(out)
+    if failed is not None:
+        raise failed
     return LIB
 
 
