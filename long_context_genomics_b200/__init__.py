@@ -4,9 +4,9 @@ layers around it.
 Argument marshalling only.  Every step of the computation runs in the CUDA
 kernels of libag.so (see include/ag.h for the C ABI); there is no CPU or
 PyTorch fallback, and importing this package raises if the library is
-missing.  The layers' calls go through _layers.so: without it they raise
-ImportError, and the attention works.  PyTorch supplies device memory and the
-current stream.
+missing.  The layers' calls go through _layers.so, which is compiled for one
+torch: without it, or with one for another torch, they raise ImportError, and
+the attention works.  PyTorch supplies device memory and the current stream.
 
     ag_pair_bias_project(pair[P,P,Cp] f32, W[Cp,H] f32) -> bias[H,P,P] f32
     ag_attn_fwd(q[B,H,L,D] bf16, k[B,L,D] bf16, v[B,L,D] bf16,
@@ -146,6 +146,9 @@ def _load_layers():
         from . import _layers
     except ImportError as e:  # e.g. symbols that this torch does not have
         return _NoLayers(f"does not load ({e})")
+    built_for = getattr(_layers, "built_for", "torch unknown")
+    if built_for.split()[1] != torch.__version__:
+        return _NoLayers(f"was built for {built_for}, this is torch {torch.__version__}")
     _layers.bind(tuple(ctypes.cast(f, ctypes.c_void_p).value for f in (
         lib.ag_linear_fwd, lib.ag_linear_fwd_workspace, lib.ag_linear_bwd,
         lib.ag_linear_bwd_workspace, lib.ag_qk_norm_rope_fwd, lib.ag_qk_norm_rope_bwd,

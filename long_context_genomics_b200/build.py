@@ -6,13 +6,16 @@ _layers.so (the compiled half of the layers' Python binding).
 The library links the CUDA runtime statically and reaches the driver's
 tensor-map encoder through cudaGetDriverEntryPoint, so it needs no CUDA
 driver library at link time and cross-compiles on a machine without a GPU.
-_layers.so is compiled by g++ against the headers of the installed torch.  Without torch the library is built alone (the C ABI needs nothing else).
+_layers.so is compiled by g++ against the headers of the installed torch and
+works with that torch only: _layers.built_for names it, and another one builds
+it anew.  Without torch the library is built alone (the C ABI needs nothing else).
 """
 from __future__ import annotations
 
 import argparse
 import importlib.util
 import os
+import re
 import subprocess
 import sys
 import sysconfig
@@ -23,6 +26,7 @@ CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libag.so")
 LAYERS = os.path.join(HERE, "_layers.so")
+LAYERS_BUILT_FOR = os.path.join(HERE, "_layers.built_for")
 LAYERS_SOURCE = os.path.join(CSRC, "layers_binding.cpp")
 SOURCES = ["ag_api.cu", "ag_layers_api.cu", "attn_fwd_sm100.cu", "attn_noalloc.cu", "attn_bwd.cu",
            "attn_bwd_sm100.cu", "pair_bias_project.cu", "linear.cu", "linear_sm100.cu",
@@ -52,9 +56,23 @@ def torch_dir():
     return os.path.dirname(spec.origin) if spec and spec.origin else None
 
 
+def built_for(torch: str) -> str:
+    """What a _layers.so depends on: the torch and the Python it is compiled for."""
+    with open(os.path.join(torch, "version.py")) as f:
+        version = re.search(r"__version__\s*=\s*['\"]([^'\"]+)", f.read())
+    return f"torch {version.group(1) if version else '?'} {sysconfig.get_config_var('SOABI')}"
+
+
 def _layers_stale() -> bool:
-    return torch_dir() is not None and _stale(
-        LAYERS, [LAYERS_SOURCE, os.path.join(ROOT, "include", "ag.h")])
+    torch = torch_dir()
+    if torch is None:
+        return False
+    if _stale(LAYERS, [LAYERS_SOURCE, os.path.join(ROOT, "include", "ag.h")]):
+        return True
+    if not os.path.exists(LAYERS_BUILT_FOR):
+        return True
+    with open(LAYERS_BUILT_FOR) as f:
+        return f.read().strip() != built_for(torch)
 
 
 def needs_build() -> bool:
@@ -62,7 +80,14 @@ def needs_build() -> bool:
 
 
 def _layers_command(torch: str):
-    cmd = [CXX, "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden"]
+    # torch's own flag for the C++ library's ABI, asked of that torch.
+    abi = subprocess.run([sys.executable, "-c", "import torch; print(int(torch.compiled_with_cxx11_abi()))"],
+                         capture_output=True, text=True)
+    if abi.returncode != 0:
+        raise RuntimeError("_layers build failed: torch does not import:\n" + abi.stderr)
+    cmd = [CXX, "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={abi.stdout.strip()}",
+           f'-DAG_BUILT_FOR="{built_for(torch)}"']
     for d in (os.path.join(torch, "include"),
               os.path.join(torch, "include", "torch", "csrc", "api", "include"),
               sysconfig.get_paths()["include"], os.path.join(CUDA, "include")):
@@ -78,6 +103,8 @@ def _build_layers(torch: str, verbose: bool) -> None:
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError("_layers build failed:\n" + res.stdout + res.stderr)
+    with open(LAYERS_BUILT_FOR, "w") as f:
+        f.write(built_for(torch) + "\n")
 
 
 def build(verbose: bool = False, ptxas_v: bool = False) -> str:

@@ -562,4 +562,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_layers",
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__layers() { return PyModule_Create(&module); }
+// `built_for` says which torch and Python this was compiled for (build.py).
+PyMODINIT_FUNC PyInit__layers() {
+  PyObject *m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "built_for", AG_BUILT_FOR) < 0) Py_CLEAR(m);
+  return m;
+}

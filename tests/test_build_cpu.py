@@ -71,7 +71,7 @@ def test_reports_a_library_that_does_not_build(tree, tmp_path):
         tree.build()
 
 
-def _import_without(tmp_path, name, code, layers=None):
+def _import(tmp_path, name, code, layers=None, before=""):
     """Runs `code` with a copy of the package that has the library and, unless
     it is None, `layers` for the compiled binding."""
     pkg = tmp_path / name
@@ -80,8 +80,8 @@ def _import_without(tmp_path, name, code, layers=None):
     os.symlink(os.path.join(PACKAGE, "libag.so"), pkg / "libag.so")
     if layers is not None:
         layers(pkg / "_layers.so")
-    return subprocess.run([sys.executable, "-c", f"import {name} as ag\n{code}"], cwd=tmp_path,
-                          capture_output=True, text=True, timeout=300)
+    return subprocess.run([sys.executable, "-c", f"{before}\nimport {name} as ag\n{code}"],
+                          cwd=tmp_path, capture_output=True, text=True, timeout=300)
 
 
 ATTENTION = """
@@ -100,12 +100,41 @@ for call in (lambda: ag.ag_linear_fwd(torch.zeros(1, 8), torch.zeros(8, 8)),
 
 
 def test_attention_needs_no_compiled_binding(tmp_path):
-    res = _import_without(tmp_path, "ag_without", ATTENTION)
+    res = _import(tmp_path, "ag_without", ATTENTION)
     assert res.returncode == 0, res.stdout + res.stderr
     assert res.stdout.count("_layers.so is missing: build it with") == 3
 
 
 def test_a_binding_that_does_not_load_is_named(tmp_path):
-    res = _import_without(tmp_path, "ag_broken", ATTENTION, lambda p: p.write_text("not a library"))
+    res = _import(tmp_path, "ag_broken", ATTENTION, lambda p: p.write_text("not a library"))
     assert res.returncode == 0, res.stdout + res.stderr
     assert res.stdout.count("_layers.so does not load") == 3 and "build.py" in res.stdout
+
+
+def test_another_torch_builds_the_binding_anew(tree, tmp_path, monkeypatch):
+    tree.build()
+    assert not tree.needs_build()
+    now = tree.built_for(tree.torch_dir())
+    other = tmp_path / "torch"
+    other.mkdir()
+    (other / "version.py").write_text("__version__ = '2.12.1+cu130'\n")
+    monkeypatch.setattr(tree, "torch_dir", lambda: str(other))
+    assert tree.built_for(str(other)).startswith("torch 2.12.1+cu130 ") and now.startswith("torch ")
+    assert tree.needs_build()
+    monkeypatch.undo()
+    os.remove(tree.LAYERS_BUILT_FOR)
+    assert tree.needs_build()
+
+
+def test_the_binding_is_compiled_for_the_abi_of_torch(tree):
+    torch = pytest.importorskip("torch")
+    assert (f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}"
+            in tree._layers_command(tree.torch_dir()))
+
+
+def test_a_binding_for_another_torch_is_refused(tmp_path):
+    """(Where its symbols happen to be there: the version tells.)"""
+    res = _import(tmp_path, "ag_other", ATTENTION, before="import torch\ntorch.__version__ = '2.10.0'",
+                  layers=lambda p: os.symlink(os.path.join(PACKAGE, "_layers.so"), p))
+    assert res.returncode == 0, res.stdout + res.stderr
+    assert res.stdout.count("this is torch 2.10.0") == 3 and "was built for torch" in res.stdout
