@@ -207,16 +207,20 @@ __global__ void __launch_bounds__(256) column_join_kernel(const ColumnParts c) {
   join_columns(c, blockIdx.x);
 }
 
+// Whether TMA can read a matrix in place.
+bool tma_readable(const void *p, int64_t ld) { return aligned(p, 16) && ld % 8 == 0; }
+
 // --------------------------------------------------------------------------
 // Up to 8 rows of x: the weights' one pass through the SMs sets the time, and a
 // tile of 256 rows would be almost empty.  A warp takes kRowsW rows of W at a
 // time, its lanes 8 consecutive terms each (V == 1: one, for rows that 16-byte
 // loads cannot read), and the warps of a block first share out the summed
 // dimension, so that even a small W has all its loads in flight at once.  Each
-// block writes its outputs itself: no workspace and one launch.  Up to 8 rows,
-// us at 1, 4 and 8 rows and the tensor cores' at 9: 1024 x 1536 2.9, 3.4, 5.5
-// and 8.1; 4096 x 1024 4.7, 6.5, 10.6 and 7.8 (10.2 at 8); 1024 x 4096 3.9, 5.0,
-// 8.1 and 9.4; 128 x 1024 2.5, 3.1, 5.0 and 8.3; 501 x 1003 2.6, 3.4, 4.7 and 9.9.
+// block writes its outputs itself: no workspace and one launch.  us at 1, 4 and 8
+// rows and the tensor cores' at 4 and 8: 1024 x 1536 2.9, 3.4, 5.5 and 8.3, 8.6;
+// 4096 x 1024 4.7, 6.5, 10.5 and 7.5, 7.5; 1024 x 4096 3.7, 4.7, 8.0 and 9.4, 9.3;
+// 128 x 1024 2.5, 3.2, 5.0 and 8.1, 8.3; 501 x 1003 2.7, 3.5, 4.7 and 10.0, 10.3;
+// 16384 x 1024 10.4, 19.4, 29.3 and 12.6, 12.1.
 constexpr int kSkinnyRows = 8;
 constexpr int kRowsW = 4;
 
@@ -280,19 +284,61 @@ __global__ void __launch_bounds__(256)
   }
 }
 
+// How the kernel divides a product: warps over the summed dimension, blocks, and
+// the steps of a warp along it.
+struct SkinnyShape {
+  bool vec;
+  int warps_k;
+  int64_t blocks, steps;
+};
+SkinnyShape skinny_shape(const LinearFwd &a) {
+  SkinnyShape s;
+  s.vec = a.K % 8 == 0 && a.ldx % 8 == 0 && a.ldw % 8 == 0 && aligned(a.x, 16) && aligned(a.W, 16);
+  const int64_t deep = 32 * (s.vec ? 8 : 1);
+  s.warps_k = 1;
+  while (s.warps_k < 8 && s.warps_k * deep < a.K) s.warps_k *= 2;
+  const int64_t rows = static_cast<int64_t>(8 / s.warps_k) * kRowsW;
+  s.blocks = (a.N + rows - 1) / rows;
+  s.steps = (a.K + s.warps_k * deep - 1) / (s.warps_k * deep);
+  return s;
+}
+
+// Whether a product of few rows goes through the skinny kernel: one row always,
+// up to 8 where that is estimated to take no longer than the tensor cores (with
+// their copies of rows that TMA cannot read).  Estimated in SM cycles from the
+// rounds of blocks (3 of 1 or 2 rows of x to an SM, 2 of more) and their steps,
+// of which those of single loads are a tenth; fitted to 43 weights of 64 x 65536
+// to 65536 x 512 at 2 to 8 rows: the choice takes 0.8 % more than the better of
+// both on average, the skinny kernel for all of them 14 %.
+bool takes_skinny(const LinearFwd &a) {
+  if (a.M > kSkinnyRows || a.M <= 1) return a.M <= 1;
+  struct Cost {
+    int per_sm, start, round, step;
+  };
+  const Cost c = a.M == 2  ? Cost{3, 2850, 2470, 1615}
+                 : a.M <= 4 ? Cost{2, 2280, 3135, 1805}
+                            : Cost{2, 3800, 3800, 3800};
+  const SkinnyShape s = skinny_shape(a);
+  const int64_t at_once = static_cast<int64_t>(c.per_sm) * a.num_sms;
+  const double rounds = static_cast<double>((s.blocks + at_once - 1) / at_once);
+  const double time = c.start + rounds * (c.round + c.step * (s.vec ? 1.0 : 0.1) * s.steps);
+  // (No plan takes less than one tile's products, or one step of them and a join;
+  // so the smallest calls need none.)
+  const double whole = 8700 + item_time(128, (a.K + 63) / 64),
+               split = 8700 + item_time(128, 1) + join_time(2, 1, 1);
+  if (time <= (whole < split ? whole : split)) return true;
+  const bool copies = !tma_readable(a.x, a.ldx) || !tma_readable(a.W, a.ldw);
+  return time <= plan_gemm(a.M, a.N, a.K, a.num_sms / 2).time + (copies ? 5000 : 0);
+}
+
 template <int MT>
 cudaError_t launch_skinny(const LinearFwd &a) {
-  const bool vec = a.K % 8 == 0 && a.ldx % 8 == 0 && a.ldw % 8 == 0 && aligned(a.x, 16) &&
-                   aligned(a.W, 16);
-  int warps_k = 1;
-  while (warps_k < 8 && static_cast<int64_t>(warps_k) * 32 * (vec ? 8 : 1) < a.K) warps_k *= 2;
-  const int64_t rows = static_cast<int64_t>(8 / warps_k) * kRowsW;
-  const unsigned blocks = static_cast<unsigned>((a.N + rows - 1) / rows);
-  auto *kernel = vec ? linear_skinny_kernel<MT, 8> : linear_skinny_kernel<MT, 1>;
-  return launch_after_previous(kernel, blocks, 256, 0, a.stream,
+  const SkinnyShape s = skinny_shape(a);
+  auto *kernel = s.vec ? linear_skinny_kernel<MT, 8> : linear_skinny_kernel<MT, 1>;
+  return launch_after_previous(kernel, static_cast<unsigned>(s.blocks), 256, 0, a.stream,
                                static_cast<const uint16_t *>(a.x), a.ldx,
                                static_cast<const uint16_t *>(a.W), a.ldw, static_cast<int>(a.M),
-                               a.N, a.K, warps_k, a.epi);
+                               a.N, a.K, s.warps_k, a.epi);
 }
 
 // --------------------------------------------------------------------------
@@ -307,8 +353,6 @@ struct Workspace {
     return p;
   }
 };
-
-bool tma_readable(const void *p, int64_t ld) { return aligned(p, 16) && ld % 8 == 0; }
 
 // The operand as TMA can read it, in place or as a copy in the workspace.
 struct Packed {
@@ -422,13 +466,13 @@ BwdLayout bwd_layout(const LinearBwd &a, Workspace &ws) {
 
 cudaError_t linear_fwd_workspace(const LinearFwd &a, int64_t *bytes) {
   Workspace ws{nullptr};
-  if (a.M > kSkinnyRows) fwd_layout(a, ws);
+  if (!takes_skinny(a)) fwd_layout(a, ws);
   *bytes = ws.used;
   return cudaSuccess;
 }
 
 cudaError_t launch_linear_fwd(const LinearFwd &a) {
-  if (a.M <= kSkinnyRows)
+  if (takes_skinny(a))
     return a.M == 1   ? launch_skinny<1>(a)
            : a.M == 2 ? launch_skinny<2>(a)
            : a.M <= 4 ? launch_skinny<4>(a)

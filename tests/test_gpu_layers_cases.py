@@ -7,8 +7,8 @@ import pytest
 import torch
 
 import layers_reference as ref
-from test_gpu_layers import (BF16, F16, F32, _close, _gen, _half_step, _ok, _randn,  # noqa: F401
-                             ag)
+from test_gpu_layers import (BF16, F16, F32, _close, _gen, _half_step, _linear_bwd_case,  # noqa: F401
+                             _linear_case, _ok, _randn, ag)
 
 pytestmark = pytest.mark.gpu
 
@@ -175,3 +175,31 @@ def test_gelu_and_slope_of_every_size(ag, M):
     want = ref.act_slope(z, "gelu")
     of_phi = (7 + 1.5 * z.square()) * 2.0 ** -24 * x * phi
     _close("slope", dx, want, of_tail + of_phi + 2.0 ** -24 * (want.abs() + (z > 0)) + lost)
+
+
+# ---------------------------------------------------------------------------
+# Linear layers of few rows: two kernels, by an estimate of their times
+@pytest.mark.parametrize("M", range(1, 10))
+@pytest.mark.parametrize("N,K", [(4096, 1024), (1024, 1536), (16384, 1024), (8192, 256), (64, 16384),
+                                 (5001, 1003), (40, 72)])
+def test_linear_few_rows_on_both_sides_of_the_rule(ag, M, N, K):
+    _linear_case(ag, M, N, K, act="gelu")
+    _linear_case(ag, M, N, K, T=F16, out=F32, residual=False, preact=False)
+
+
+def test_linear_few_rows_take_the_tensor_cores_where_those_are_faster(ag):
+    """(Only those split a sum, and so take a workspace.)  Measured, us, on the
+    weight-streaming kernel and on the tensor cores: 8 x 64 x 65536 67 and 17,
+    8 x 1024 x 16384 20 and 15, 2 x 64 x 65536 25 and 17; 8 x 1024 x 1536 5.5 and 8.6,
+    4 x 1024 x 8192 6.7 and 13, 1 x 1024 x 16384 7.0 and 17."""
+    import ctypes
+
+    def bytes_of(M, N, K):
+        n = ctypes.c_int64(-1)
+        assert ag.lib.ag_linear_fwd_workspace(256, K, 512, K, M, N, K, ctypes.byref(n)) == 0
+        return n.value
+
+    for shape in ((8, 64, 65536), (8, 1024, 16384), (2, 64, 65536)):
+        assert bytes_of(*shape) > 0, shape
+    for shape in ((8, 1024, 1536), (4, 1024, 8192), (1, 1024, 16384)):
+        assert bytes_of(*shape) == 0, shape
