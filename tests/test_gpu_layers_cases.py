@@ -203,3 +203,9 @@ def test_linear_few_rows_take_the_tensor_cores_where_those_are_faster(ag):
         assert bytes_of(*shape) > 0, shape
     for shape in ((8, 1024, 1536), (4, 1024, 8192), (1, 1024, 16384)):
         assert bytes_of(*shape) == 0, shape
+
+
+@pytest.mark.parametrize("M,N,K", [(4488, 4960, 392), (248, 3136, 360), (136, 2736, 72)])
+def test_linear_gradients_near_the_rule_of_one_launch(ag, M, N, K):
+    _linear_bwd_case(ag, M, N, K)
+    _linear_bwd_case(ag, M, N, K, T=F16, dx_t=F32, dw_t=F16, act="silu")
