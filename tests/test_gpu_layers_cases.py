@@ -209,3 +209,57 @@ def test_linear_few_rows_take_the_tensor_cores_where_those_are_faster(ag):
 def test_linear_gradients_near_the_rule_of_one_launch(ag, M, N, K):
     _linear_bwd_case(ag, M, N, K)
     _linear_bwd_case(ag, M, N, K, T=F16, dx_t=F32, dw_t=F16, act="silu")
+
+
+# ---------------------------------------------------------------------------
+# Long sums: nothing left out, nothing counted twice
+def _whole(gen, *shape, T=BF16):
+    """Whole numbers of -3 to 3 without 0: their products' sums of up to 2^20 terms
+    stay below 2^24, so that fp32 holds every partial sum exactly, in any order,
+    rounded or truncated."""
+    v = torch.randint(1, 4, shape, generator=gen, device="cuda", dtype=torch.int8)
+    return (v * (torch.randint(0, 2, shape, generator=gen, device="cuda", dtype=torch.int8) * 2 - 1)).to(T)
+
+
+LONG = [(70001, 16, 24), (64, 24, 40000), (6, 40, 20001), (9, 4104, 8), (19000, 256, 256),
+        (40000, 128, 128), (9000, 301, 701), (8192, 1152, 1024), (3000, 1500, 999),
+        (1000, 3008, 600), (300, 200, 5000), (777, 501, 1003), (65536, 128, 128), (2048, 2048, 8),
+        (8, 64, 65536), (5, 4096, 1024), (4096, 1024, 4096), (130000, 64, 61), (1, 8, 32768)]
+
+
+@pytest.mark.parametrize("T", [BF16, F16])
+@pytest.mark.parametrize("M,N,K", LONG)
+def test_linear_sums_of_whole_numbers_are_exact(ag, M, N, K, T):
+    """y, dx, dW and db of whole numbers, bit for bit: a tile, a part of a split
+    sum or a part of the rows that is lost or doubled shows, whatever the length
+    (a bound on rounded sums of 40000 terms lets 64 of them go)."""
+    g = torch.Generator(device="cuda").manual_seed(M + N + K)
+    x, W, dy = _whole(g, M, K, T=T), _whole(g, N, K, T=T), _whole(g, M, N, T=T)
+    b = torch.randint(-100, 100, (N,), generator=g, device="cuda").float()
+    xd, Wd, dyd = x.double(), W.double(), dy.double()
+    y = ag.ag_linear_fwd(x, W, bias=b, out_dtype=F32)
+    _ok(ag)
+    assert torch.equal(y.double(), xd @ Wd.T + b.double())
+    dx, dW, db = ag.ag_linear_bwd(dy, x, W, dx_dtype=F32)
+    only_dx = ag.ag_linear_bwd(dy, x, W, dx_dtype=F32, need_dW=False, need_db=False)[0]
+    only_dW = ag.ag_linear_bwd(dy, x, W, need_dx=False, need_db=False)[1]
+    only_db = ag.ag_linear_bwd(dy, x, W, need_dx=False, need_dW=False)[2]
+    _ok(ag)
+    for got, want in ((dx, dyd @ Wd), (dW, dyd.T @ xd), (db, dyd.sum(0))):
+        assert torch.equal(got.double(), want)
+    assert torch.equal(only_dx, dx) and torch.equal(only_dW, dW) and torch.equal(only_db, db)
+
+
+def test_the_check_of_whole_numbers_sees_a_lost_tile(ag):
+    """The same comparison against oracles with 64 terms, a split's part or one
+    row left out, or one counted twice."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    M, N, K = 16, 24, 70001
+    x, W = _whole(g, M, K), _whole(g, N, K)
+    y = ag.ag_linear_fwd(x, W, out_dtype=F32).double()
+    _ok(ag)
+    xd, Wd = x.double(), W.double()
+    assert torch.equal(y, xd @ Wd.T)
+    for lost in (slice(64, 128), slice(0, K // 32), slice(K - 1, K)):
+        part = xd[:, lost] @ Wd[:, lost].T
+        assert not torch.equal(y, xd @ Wd.T - part) and not torch.equal(y, xd @ Wd.T + part)
