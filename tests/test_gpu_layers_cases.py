@@ -263,3 +263,38 @@ def test_the_check_of_whole_numbers_sees_a_lost_tile(ag):
     for lost in (slice(64, 128), slice(0, K // 32), slice(K - 1, K)):
         part = xd[:, lost] @ Wd[:, lost].T
         assert not torch.equal(y, xd @ Wd.T - part) and not torch.equal(y, xd @ Wd.T + part)
+
+
+# ---------------------------------------------------------------------------
+# The accumulator is taken over every 512 terms
+@pytest.mark.parametrize("kind", ["y", "dx", "dW", "split"])
+def test_linear_sums_do_not_drift(ag, kind):
+    """32768 positive terms, one product to a cluster (74 tiles: no split), and a
+    split one.  The tensor core truncates: each of the steps of a takeover's 512
+    terms (16 terms or 8 to a step, at most 64) loses up to 2^-23 of the sum so
+    far, on average of half the takeover's: 32 * 2^-23 of the whole.  The 64
+    takeovers round by 2^-24 of the sum so far: 32 * 2^-24.  So 48 * 2^-23 =
+    5.8e-6 bounds it, and the drift of an accumulator over the whole length
+    (2048 steps of 16 terms that lose a quarter of 2^-23 on average: 256 * 2^-23
+    and more; measured, 1.6e-4) lies far above."""
+    n, M, N = 32768, 74 * 128, 512
+    if kind == "split":
+        M, N = 64, 40
+    g = torch.Generator(device="cuda").manual_seed(5)
+    pos = lambda *s: (torch.rand(s, generator=g, device="cuda") + 0.5).to(BF16)  # noqa: E731
+    rows = slice(0, 200)
+    if kind in ("y", "split"):
+        x, W = pos(M, n), pos(N, n)
+        got = ag.ag_linear_fwd(x, W, out_dtype=F32)[rows]
+        want = x[rows].double() @ W.double().T
+    elif kind == "dx":
+        dy, W, x = pos(M, n), pos(n, N), pos(M, N)
+        got = ag.ag_linear_bwd(dy, x, W, need_dW=False, need_db=False, dx_dtype=F32)[0][rows]
+        want = dy[rows].double() @ W.double()
+    else:
+        dy, x, W = pos(n, M), pos(n, N), pos(M, N)
+        got = ag.ag_linear_bwd(dy, x, W, need_dx=False, need_db=False)[1][rows]
+        want = dy[:, rows].double().T @ x.double()
+    _ok(ag)
+    err = (got.double() / want - 1).abs().max()
+    assert float(err) <= 48 * 2.0 ** -23
