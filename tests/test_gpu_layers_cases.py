@@ -298,3 +298,44 @@ def test_linear_sums_do_not_drift(ag, kind):
     _ok(ag)
     err = (got.double() / want - 1).abs().max()
     assert float(err) <= 48 * 2.0 ** -23
+
+
+# ---------------------------------------------------------------------------
+# Both gradients where TMA can write dx's rows but not dW's (two launches)
+@pytest.mark.parametrize("M,N,K,act", [(777, 501, 1004, "none"), (2048, 512, 1004, "none"),
+                                       (2048, 1024, 1004, "gelu"), (300, 64, 36, "silu")])
+def test_linear_gradients_of_unlike_rows(ag, M, N, K, act):
+    """16-bit dW of a row length that is no multiple of 8 beside fp32 dx (and a
+    pre-activation with rows apart)."""
+    g = _gen(M)
+    dy, x = _randn(g, M, N, dtype=BF16), _randn(g, M, K, dtype=BF16)
+    W = _randn(g, N, K, dtype=BF16, scale=1 / math.sqrt(N))
+    z = torch.zeros(M, K + 4, dtype=BF16, device="cuda")[:, :K]
+    z.copy_(_randn(g, M, K, dtype=BF16))
+    dx, dW, db = ag.ag_linear_bwd(dy, x, W, act=act, preact=z if act != "none" else None,
+                                  dx_dtype=F32, dW_dtype=BF16)
+    _ok(ag)
+    dyd, xd, Wd = dy.double(), x.double(), W.double()
+    want, tol = dyd @ Wd, (N + 8) * 2.0 ** -23 * (dyd.abs() @ Wd.abs())
+    if act != "none":
+        tol = tol * 1.13 + want.abs() * 2.0 ** -20 * (1 + z.double().abs())
+        want = want * ref.act_slope(z.double(), act)
+    _close("dx", dx, want, tol * (1 + 2.0 ** -22) + _half_step(F32, want))
+    want = dyd.T @ xd
+    _close("dW", dW, want, (M + 8) * 2.0 ** -23 * (dyd.abs().T @ xd.abs()) * (1 + 2.0 ** -7)
+           + _half_step(BF16, want))
+    _close("db", db, dyd.sum(0), (M + 8) * 2.0 ** -24 * dyd.abs().sum(0) + _half_step(F32, dyd.sum(0)))
+
+
+def test_linear_gradients_where_dW_starts_off_alignment(ag):
+    """dW 2 bytes past a 16-byte boundary beside an aligned dx."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    M, N, K = 500, 136, 264
+    dy, x, W = (_whole(g, *s) for s in ((M, N), (M, K), (N, K)))
+    flat = torch.full((N * K + 2,), 7.0, dtype=BF16, device="cuda")
+    dW = flat[1:-1].view(N, K)
+    dx, _, db = ag.ag_linear_bwd(dy, x, W, dW=dW)
+    wdx, wdW, wdb = ag.ag_linear_bwd(dy, x, W, dW_dtype=BF16)
+    _ok(ag)
+    assert torch.equal(dW, wdW) and torch.equal(db, wdb) and torch.equal(dx, wdx)
+    assert float(flat[0]) == 7.0 and float(flat[-1]) == 7.0
