@@ -32,7 +32,7 @@ SOURCES = ["ag_api.cu", "ag_layers_api.cu", "attn_fwd_sm100.cu", "attn_noalloc.c
            "attn_bwd_sm100.cu", "pair_bias_project.cu", "linear.cu", "linear_sm100.cu",
            "qk_norm_rope.cu", "grad_clip.cu"]
 HEADERS = ["sm100.cuh", "ag_internal.h", "attn_bwd_phases.cuh", "linear_epilogue.cuh",
-           "linear_gemm.h", "launch.cuh"]
+           "linear_gemm.h", "linear_ptx.cuh", "launch.cuh"]
 CUDA = "/usr/local/cuda"
 NVCC = os.environ.get("NVCC", os.path.join(CUDA, "bin", "nvcc"))
 CXX = os.environ.get("CXX", "g++")

@@ -52,7 +52,7 @@
 #include "linear_epilogue.cuh"
 #include "launch.cuh"
 #include "linear_gemm.h"
-#include "sm100.cuh"
+#include "linear_ptx.cuh"
 
 namespace ag {
 namespace gemm {
