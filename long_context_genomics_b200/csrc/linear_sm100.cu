@@ -33,6 +33,11 @@
 // loads and stores, turned through shared memory so that they are at least
 // contiguous.
 //
+// Registers.  The 256-wide kernels with a derivative in the epilogue, and those of
+// both gradients, hold more than 96 a thread: they spill 64 to 228 bytes (loads
+// 104 to 252) around the epilogue, whose sums alone are 64 registers; the others
+// spill nothing.
+//
 // Bounds.  16384 x 4096 x 1024 without an activation takes 100 to 102 us, 1.36
 // PFLOP/s: the products, at the clock that the board's power leaves (the
 // library's product takes 100).  8192 x 1024 x 1536 takes 22.4 us with bias and

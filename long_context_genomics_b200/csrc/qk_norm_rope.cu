@@ -24,6 +24,8 @@
 // 8 + 1 heads of 128, bf16): 20.4 us in the forward; four rows at a time 24 us
 // (fewer warps fit), sixteen elements to a lane 23 us, a fixed grid over
 // positions 23.6 us.  Gradients of half of that (76 MB): 25 us.
+// Instances of 32-bit q and k spill: up to 20 bytes in the forward (64 registers,
+// four blocks an SM), up to 52 in the gradients (128, two blocks).
 //
 // General kernels: one warp per row through shared memory, any size or stride.  A
 // block takes `at_once` positions a turn, enough for a row to each warp.  Bound by
