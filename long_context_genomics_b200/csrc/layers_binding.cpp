@@ -107,6 +107,9 @@ const Tensor &tensor(PyObject *o, const char *name) {
   const Tensor &t = THPVariable_Unpack(o);
   if (!t.is_cuda()) refuse(PyExc_ValueError, std::string(name) + " must be on a CUDA device");
   if (t.layout() != at::kStrided) refuse(PyExc_TypeError, std::string(name) + " must be a strided tensor");
+  // (A view that only notes a change of sign: its memory holds the other values.)
+  if (t.is_neg() || t.is_conj())
+    refuse(PyExc_ValueError, std::string(name) + " is a lazily negated view: resolve it first");
   return t;
 }
 const Tensor &tensor_of(PyObject *o, const char *name, ScalarType type, at::Device dev) {

@@ -339,3 +339,19 @@ def test_linear_gradients_where_dW_starts_off_alignment(ag):
     _ok(ag)
     assert torch.equal(dW, wdW) and torch.equal(db, wdb) and torch.equal(dx, wdx)
     assert float(flat[0]) == 7.0 and float(flat[-1]) == 7.0
+
+
+def test_lazily_negated_views_are_refused(ag):
+    """Their memory holds the values before the change of sign."""
+    q = _randn(_gen(1), 1, 4, 2, 8)
+    neg = torch._neg_view(q)
+    assert neg.is_neg() and torch.equal(neg, -q)
+    with pytest.raises(ValueError, match="negated"):
+        ag.ag_qk_norm_rope_fwd(neg, None)
+    with pytest.raises(ValueError, match="negated"):
+        ag.ag_grad_clip([neg], 1.0)
+    with pytest.raises(ValueError, match="negated"):
+        ag.ag_linear_fwd(torch._neg_view(q[0, 0].to(BF16)), q[0, 1].to(BF16))
+    out, _ = ag.ag_qk_norm_rope_fwd(neg.resolve_neg(), None, norm="none", out_dtype=F32)
+    _ok(ag)
+    assert torch.equal(out, -q.transpose(1, 2))
