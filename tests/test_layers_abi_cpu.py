@@ -261,8 +261,8 @@ SIDE_BY_SIDE = {
     "one sequence": dict(B=1, dq_sb=1024, dk_sb=9 * 128 * 7),
     "one of both": dict(B=1, L=1, dq_sb=1024, dq_sl=1024, dk_sb=128, dk_sl=128),
     # [B, L, H, 3, D]: each head's query, key and value together.
-    "interleaved heads": dict(Hk=8, dq_sb=7 * 3072, dq_sl=3072, dq_sh=384, dk_sb=7 * 3072,
-                              dk_sl=3072, dk_sh=384, dk=_p(5) + 256),
+    "interleaved heads": dict(Hq=4, Hk=4, dq_sb=7 * 1536, dq_sl=1536, dq_sh=384, dk_sb=7 * 1536,
+                              dk_sl=1536, dk_sh=384, dk=_p(5) + 256),
     # [B, 9, L, D]: the attention's own order, the keys behind the queries.
     "heads before positions": dict(dq_sb=9 * 7 * 128, dq_sl=128, dq_sh=7 * 128, dk_sb=9 * 7 * 128,
                                    dk_sl=128, dk_sh=7 * 128, dk=_p(5) + 8 * 7 * 256),
