@@ -377,9 +377,9 @@ typedef enum {
  * Products of dtype values are summed in float32; bias, activation and
  * residual are applied in float32 and y (and preact) rounded once; an
  * activation errs by a few 2^-24 (1 + |z|) of itself, the GELU and its
- * derivative by 1.2e-7 and, on the negative side, 5e-6 of itself.  The sums
- * are promoted out of the tensor core's accumulator every 512 terms, which
- * truncates rather than rounds (see linear_sm100.cu).
+ * derivative by 1.2e-7 and, on the negative side down to z = -8, 5e-6 of
+ * itself.  The sums are promoted out of the tensor core's accumulator, which
+ * truncates rather than rounds, every 512 terms (see linear_sm100.cu).
  * M >= 0 (M == 0 is a no-op), N, K >= 1 (AG_ERR_SHAPE), and a row stride not
  * below its row (AG_ERR_SHAPE); M <= 2^26, N, K <= 2^20, M N, M K and N K <=
  * 2^38, every stride of more than one row <= 2^28 (AG_ERR_UNSUPPORTED); an

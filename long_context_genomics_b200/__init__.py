@@ -133,6 +133,8 @@ class _NoLayers:
         self._why = why
 
     def __getattr__(self, name):
+        if name.startswith("__"):  # (what copying or inspecting a module looks for)
+            raise AttributeError(name)
         raise ImportError(f"{LAYERS_PATH} {self._why}: build it with "
                           "`python long_context_genomics_b200/build.py` "
                           "(or __graft_entry__.build())")
